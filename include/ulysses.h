@@ -65,10 +65,12 @@ enum {
   ULYSSES_ERR_CUDA = 3,
   ULYSSES_ERR_TIMEOUT = 4,
   ULYSSES_ERR_BAD_SEQLENS = 5,
-  ULYSSES_ERR_BOUNDS = 6
+  ULYSSES_ERR_BOUNDS = 6,
+  ULYSSES_ERR_BAD_PAGES = 7
 };
 
-enum { ULYSSES_BF16 = 0, ULYSSES_FP32 = 1 };
+/* E4M3 is a type of cached rows only (ulysses_cache_write and its readers). */
+enum { ULYSSES_BF16 = 0, ULYSSES_FP32 = 1, ULYSSES_E4M3 = 2 };
 
 /* Kernel selection for diagnostics: AUTO picks the tcgen05 kernels for BF16
  * with D = 128 and the fp32 SIMT kernels otherwise; SIMT forces the latter. */
@@ -310,6 +312,117 @@ int ulysses_attn_bwd_noalloc(const void* q_h, const void* k_h, const void* v_h, 
                              float scale, int dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions, between the QKV projection and attention (and on the
+ * gradients between attention's backward and the projection's).  Several
+ * tensors of the same tokens (Q and K) in one launch; each is addressed by
+ * strides, so sequence layout, head layout and slices of a fused projection's
+ * result need no copy.
+ *   y = R(a) x on the first rot_dim features of every head, the rest copied;
+ *   pair i (0 <= i < rot_dim / 2) is (x_i, x_{i + rot_dim/2}) with
+ *   ULYSSES_PAIRS_HALF and (x_{2i}, x_{2i+1}) with ULYSSES_PAIRS_ADJACENT, and
+ *   (y1, y2) = (x1 cos a - x2 sin a, x1 sin a + x2 cos a),
+ *   a = positions[axes[i]][b][s] * inv_freq[i].
+ * ulysses_rope_bwd is the adjoint (the rotation by -a): src holds dY, dst dX.
+ *   items      n_items <= 4 tensors, read on the host during the call: element
+ *              (b, s, h, d) is at src[b*src_b + s*src_s + h*src_h + d] (strides
+ *              in elements; src strides may be 0).  dst likewise; its elements
+ *              must be distinct.  In place (dst == src, equal strides, equal
+ *              types) is allowed; any other overlap is not.
+ *   positions  [n_axes][B][S] int32, device; any values.  1 <= n_axes <= 4.
+ *   inv_freq   [rot_dim / 2] double, HOST pointer, finite, read during the call.
+ *   axes       [rot_dim / 2] int32, HOST pointer: the axis each pair turns by
+ *              (NULL: axis 0).
+ *   dtype, out_dtype  of src and dst: equal, or FP32 -> BF16 (rounded once).
+ *   D in {64, 128}; rot_dim a multiple of 16, <= D; base pointers 16-byte
+ *   aligned and strides multiples of 16 bytes.
+ * Angles are formed as turns in 64-bit fixed point (pos * round(inv_freq /
+ * (2 pi) * 2^64) mod 2^64), so far positions lose nothing. */
+enum { ULYSSES_PAIRS_HALF = 0, ULYSSES_PAIRS_ADJACENT = 1 };
+typedef struct {
+  const void* src;
+  void* dst;
+  int H;
+  int64_t src_b, src_s, src_h;
+  int64_t dst_b, dst_s, dst_h;
+} ulysses_rope_item;
+int ulysses_rope_fwd(const ulysses_rope_item* items, int n_items, const int32_t* positions, int n_axes,
+                     const double* inv_freq, const int32_t* axes, int rot_dim, int pairs, int64_t S, int B,
+                     int D, int dtype, int out_dtype, void* stream);
+int ulysses_rope_bwd(const ulysses_rope_item* items, int n_items, const int32_t* positions, int n_axes,
+                     const double* inv_freq, const int32_t* axes, int rot_dim, int pairs, int64_t S, int B,
+                     int D, int dtype, int out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged key-value cache: rows of D values in pages of page_size tokens,
+ *   k_cache, v_cache  [num_pages][H_kv][page_size][D] in cache_dtype
+ *   k_scale, v_scale  [num_pages][H_kv][page_size] fp32 for ULYSSES_E4M3 (the
+ *                     row's value is code * scale), NULL otherwise
+ *   page_table        [B][table_cols] int32, device: token p of sequence b is
+ *                     row p % page_size of page page_table[b][p / page_size];
+ *                     entries past a sequence's last page are never read
+ * page_size is a multiple of 16, table_cols * page_size <= 2^30, D in {64,
+ * 128}; caches 16-byte aligned.
+ *
+ * ulysses_cache_write stores the K and V rows of new tokens.
+ *   k, v      element (t, h, d) at k[t*k_s + h*k_h + d] (strides in elements,
+ *             multiples of 16 bytes; bases 16-byte aligned), T tokens
+ *   cu_new    [B + 1] int32, device: sequence b's new tokens are rows
+ *             [cu_new[b], cu_new[b+1]); rows from cu_new[B] on are not read.
+ *             NULL: one token per sequence (T == B), and a sequence of length 0
+ *             is an empty place of the batch that writes nothing
+ *   seq_lens  [B] int32, device: the lengths WITH the new tokens, so the last
+ *             new token of sequence b goes to position seq_lens[b] - 1
+ *   cache_dtype == dtype stores the rows as they are; ULYSSES_E4M3 stores
+ *   scale = max(max|x|, 2^-100) / 448 and code = e4m3(x * (448 / max(...))),
+ *   round to nearest even; a row with an infinity or NaN gets scale NaN, so it
+ *   reads back as NaN.
+ *   The tokens of one call must have distinct places (a page owned by two
+ *   sequences must not be written through both in one call).
+ *
+ * ulysses_cache_read gathers rows back: token t of the packed outputs, in
+ *   sequence b (cu[b] <= t < cu[b+1]), is position first[b] + t - cu[b]
+ *   (first NULL: 0).  Rows from cu[B] on are left as they were.  dtype is the
+ *   cache's type, or BF16/FP32 for ULYSSES_E4M3 (code * scale, rounded once).
+ *
+ * A position outside the table, or a page id outside [0, num_pages), makes
+ * ulysses_check return ULYSSES_ERR_BAD_PAGES, and a cu that does not rise from
+ * 0 to at most T ULYSSES_ERR_BAD_SEQLENS; such tokens are skipped. */
+int ulysses_cache_write(const void* k, const void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h,
+                        int64_t T, int B, const int32_t* cu_new, const int32_t* page_table, int table_cols,
+                        const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                        int64_t num_pages, int page_size, int H_kv, int D, int dtype, int cache_dtype,
+                        void* stream);
+int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                       const int32_t* page_table, int table_cols, const int32_t* cu, const int32_t* first,
+                       void* k, void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h, int64_t T, int B,
+                       int64_t num_pages, int page_size, int H_kv, int D, int dtype, int cache_dtype,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token per sequence over the paged cache.
+ *   q    element (b, h, d) at q[b*q_b + h*q_h + d], H_q heads; head h reads kv
+ *        head h / G, G = H_q / H_kv
+ *   seq_lens [B] int32, device: the keys of sequence b are positions
+ *        [0, seq_lens[b]); length 0 gives O = 0 and LSE = -inf
+ *   o    written at o[b*o_b + h*o_h + d] in dtype;  lse [B][H_q] fp32 (or NULL)
+ *   dtype BF16 with a BF16 or E4M3 cache, FP32 with an FP32 or E4M3 cache
+ *   workspace  >= ulysses_attn_decode_workspace() bytes (0: may be NULL),
+ *        256-byte aligned, contents need no init; calls that share one must
+ *        not overlap on the GPU
+ * Slots past a sequence's length are never read.  A length below 0 or beyond
+ * the table, and a page id outside [0, num_pages), are reported by
+ * ulysses_check as ULYSSES_ERR_BAD_PAGES (the keys concerned are left out).
+ * Results do not depend on the order in which the GPU runs the call's blocks.
+ * B * H_q <= 2^24; strides and alignment as for ulysses_cache_write. */
+size_t ulysses_attn_decode_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
+                                     int cache_dtype);
+int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int32_t* page_table, int table_cols,
+                        const int32_t* seq_lens, void* o, int64_t o_b, int64_t o_h, float* lse, int B, int H_q,
+                        int H_kv, int D, int64_t num_pages, int page_size, float scale, int dtype,
+                        int cache_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Whole layer (steps 3-5, forward or backward) with the UPipe stage loop run
  * natively: for every rank r and chunk c, seq2head of the stage's Q/K/V
  * (and O/dO), attention, head2seq of the results.  Head-layout buffers of one
@@ -339,7 +452,8 @@ int ulysses_layer_bwd(const void* q_seq, const void* k_seq, const void* v_seq, c
  * ulysses_check: synchronises `stream`, then reads and clears the device
  *   error word that kernels set when a bounded wait expires (returns
  *   ULYSSES_ERR_TIMEOUT) or when cu_seqlens is malformed
- *   (ULYSSES_ERR_BAD_SEQLENS).  Returns ULYSSES_ERR_CUDA if the stream
+ *   (ULYSSES_ERR_BAD_SEQLENS) or a page table entry or length is out of range
+ *   (ULYSSES_ERR_BAD_PAGES).  Returns ULYSSES_ERR_CUDA if the stream
  *   reports a CUDA error.
  * ulysses_last_error: message of the last failure on this thread ("" if none).
  * ulysses_set_kernel: ULYSSES_KERNEL_AUTO or ULYSSES_KERNEL_SIMT (process wide).

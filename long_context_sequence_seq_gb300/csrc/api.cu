@@ -76,6 +76,9 @@ unsigned read_error_api(cudaStream_t st);
 unsigned read_error_attn_tc_fwd(cudaStream_t st);
 unsigned read_error_attn_tc_bwd(cudaStream_t st);
 unsigned read_error_proj_gemm(cudaStream_t st);
+unsigned read_error_rope(cudaStream_t st);
+unsigned read_error_kv_cache(cudaStream_t st);
+unsigned read_error_attn_decode(cudaStream_t st);
 ULYSSES_ERROR_READER(read_error_api)
 
 // cu_seqlens check: cu[0] == 0, cu[nd] == S, non-decreasing.
@@ -98,17 +101,13 @@ int launch_tc_bwd(const AttnArgs& a, cudaStream_t st);  // attn_tc_bwd.cu
 bool tc_fwd_supported(const AttnArgs& a);
 bool tc_bwd_supported(const AttnArgs& a);
 
+bool simt_chosen() { return g_kernel_choice.load() == ULYSSES_KERNEL_SIMT; }
+
 }  // namespace ulysses
 
 using namespace ulysses;
 
 namespace {
-
-int elt_size(int dtype) { return dtype == ULYSSES_BF16 ? 2 : (dtype == ULYSSES_FP32 ? 4 : 0); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Heads of a stage: n heads starting at h0.
 int stage_span(int H, int P, int C, int stage, int* n, int* h0) {
@@ -163,8 +162,6 @@ void job_ranges(bool to_head, const RelayoutJob& j, int64_t S, int B, int D, int
   *a = (const char*)j.src; *la = to_head ? seq_bytes : head_bytes;
   *b = (const char*)j.dst; *lb = to_head ? head_bytes : seq_bytes;
 }
-
-bool overlap(const char* a, size_t la, const char* b, size_t lb) { return a < b + lb && b < a + la; }
 
 // A batch of re-layouts of one launch: every item's destination must be
 // disjoint from every item's source (the launch has no order among them).
@@ -836,11 +833,14 @@ int ulysses_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
   unsigned w = read_error_api(st) | read_error_attn_tc_fwd(st) | read_error_attn_tc_bwd(st) |
-               read_error_proj_gemm(st);
+               read_error_proj_gemm(st) | read_error_rope(st) | read_error_kv_cache(st) |
+               read_error_attn_decode(st);
   e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "error-word read failed: %s", cudaGetErrorString(e));
   if (w & kErrTimeout) return set_error(ULYSSES_ERR_TIMEOUT, "a kernel gave up a bounded wait");
   if (w & kErrSeqlens) return set_error(ULYSSES_ERR_BAD_SEQLENS, "cu_seqlens must rise from 0 to S");
+  if (w & kErrPages)
+    return set_error(ULYSSES_ERR_BAD_PAGES, "a cached length, position or page id is outside the page table");
   if (w & kErrBounds) return set_error(ULYSSES_ERR_BOUNDS, "a kernel index fell outside its buffer (checked build)");
   return ULYSSES_OK;
 }

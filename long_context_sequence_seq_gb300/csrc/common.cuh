@@ -14,6 +14,7 @@ enum : unsigned {
   kErrTimeout = 1u,     // a bounded wait gave up
   kErrSeqlens = 2u,     // cu_seqlens not monotone from 0 to S
   kErrBounds = 4u,      // checked build: an index fell outside its buffer
+  kErrPages = 8u,       // a cached position or page id outside the page table's range
 };
 
 // One error word per translation unit (no relocatable device code is needed);

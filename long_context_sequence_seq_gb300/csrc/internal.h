@@ -2,11 +2,19 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "device_once.h"
+#include "ulysses.h"
 
 namespace ulysses {
+
+// Argument helpers of the C entry points.
+inline int elt_size(int dtype) { return dtype == ULYSSES_BF16 ? 2 : (dtype == ULYSSES_FP32 ? 4 : 0); }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool overlap(const char* a, size_t la, const char* b, size_t lb) { return a < b + lb && b < a + la; }
 
 // Arguments of one attention launch on head-layout buffers (batch folded into
 // the head index: buffer q head n in [0, n_q) reads kv head n / G).
@@ -71,5 +79,57 @@ int launch_qkv_proj(const void* x, const void* w, void* qkv_head, int64_t S, int
                     cudaStream_t st);                                                     // proj_gemm.cu
 int launch_out_proj(const void* o_head, const void* w, void* y, int64_t S, int H_q, int D, int hidden,
                     cudaStream_t st);                                                     // proj_gemm.cu
+
+
+// One tensor of a rotary launch (rope.cu), element strides; head0 is the first
+// of its heads in the launch's numbering, src_n / dst_n the elements spanned.
+constexpr int kMaxRopeItems = 4, kMaxRopeAxes = 4, kMaxRopePairs = 64;
+struct RopeJob {
+  const void* src; void* dst;
+  int H, head0;
+  int64_t src_b, src_s, src_h, dst_b, dst_s, dst_h;
+  int64_t src_n, dst_n;
+};
+struct RopeArgs {
+  RopeJob job[kMaxRopeItems];
+  int njobs, heads;            // tensors, heads of all of them
+  const int32_t* pos;          // [n_axes][N]
+  int64_t S, N;                // tokens per batch entry, tokens in all
+  int D, half, pairs, inverse;
+  int heads_fast;              // rows of one token lie closer than rows of one head
+  int dtype, out_dtype;
+  uint64_t freq[kMaxRopePairs];   // turns per position, in units of 2^-64
+  uint8_t axis[kMaxRopePairs];
+};
+int launch_rope(const RopeArgs& a, cudaStream_t st);
+
+// The paged cache and the tokens of one write or read (kv_cache.cu).
+struct CacheArgs {
+  void* kc; void* vc; float* ks; float* vs;       // caches and scales
+  void* k; void* v;                               // tokens' rows
+  int64_t k_s, k_h, v_s, v_h;
+  const int32_t* cu; const int32_t* lens;         // write: lens; read: first (in lens)
+  const int32_t* table;
+  int64_t T, num_pages;
+  int B, cols, page, H, D, dtype, cache_dtype;
+};
+int launch_cache_write(const CacheArgs& a, cudaStream_t st);
+int launch_cache_read(const CacheArgs& a, cudaStream_t st);
+
+// Attention of one new token per sequence over the paged cache (attn_decode.cu).
+struct DecodeArgs {
+  const void* q; int64_t q_b, q_h;
+  void* o; int64_t o_b, o_h;
+  float* lse;
+  const void* kc; const void* vc; const float* ks; const float* vs;
+  const int32_t* table; const int32_t* lens;
+  int64_t num_pages;
+  int B, H_q, H_kv, G, D, cols, page, dtype, cache_dtype;
+  float scale_log2;            // score scale * log2(e)
+  void* ws;
+};
+size_t decode_workspace(const DecodeArgs& a);
+int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st);
+bool simt_chosen();                                                       // api.cu
 
 }  // namespace ulysses

@@ -20,8 +20,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libulysses_checked.so" if os.environ.get("ULYSSES_CHECKED") == "1"
                         else "libulysses.so")
 
-OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS, ERR_BOUNDS = range(7)
-BF16, FP32 = 0, 1
+OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS, ERR_BOUNDS, ERR_BAD_PAGES = range(8)
+BF16, FP32, E4M3 = 0, 1, 2
+PAIRS_HALF, PAIRS_ADJACENT = 0, 1
 KERNEL_AUTO, KERNEL_SIMT = 0, 1
 
 _lib = None
@@ -31,6 +32,13 @@ class RelayoutItem(ctypes.Structure):
     """ulysses_relayout_item: one tensor of a batched re-layout launch."""
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("H", ctypes.c_int),
                 ("head_chunk", ctypes.c_int), ("stage", ctypes.c_int), ("add", ctypes.c_int)]
+
+
+class RopeItem(ctypes.Structure):
+    """ulysses_rope_item: one tensor of a rotary launch (element strides)."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("src_b", ctypes.c_int64), ("src_s", ctypes.c_int64), ("src_h", ctypes.c_int64),
+                ("dst_b", ctypes.c_int64), ("dst_s", ctypes.c_int64), ("dst_h", ctypes.c_int64)]
 
 
 class UlyssesError(RuntimeError):
@@ -88,6 +96,16 @@ def lib():
                                     i32, i32, f32, i32, vp, sz, vp]
     L.ulysses_layer_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32,
                                     i32, i32, vp, i32, i32, f32, i32, vp, sz, vp]
+    for fn in (L.ulysses_rope_fwd, L.ulysses_rope_bwd):
+        fn.argtypes = [ctypes.POINTER(RopeItem), i32, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32, i32, vp]
+    L.ulysses_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, i64, i32,
+                                      i32, i32, i32, i32, vp]
+    L.ulysses_cache_read.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i64, i32,
+                                     i32, i32, i32, i32, vp]
+    L.ulysses_attn_decode_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32]
+    L.ulysses_attn_decode_workspace.restype = sz
+    L.ulysses_attn_decode.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, i64, i64, vp, i32, i32, i32, i32,
+                                      i64, i32, f32, i32, i32, vp, sz, vp]
     L.ulysses_check.argtypes = [vp]
     L.ulysses_last_error.restype = ctypes.c_char_p
     L.ulysses_set_kernel.argtypes = [i32]
@@ -482,3 +500,310 @@ def layer_bwd_fused(q_seq, k_seq, v_seq, o_seq, do_seq, lse, P, head_chunk, cu_s
                                       int(bool(causal)), float(scale or 0.0), dt, _p(workspace),
                                       workspace.numel(), _stream(stream)))
     return dq, dk, dv
+
+
+# --------------------------------------------------------------- strided calls
+# The calls below take tensors by their strides: sequence layout, head layout
+# and slices of a fused projection's result alike ("seq": tokens, heads, D;
+# "head": heads, tokens, D; D contiguous).  They run on the device of their
+# tensors, whichever is current, on `stream` or that device's current stream;
+# outputs and workspaces made here belong to that stream.
+
+_CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float8_e4m3fn: E4M3}
+
+
+def _code(dtype, what):
+    c = _CODES.get(dtype)
+    if c is None:
+        raise TypeError(f"{what}: unsupported dtype {dtype}")
+    return c
+
+
+def _device_of(*tensors):
+    """The one CUDA device of the tensors (None entries left out)."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("expected a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return dev
+
+
+def _flat(t, dtype, what):
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, layout, what, dims=3):
+    """(token stride, head stride, tokens, heads) of a 3-D tensor of rows."""
+    if t.dim() != dims:
+        raise ValueError(f"{what} must have {dims} dimensions")
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if layout == "seq":
+        return t.stride(-3), t.stride(-2), t.shape[-3], t.shape[-2]
+    if layout == "head":
+        return t.stride(-2), t.stride(-3), t.shape[-2], t.shape[-3]
+    raise ValueError(f"unknown layout {layout!r}")
+
+
+def _launch(fn, dev, stream, tensors, *args):
+    """fn(*args, stream) on device dev.  A stream other than the device's
+    current one is recorded on the tensors, so that freeing one of them does
+    not hand its memory on while the call still runs."""
+    def go():
+        cur = torch.cuda.current_stream(dev)
+        if stream is None or stream == cur:
+            return fn(*args, cur.cuda_stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return fn(*args, stream.cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        _ck(go())
+    else:
+        with torch.cuda.device(dev):
+            _ck(go())
+
+
+def _empty(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+# --------------------------------------------------------------- rotary positions
+
+def rope_frequencies(rot_dim, base=10000.0, sections=None):
+    """Host tensors (inv_freq [rot_dim/2] float64, axes [rot_dim/2] int32) for
+    rope_fwd / rope_bwd: inv_freq[i] = base^(-2i/rot_dim).  sections gives, for
+    positions of several axes (time, height, width), how many of the pairs turn
+    by each axis, in order; None is one axis."""
+    half = rot_dim // 2
+    inv = torch.tensor([float(base) ** (-i / half) for i in range(half)], dtype=torch.float64)
+    sections = [half] if sections is None else list(sections)
+    if sum(sections) != half:
+        raise ValueError(f"sections {sections} must add up to rot_dim/2 = {half}")
+    return inv, torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.int32)
+
+
+def _rope(fn, q, k, positions, inv_freq, axes, layout, pairs, dtype, out, stream):
+    given = [t for t in (q, k) if t is not None]
+    if not given:
+        raise ValueError("rope: no tensor given")
+    if out is not None:
+        out = list(out) if isinstance(out, (tuple, list)) else [out]
+        if len(out) != len(given):
+            raise ValueError("rope: one output for each tensor")
+    dev = _device_of(*given, positions, *(out or ()))
+    first = given[0]
+    dt = first.dtype if dtype is None else dtype
+    D = first.shape[-1]
+    items = (RopeItem * len(given))()
+    results = []
+    S = B = None
+    for i, t in enumerate(given):
+        four = t.dim() == 4
+        ss, sh, n, H = _rows(t, layout, "rope input", 4 if four else 3)
+        nb, sb = (t.shape[0], t.stride(0)) if four else (1, 0)
+        if S is None:
+            S, B = n, nb
+        if (n, nb, t.shape[-1], t.dtype, t.dim()) != (S, B, D, first.dtype, first.dim()):
+            raise ValueError("rope: tensors of one call share their tokens, D and dtype")
+        o = _empty(t.shape, dt, dev, stream) if out is None else out[i]
+        if o.shape != t.shape or o.dtype != dt:
+            raise ValueError("rope: an output must have its input's shape and the call's dtype")
+        os_, oh, _, _ = _rows(o, layout, "rope output", 4 if four else 3)
+        items[i] = RopeItem(t.data_ptr(), o.data_ptr(), H, sb, ss, sh, o.stride(0) if four else 0, os_, oh)
+        results.append(o)
+    n_axes, rest = (1, tuple(positions.shape)) if positions.dim() == first.dim() - 2 else \
+        (positions.shape[0], tuple(positions.shape[1:]))
+    if rest != ((B, S) if first.dim() == 4 else (S,)):
+        raise ValueError(f"rope: positions {tuple(positions.shape)} do not match {B} x {S} tokens")
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 tensor in host memory")
+    if axes is not None and (axes.dtype != torch.int32 or axes.is_cuda or not axes.is_contiguous()
+                             or axes.numel() != inv_freq.numel()):
+        raise ValueError("axes must be a contiguous int32 tensor in host memory, one entry for each frequency")
+    if pairs not in ("half", "adjacent"):
+        raise ValueError(f"unknown pair order {pairs!r}")
+    _launch(fn, dev, stream, (*given, positions, *results), items, len(given),
+            _flat(positions, torch.int32, "positions"), n_axes, inv_freq.data_ptr(),
+            None if axes is None else axes.data_ptr(), 2 * inv_freq.numel(),
+            PAIRS_HALF if pairs == "half" else PAIRS_ADJACENT, S, B, D, _code(first.dtype, "rope"), _code(dt, "rope"))
+    return results[0] if len(given) == 1 else tuple(results)
+
+
+def rope_fwd(q, k, positions, inv_freq, axes=None, layout="seq", pairs="half", out=None, stream=None):
+    """Rotary positions on Q and K (either may be None), one launch.
+
+    q, k: [T, H, D] or [B, S, H, D] in sequence layout ("seq"), [H, T, D] or
+    [B, n, S, D] in head layout ("head"); bf16 or fp32, any strides with D
+    contiguous.  positions: int32 [T] ([B, S]), or [n_axes, ...] with axes
+    naming the axis of every pair; inv_freq, axes: host tensors
+    (rope_frequencies).  The first 2 * len(inv_freq) features of a head turn:
+    pairs (i, i + half) with "half", (2i, 2i+1) with "adjacent"; the others are
+    copied.  out: the outputs, q and k themselves for in place.  Returns the
+    rotated tensors, in the order given."""
+    return _rope(lib().ulysses_rope_fwd, q, k, positions, inv_freq, axes, layout, pairs, None, out, stream)
+
+
+def rope_bwd(dq, dk, positions, inv_freq, axes=None, layout="seq", pairs="half", dtype=None, out=None, stream=None):
+    """Adjoint of rope_fwd: gradients of the rotated Q and K (as layer_bwd
+    gives them, fp32 or bf16) to those of the projection's Q and K.  dtype: the
+    outputs' type (default: the gradients'; bf16 from fp32 rounds once)."""
+    return _rope(lib().ulysses_rope_bwd, dq, dk, positions, inv_freq, axes, layout, pairs, dtype, out, stream)
+
+
+# --------------------------------------------------------------- paged key-value cache
+
+def kv_cache(num_pages, page_size, H_kv, D, dtype=torch.bfloat16, device="cuda"):
+    """Buffers of a paged cache: (k_cache, v_cache [num_pages, H_kv, page_size,
+    D], k_scale, v_scale [num_pages, H_kv, page_size] fp32, or None unless
+    dtype is torch.float8_e4m3fn).  Zero-filled."""
+    shape = (num_pages, H_kv, page_size, D)
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return k, v, None, None
+    ks, vs = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Pointers of the cache's buffers, in the C calls' order, after the checks
+    that need the tensors."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [num_pages, H_kv, page_size, D] of one shape and dtype")
+    for t in (k_scale, v_scale):
+        if t is not None and t.shape != k_cache.shape[:3]:
+            raise ValueError("scales must be [num_pages, H_kv, page_size]")
+    dt = k_cache.dtype
+    return (_flat(k_cache, dt, "k_cache"), _flat(v_cache, dt, "v_cache"),
+            None if k_scale is None else _flat(k_scale, torch.float32, "k_scale"),
+            None if v_scale is None else _flat(v_scale, torch.float32, "v_scale"))
+
+
+def _batch_table(page_table, n, what):
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError(f"page_table must be [B, columns], B = {n} as {what}")
+    return _flat(page_table, torch.int32, "page_table"), page_table.shape[1]
+
+
+def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_scale=None, v_scale=None, layout="seq",
+                stream=None):
+    """Store the K and V rows of new tokens in the paged cache.
+
+    k, v: [T, H_kv, D] ("seq") or [H_kv, T, D] ("head"), any strides with D
+    contiguous.  page_table int32 [B, columns], seq_lens int32 [B]: the lengths
+    with the new tokens.  cu_new int32 [B + 1]: sequence b's new tokens are
+    rows [cu_new[b], cu_new[b+1]); None: one token per sequence, and a length
+    of 0 marks an empty place of the batch.  An e4m3 cache (with its scales) is
+    quantised row by row on the way.  Bad positions or pages raise in check()."""
+    ks, kh, T, H = _rows(k, layout, "k")
+    vs, vh, Tv, Hv = _rows(v, layout, "v")
+    if (T, H, k.shape[-1], k.dtype) != (Tv, Hv, v.shape[-1], v.dtype):
+        raise ValueError("k and v must have one shape and dtype")
+    if (H, k.shape[-1]) != (k_cache.shape[1], k_cache.shape[-1]):
+        raise ValueError("rows and cache differ in heads or D")
+    dev = _device_of(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new)
+    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
+    B = seq_lens.numel()
+    tab, cols = _batch_table(page_table, B, "seq_lens")
+    if cu_new is not None and cu_new.numel() != B + 1:
+        raise ValueError("cu_new must have B + 1 entries")
+    _launch(lib().ulysses_cache_write, dev, stream,
+            (k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new),
+            k.data_ptr(), v.data_ptr(), ks, kh, vs, vh, T, B,
+            None if cu_new is None else _flat(cu_new, torch.int32, "cu_new"), tab, cols,
+            _flat(seq_lens, torch.int32, "seq_lens"), pk, pv, pks, pvs, k_cache.shape[0], k_cache.shape[2], H,
+            k.shape[-1], _code(k.dtype, "k"), _code(k_cache.dtype, "k_cache"))
+
+
+def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=None, v_scale=None, dtype=None,
+               layout="seq", out=None, stream=None):
+    """Gather cached rows back: token t of the packed outputs, in sequence b
+    (cu_seqlens[b] <= t < cu_seqlens[b+1]), is position first[b] + t -
+    cu_seqlens[b] (first None: 0).  Returns (k, v) with T tokens, [T, H_kv, D]
+    or [H_kv, T, D]; rows from cu_seqlens[B] on are left as they were.  dtype:
+    the cache's, or bf16 (default) / fp32 from an e4m3 cache."""
+    dev = _device_of(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first, *(out or ()))
+    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
+    n_pages, H, page, D = k_cache.shape
+    if dtype is None:
+        dtype = out[0].dtype if out is not None else torch.bfloat16 if k_cache.dtype == torch.float8_e4m3fn else \
+            k_cache.dtype
+    B = cu_seqlens.numel() - 1
+    tab, cols = _batch_table(page_table, B, "cu_seqlens")
+    if first is not None and first.numel() != B:
+        raise ValueError("first must have B entries")
+    shape = (T, H, D) if layout == "seq" else (H, T, D)
+    k, v = out if out is not None else (_empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream))
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError(f"cache_read: outputs must be {shape} of {dtype}")
+    ks, kh, _, _ = _rows(k, layout, "k")
+    vs, vh, _, _ = _rows(v, layout, "v")
+    _launch(lib().ulysses_cache_read, dev, stream,
+            (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first),
+            pk, pv, pks, pvs, tab, cols, _flat(cu_seqlens, torch.int32, "cu_seqlens"),
+            None if first is None else _flat(first, torch.int32, "first"), k.data_ptr(), v.data_ptr(), ks, kh, vs, vh,
+            T, B, n_pages, page, H, D, _code(dtype, "k"), _code(k_cache.dtype, "k_cache"))
+    return k, v
+
+
+# --------------------------------------------------------------- single-token attention
+
+def attn_decode_workspace(q, k_cache, page_table, layout="seq"):
+    """Workspace for attn_decode on tensors of these shapes (uint8, on their
+    device; empty where the call needs none)."""
+    _, _, B, H_q = _rows(q, layout, "q")
+    n = lib().ulysses_attn_decode_workspace(B, H_q, k_cache.shape[1], q.shape[-1], page_table.shape[1],
+                                            k_cache.shape[2], _code(q.dtype, "q"), _code(k_cache.dtype, "k_cache"))
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale=None, scale=None, layout="seq",
+                workspace=None, out=None, lse=None, stream=None):
+    """Attention of one new token per sequence over the paged cache.
+
+    q: [B, H_q, D] ("seq") or [H_q, B, D] ("head", as qkv_proj gives it), any
+    strides with D contiguous; bf16 (bf16 or e4m3 cache) or fp32 (fp32 or e4m3
+    cache).  The keys of sequence b are its first seq_lens[b] (int32 [B])
+    cached positions; length 0 gives O = 0, LSE = -inf.  Returns (O shaped as
+    q, LSE [B, H_q] fp32).  workspace: attn_decode_workspace(), for calls that
+    do not overlap on the GPU; made per call if not given."""
+    qb, qh, B, H_q = _rows(q, layout, "q")
+    dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse)
+    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
+    n_pages, H_kv, page, D = k_cache.shape
+    if q.shape[-1] != D or seq_lens.numel() != B:
+        raise ValueError("attn_decode: q, cache and seq_lens differ in D or B")
+    tab, cols = _batch_table(page_table, B, "q")
+    L = lib()
+    dq, dc = _code(q.dtype, "q"), _code(k_cache.dtype, "k_cache")
+    if out is None:
+        out = _empty(q.shape, q.dtype, dev, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("attn_decode: out must have q's shape and dtype")
+    ob, oh, _, _ = _rows(out, layout, "out")
+    if lse is None:
+        lse = _empty((B, H_q), torch.float32, dev, stream)
+    elif tuple(lse.shape) != (B, H_q):
+        raise ValueError("attn_decode: lse must be [B, H_q]")
+    if workspace is None:
+        n = L.ulysses_attn_decode_workspace(B, H_q, H_kv, D, cols, page, dq, dc)
+        workspace = _empty((n,), torch.uint8, dev, stream) if n else None
+    ws, n = (None, 0) if workspace is None else (_flat(workspace, torch.uint8, "workspace"), workspace.numel())
+    _launch(L.ulysses_attn_decode, dev, stream,
+            (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse),
+            q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, torch.int32, "seq_lens"),
+            out.data_ptr(), ob, oh, _flat(lse, torch.float32, "lse"), B, H_q, H_kv, D, n_pages, page,
+            float(scale or 0.0), dq, dc, ws, n)
+    return out, lse
