@@ -7,10 +7,34 @@
 // s > m + 8 moves m and rescales the sums, otherwise m stays, which is exact
 // because o = acc / l and lse = m + log l hold for any m.
 //
-// SIMT kernel: one CTA per (sequence, kv head, up to HG of its query heads).
-// A warp walks tiles of 16 keys (always inside one page); 8 lanes hold a key's
-// row, so 4 keys are in work at a time, each group of 8 lanes with a running
-// softmax of its own; groups and warps are joined at the end.
+// Split.  An item is (sequence, kv head, group of its query heads); its keys
+// come in units of 16, which lie in one page.  The units of all items, one
+// after the other, are dealt to the launch's warps in equal contiguous ranges,
+// whatever the lengths: the warps read the lengths, no host knows them.  An
+// item inside one warp's range is finished there; the pieces of the others go
+// to the workspace, two slots a warp (the piece that its range begins in and
+// the one that it ends in), and the join kernel, launched behind with a
+// programmatic dependency so that its launch overlaps, adds each item's pieces
+// in the order of the warps.  No atomics, nothing to initialise.
+//
+// Two engines walk a piece.
+//   Matrix engine (bf16 queries): keys are the M = 16 side of mma m16n8k16 and
+//   the query heads of the group (up to 8 or 16) the N side.  At 4 heads a key
+//   costs 4 flops per cached byte, a tenth of what tcgen05 would need to be
+//   busy: the warp-level instruction leaves the pipe idle most of the time, and
+//   its register operands take rows straight from global memory, since the
+//   contraction may run over d in any order that Q shares: no shared memory,
+//   no barrier, no copy.  Rows stay in the lanes that loaded them:
+//     S = K Q^T   lane (g, j) holds rows g and g + 8, the 16-byte words j, j+4, ..
+//     O^T += V^T P^T   it holds rows 2j, 2j+1, 2j+8, 2j+9, words g, g+8, ..; pairs
+//                 of rows are interleaved by byte permutes, and P turns from
+//                 S's layout to the operand's by movmatrix
+//   E4m3 codes become f16 exactly.  q is scaled by a power of two into f16's
+//   range (exact, but for elements 2^-24 below its largest); the rows' scales
+//   enter in fp32: K's times the score, V's in the weight, as 2^(s + log2 vs - M)
+//   with a running maximum M of its own, so f16 weights keep 11 bits of the
+//   largest contribution whatever the rows' scales are.
+//   SIMT engine (fp32 queries, and by choice): fp32 throughout, 8 lanes a key.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -22,11 +46,23 @@ namespace {
 
 using namespace rows;
 
-constexpr int kTile = 16;                       // keys of a tile
+constexpr int kUnit = 16;                       // keys of a unit
 constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr float kLazy = 8.f;                    // a maximum moves when exceeded by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                       // of a CTA
+constexpr int kMaxBatch = 2048;                 // sequences of one launch (their prefix sums sit in shared memory)
+
+// How a launch is split (host), the same for both of its kernels.
+struct Plan {
+  int groups;       // query-head groups of a kv head
+  int heads;        // query heads of a group (the last may have fewer)
+  int warps;        // of the launch
+  int min_units;    // a warp takes at least this many units
+  int64_t* prefix;  // [B + 1] units before each sequence (one head); workspace
+  float2* ml;       // [2 * warps][heads] (m, l); workspace
+  float* o;         // [2 * warps][heads][D] sums; workspace
+};
 
 // Keys of sequence b: its length, cut to what the table can hold.
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
@@ -39,19 +75,422 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   return (int)n;
 }
 
-// Row index ([num_pages][H_kv][page] rows) of key `key` of sequence b, kv head
-// h; -1 (reported) for a page id out of range.  key is a multiple of kTile.
-__device__ __forceinline__ int64_t tile_row(const DecodeArgs& a, int b, int h, int key) {
-  const int col = key / a.page;
-  const int pg = __ldg(a.table + (int64_t)b * a.cols + col);
-  if (pg < 0 || pg >= a.num_pages) {
-    raise_error(kErrPages);
-    return -1;
-  }
-  return ((int64_t)pg * a.H_kv + h) * a.page + (key - col * a.page);
+// Warps that share `total` units, and the first unit of each.
+__device__ __forceinline__ int64_t active_warps(const Plan& p, int64_t total) {
+  const int64_t w = (total + p.min_units - 1) / p.min_units;
+  return w < p.warps ? w : p.warps;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t w, int64_t active, int64_t total) {
+  // w * total / active, without leaving 64 bits
+  const int64_t each = total / active, rest = total - each * active;
+  return w * each + (w < rest ? w : rest);
+}
+__device__ __forceinline__ int64_t warp_of(int64_t unit, int64_t active, int64_t total) {   // the w above
+  const int64_t each = total / active, rest = total - each * active;
+  return unit < rest * (each + 1) ? unit / (each + 1) : rest + (unit - rest * (each + 1)) / each;
 }
 
-// ------------------------------------------------------------------ SIMT tiles
+// The piece of an item that a warp walks.
+struct Piece {
+  int b, h, g0, gn;      // sequence, kv head, first query head of the group and how many
+  int unit0, units;      // units of the item
+  int len;               // the sequence's keys
+};
+
+// Walks the pages of a piece, a unit at a time.
+struct Walk {
+  const int32_t* row;    // the sequence's table row
+  int col, off, page, last_col;
+  int64_t base, head, num_pages;
+  __device__ __forceinline__ Walk(const DecodeArgs& a, const Piece& p) {
+    row = a.table + (int64_t)p.b * a.cols;
+    page = a.page;
+    const int key = p.unit0 * kUnit;
+    col = key / page;
+    off = key - col * page;
+    last_col = ((p.unit0 + p.units) * kUnit - 1) / page;
+    head = (int64_t)p.h * page;
+    base = (int64_t)a.H_kv * page;
+    num_pages = a.num_pages;
+  }
+  // page id of the next unit (issued ahead of its use)
+  __device__ __forceinline__ int fetch() const { return col <= last_col ? __ldg(row + col) : -1; }
+  // row index of that unit's first key, given its page id; steps to the unit after
+  __device__ __forceinline__ int64_t step(int pg) {
+    const bool bad = pg < 0 || pg >= num_pages;
+    if (bad && col <= last_col) raise_error(kErrPages);
+    const int64_t r = bad ? -1 : (int64_t)pg * base + head + off;
+    off += kUnit;
+    if (off == page) { off = 0; ++col; }
+    return r;
+  }
+};
+
+// ------------------------------------------------------------------ matrix engine
+
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, as exp2f, without its handling of tiny results
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <bool kQuant, int D, int NT>
+struct MatrixEngine {
+  using TQ = __nv_bfloat16;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kRowB = kQuant ? D : 2 * D;        // bytes of a row
+  static constexpr int kSub = 256 / kRowB;                // units of a step: 32 registers of K and of V
+  static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
+  static constexpr int kVB = kRowB / 8 < 16 ? 8 : 16;     // V: bytes of a word
+  static constexpr int kVW = kRowB / (8 * kVB);           //    words of a row per lane
+  static constexpr int kVE = kQuant ? kVB : kVB / 2;      //    elements of a word
+  static constexpr int kMT = D / 16;                      // M tiles of O^T
+
+  uint32_t q[NT][kKW * 4 * (kQuant ? 2 : 1)];
+  float acc[NT][kMT][4];
+  float m[NT][2], l[NT][2], mw[NT][2], sc[NT][2];
+  int lane, g, j;
+
+  __device__ __forceinline__ MatrixEngine(int lane_) : lane(lane_), g(lane_ >> 2), j(lane_ & 3) {}
+
+  __device__ __forceinline__ void begin(const DecodeArgs& a, const Piece& p) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int hl = t * 8 + g;
+      const bool live = hl < p.gn;
+      const TQ* qp = reinterpret_cast<const TQ*>(a.q) + (int64_t)p.b * a.q_b + (int64_t)(p.h * a.G + p.g0 + (live ? hl : 0)) * a.q_h;
+      constexpr int kE = kQuant ? 16 : 8;                  // elements of a K word
+      float big = 0.f;
+#pragma unroll
+      for (int w = 0; w < kKW; ++w) {
+#pragma unroll
+        for (int x = 0; x < kE / 8; ++x) {
+          const uint4 v = live ? ld16(qp + (w * 4 + j) * kE + x * 8) : make_uint4(0, 0, 0, 0);
+          uint32_t* d = &q[t][(w * (kE / 8) + x) * 4];
+          d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+        }
+      }
+      float f = a.scale_log2;
+      if (kQuant) {
+        constexpr int kN = sizeof(q[0]) / 4;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          float e[2];
+          bf16x2_to_f32(q[t][i], e);
+          big = fmaxf(big, fmaxf(fabsf(e[0]), fabsf(e[1])));
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // the power of two below the head's largest element
+        int e = (int)(__float_as_uint(big) >> 23) - 127;
+        e = e < -100 ? -100 : (e > 126 ? 126 : e);
+        const float down = __int_as_float((127 - e) << 23);
+        f *= __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          float x[2];
+          bf16x2_to_f32(q[t][i], x);
+          q[t][i] = f32_to_f16x2(x[0] * down, x[1] * down);
+        }
+      }
+      // from head g's lanes to those that hold the scores of heads 2j, 2j + 1
+      sc[t][0] = __shfl_sync(0xffffffffu, f, 8 * j);
+      sc[t][1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) { m[t][c] = kNoMax; l[t][c] = 0.f; mw[t][c] = kNoMax; }
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[t][i][c] = 0.f;
+    }
+  }
+
+  // rows of unit u of the step: keys [key, key + 16), the first at `row` (-1: none)
+  struct Rows { uint4 k[kSub][2][kKW]; uint32_t v[kSub][4][kVW * kVB / 4]; float ks[kSub][2], vs[kSub][2]; };
+
+  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int u, int64_t row, int keys) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bool ok = row >= 0 && g + 8 * x < keys;
+      const char* p = reinterpret_cast<const char*>(a.kc) + (row + g + 8 * x) * kRowB + j * 16;
+#pragma unroll
+      for (int w = 0; w < kKW; ++w) r.k[u][x][w] = ok ? ld16(p + w * 64) : make_uint4(0, 0, 0, 0);
+      if (kQuant) {
+        r.ks[u][x] = ok ? __ldg(a.ks + row + g + 8 * x) : 0.f;
+        r.vs[u][x] = ok ? __ldg(a.vs + row + g + 8 * x) : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int u, int64_t row, int keys) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int key = 2 * j + (x & 1) + (x >> 1) * 8;
+      const bool ok = row >= 0 && key < keys;
+      const char* p = reinterpret_cast<const char*>(a.vc) + (row + key) * kRowB + g * kVB;
+#pragma unroll
+      for (int w = 0; w < kVW; ++w) {
+        if (kVB == 16) {
+          const uint4 t = ok ? ld16(p + w * 128) : make_uint4(0, 0, 0, 0);
+          r.v[u][x][w * 4] = t.x; r.v[u][x][w * 4 + 1] = t.y; r.v[u][x][w * 4 + 2] = t.z; r.v[u][x][w * 4 + 3] = t.w;
+        } else {
+          const uint2 t = ok ? ld8(p) : make_uint2(0, 0);
+          r.v[u][x][0] = t.x; r.v[u][x][1] = t.y;
+        }
+      }
+    }
+  }
+
+  // two elements (x, x + 1 for e = 2x) of V's word registers as 16-bit pairs
+  __device__ __forceinline__ static uint32_t v_pair(const uint32_t* w, int e2) {   // elements 2 e2, 2 e2 + 1
+    if (!kQuant) return w[e2];
+    return e4m3x2_to_f16x2((uint16_t)(w[e2 >> 1] >> (16 * (e2 & 1))));
+  }
+
+  __device__ __forceinline__ void scores(const Rows& r, int u, float (&s)[NT][4]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[t][c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKW; ++w) {
+      const uint32_t lo[4] = {r.k[u][0][w].x, r.k[u][0][w].y, r.k[u][0][w].z, r.k[u][0][w].w};
+      const uint32_t hi[4] = {r.k[u][1][w].x, r.k[u][1][w].y, r.k[u][1][w].z, r.k[u][1][w].w};
+      if (!kQuant) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t f[4] = {lo[2 * x], hi[2 * x], lo[2 * x + 1], hi[2 * x + 1]};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_bf16(s[t], f, q[t][w * 4 + 2 * x], q[t][w * 4 + 2 * x + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t f[4] = {e4m3x2_to_f16x2((uint16_t)lo[x]), e4m3x2_to_f16x2((uint16_t)hi[x]),
+                                 e4m3x2_to_f16x2((uint16_t)(lo[x] >> 16)), e4m3x2_to_f16x2((uint16_t)(hi[x] >> 16))};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(s[t], f, q[t][w * 8 + 2 * x], q[t][w * 8 + 2 * x + 1]);
+        }
+      }
+    }
+  }
+
+  // the maximum of x over the lanes of a head (equal j)
+  __device__ __forceinline__ static float max_keys(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+  }
+
+  __device__ __forceinline__ void rescale(int t, int c, float f) {
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) { acc[t][i][c] *= f; acc[t][i][c + 2] *= f; }
+  }
+
+  // one step of kSub units; `more`: load the next one's rows as the registers come free
+  template <class Next>
+  __device__ __forceinline__ void step(const DecodeArgs& a, Rows& r, const int (&keys)[kSub], Next&& next) {
+    float s[kSub][NT][4], tw[kSub][NT][4];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) scores(r, u, s[u]);
+    float lvs[kSub][2], ks[kSub][2];
+    if (kQuant) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) { lvs[u][x] = __log2f(r.vs[u][x]); ks[u][x] = r.ks[u][x]; }
+    }
+    next.load_k(r);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float top = kNoMax, topw = kNoMax;
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float v = s[u][t][c + 2 * x] * (kQuant ? sc[t][c] * ks[u][x] : sc[t][c]);
+            v = g + 8 * x < keys[u] ? v : -INFINITY;
+            s[u][t][c + 2 * x] = v;
+            top = fmaxf(top, v);
+            if (kQuant) { tw[u][t][c + 2 * x] = v + lvs[u][x]; topw = fmaxf(topw, v + lvs[u][x]); }
+          }
+        if (__any_sync(0xffffffffu, top > m[t][c] + kLazy)) {
+          const float mm = fmaxf(m[t][c], max_keys(top)), f = exp2_fast(m[t][c] - mm);
+          m[t][c] = mm;
+          l[t][c] *= f;
+          if (!kQuant) rescale(t, c, f);
+        }
+        if (kQuant && __any_sync(0xffffffffu, topw > mw[t][c] + kLazy)) {
+          const float mm = fmaxf(mw[t][c], max_keys(topw)), f = exp2_fast(mw[t][c] - mm);
+          mw[t][c] = mm;
+          rescale(t, c, f);
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p = exp2_fast(s[u][t][c + 2 * x] - m[t][c]);
+            l[t][c] += p;
+            s[u][t][c + 2 * x] = kQuant ? exp2_fast(tw[u][t][c + 2 * x] - mw[t][c]) : p;
+          }
+      }
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          pb[t][x] = transpose8x8(kQuant ? f32_to_f16x2(s[u][t][2 * x], s[u][t][2 * x + 1])
+                                         : f32_to_bf16x2(s[u][t][2 * x], s[u][t][2 * x + 1]));
+#pragma unroll
+      for (int w = 0; w < kVW; ++w)
+#pragma unroll
+        for (int e = 0; e < kVE / 2; ++e) {
+          uint32_t v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = v_pair(&r.v[u][x][w * 4], e);
+          const uint32_t f[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                                 __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (kQuant) mma_f16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
+            else mma_bf16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
+          }
+        }
+    }
+    next.load_v(r);
+  }
+
+  struct Next {
+    MatrixEngine& e; const DecodeArgs& a; const int64_t (&row)[kSub]; const int (&keys)[kSub];
+    __device__ __forceinline__ void load_k(Rows& r) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) e.load_k(a, r, u, row[u], keys[u]);
+    }
+    __device__ __forceinline__ void load_v(Rows& r) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) e.load_v(a, r, u, row[u], keys[u]);
+    }
+  };
+
+  __device__ __forceinline__ void run(const DecodeArgs& a, const Piece& p) {
+    const int64_t total = a.num_pages * a.H_kv * a.page;
+    Walk walk(a, p);
+    Rows r;
+    int64_t row[kSub];
+    int keys[kSub], nkeys[kSub], pg[kSub];
+    int left = p.len - p.unit0 * kUnit;                    // keys from the step on, of this piece
+    if (left > p.units * kUnit) left = p.units * kUnit;
+    // page ids run one step ahead of the rows, the rows one step ahead of their use
+    auto places = [&](int keys_left, int (&n)[kSub]) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        pg[u] = walk.fetch();
+        row[u] = walk.step(pg[u]);
+        n[u] = row[u] >= 0 && in_bounds(row[u] + kUnit - 1, total) ? min(max(keys_left - u * kUnit, 0), kUnit) : 0;
+      }
+    };
+    places(left, keys);
+    Next now{*this, a, row, keys};
+    now.load_k(r);
+    now.load_v(r);
+    while (left > 0) {
+      left -= kSub * kUnit;
+      places(left, nkeys);
+      Next next{*this, a, row, nkeys};
+      step(a, r, keys, next);
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) keys[u] = nkeys[u];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 4);
+        l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 8);
+        l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 16);
+        if (kQuant) rescale(t, c, exp2f(mw[t][c] - m[t][c]));   // sums in units of 2^m again
+      }
+  }
+
+  // element 0 of word w of head (t, c): kVE consecutive values of this lane
+  __device__ __forceinline__ void values(int t, int c, int w, float* f) const {
+#pragma unroll
+    for (int e = 0; e < kVE / 2; ++e) {
+      f[2 * e] = acc[t][w * (kVE / 2) + e][c];
+      f[2 * e + 1] = acc[t][w * (kVE / 2) + e][c + 2];
+    }
+  }
+  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
+    (void)heads;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int hl = t * 8 + 2 * j + c;
+        if (hl >= gn) continue;
+        if (g == 0) ml[hl] = make_float2(m[t][c], l[t][c]);
+#pragma unroll
+        for (int w = 0; w < kVW; ++w) {
+          float f[kVE];
+          values(t, c, w, f);
+          float* d = o + hl * D + (w * 8 + g) * kVE;
+#pragma unroll
+          for (int e = 0; e < kVE; e += 4) *reinterpret_cast<float4*>(d + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+      }
+  }
+  __device__ __forceinline__ void result(const DecodeArgs& a, const Piece& p) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int hl = t * 8 + 2 * j + c;
+        if (hl >= p.gn) continue;
+        const int hq = p.h * a.G + p.g0 + hl;
+        const float inv = 1.f / l[t][c];
+        if (g == 0 && a.lse) a.lse[(int64_t)p.b * a.H_q + hq] = (m[t][c] + log2f(l[t][c])) * kLn2;
+        TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)p.b * a.o_b + (int64_t)hq * a.o_h;
+#pragma unroll
+        for (int w = 0; w < kVW; ++w) {
+          float f[kVE];
+          values(t, c, w, f);
+#pragma unroll
+          for (int e = 0; e < kVE; ++e) f[e] *= inv;
+#pragma unroll
+          for (int e = 0; e < kVE; e += 8) {
+            Row8<TQ> y;
+            y.set(f + e);
+            y.store(d + (w * 8 + g) * kVE + e);
+          }
+        }
+      }
+  }
+};
+
+// ------------------------------------------------------------------ SIMT engine
 
 // One lane's part of a row: 8 lanes hold D values, lane i the 16-byte words
 // i, i + 8, ...  (for 8-bit rows of 64 values: 8-byte words).
@@ -119,148 +558,364 @@ template <int D> struct LaneRow<uint8_t, D> {
   __device__ static __forceinline__ int element(int e, int i) { return i * (D / 8) + e; }
 };
 
-template <typename TQ, typename TC, int D, int HG>
-__global__ void __launch_bounds__(kWarps * 32) decode_simt_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr bool kQuant = sizeof(TC) == 1;
-  constexpr int E = D / 8;                      // elements of a row per lane
-  const int groups = (a.G + HG - 1) / HG;
-  const int gi = blockIdx.x % groups, h = (blockIdx.x / groups) % a.H_kv, b = blockIdx.x / groups / a.H_kv;
-  const int g0 = gi * HG, gn = a.G - g0 < HG ? a.G - g0 : HG;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = lane & 7, grp = lane >> 3;
-  const int len = length_of(a, b);
-  const int64_t total = a.num_pages * a.H_kv * a.page;
 
+template <typename TQ_, typename TC, int D, int HG>
+struct SimtEngine {
+  using TQ = TQ_;
+  static constexpr bool kQuant = sizeof(TC) == 1;
+  static constexpr int kHeads = HG;
+  static constexpr int E = D / 8;               // elements of a row per lane
   float q[HG][E], acc[HG][E], m[HG], l[HG];
-#pragma unroll
-  for (int g = 0; g < HG; ++g) {
-    m[g] = kNoMax;
-    l[g] = 0.f;
-    const int hq = h * a.G + g0 + (g < gn ? g : 0);
-    const TQ* qp = reinterpret_cast<const TQ*>(a.q) + (int64_t)b * a.q_b + (int64_t)hq * a.q_h;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[g][e] = to_f32<TQ>(qp[LaneRow<TC, D>::element(e, i)]) * a.scale_log2;
-      acc[g][e] = 0.f;
-    }
-  }
-  for (int key0 = warp * kTile; key0 < len; key0 += kWarps * kTile) {
-    const int64_t row0 = tile_row(a, b, h, key0);
-    if (row0 < 0 || !in_bounds(row0 + kTile - 1, total)) continue;
-#pragma unroll 2
-    for (int k = grp; k < kTile; k += 4) {
-      const bool live = key0 + k < len;
-      const int64_t row = row0 + k;
-      LaneRow<TC, D> kr, vr;
-      kr.zero();
-      vr.zero();
-      float ks = 1.f, vs = 1.f;
-      if (live) {
-        kr.load(reinterpret_cast<const TC*>(a.kc) + row * D, i);
-        vr.load(reinterpret_cast<const TC*>(a.vc) + row * D, i);
-        if (kQuant) { ks = __ldg(a.ks + row); vs = __ldg(a.vs + row); }
-      }
-      float f[E], s[HG];
-      kr.get(f);
-#pragma unroll
-      for (int g = 0; g < HG; ++g) {
-        s[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s[g] = fmaf(q[g][e], f[e], s[g]);
-      }
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1)
-#pragma unroll
-        for (int g = 0; g < HG; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
-      vr.get(f);
-#pragma unroll
-      for (int g = 0; g < HG; ++g) {
-        float t = kQuant ? s[g] * ks : s[g];
-        t = live ? t : -INFINITY;
-        if (t > m[g] + kLazy) {
-          const float w = exp2f(m[g] - t);
-          m[g] = t;
-          l[g] *= w;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[g][e] *= w;
-        }
-        const float p = exp2f(t - m[g]);
-        l[g] += p;
-        const float pv = kQuant ? p * vs : p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[g][e] = fmaf(pv, f[e], acc[g][e]);
-      }
-    }
-  }
-  // join the four groups of the warp
-#pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {
+  int lane, i, grp;
+
+  __device__ __forceinline__ SimtEngine(int lane_) : lane(lane_), i(lane_ & 7), grp(lane_ >> 3) {}
+
+  __device__ __forceinline__ void begin(const DecodeArgs& a, const Piece& p) {
 #pragma unroll
     for (int g = 0; g < HG; ++g) {
-      const float mo = __shfl_xor_sync(0xffffffffu, m[g], o), lo = __shfl_xor_sync(0xffffffffu, l[g], o);
-      const float mm = fmaxf(m[g], mo), wa = exp2f(m[g] - mm), wb = exp2f(mo - mm);
-      m[g] = mm;
-      l[g] = l[g] * wa + lo * wb;
+      m[g] = kNoMax;
+      l[g] = 0.f;
+      const TQ* qp = reinterpret_cast<const TQ*>(a.q) + (int64_t)p.b * a.q_b +
+                     (int64_t)(p.h * a.G + p.g0 + (g < p.gn ? g : 0)) * a.q_h;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float x = __shfl_xor_sync(0xffffffffu, acc[g][e], o);
-        acc[g][e] = acc[g][e] * wa + x * wb;
+        q[g][e] = to_f32<TQ>(qp[LaneRow<TC, D>::element(e, i)]) * a.scale_log2;
+        acc[g][e] = 0.f;
       }
     }
   }
-  // join the warps
-  __shared__ float so[kWarps][HG][D], sm[kWarps][HG], sl[kWarps][HG];
-  if (grp == 0) {
+  __device__ __forceinline__ void run(const DecodeArgs& a, const Piece& p) {
+    const int64_t total = a.num_pages * a.H_kv * a.page;
+    Walk walk(a, p);
+    for (int u = 0; u < p.units; ++u) {
+      const int64_t row0 = walk.step(walk.fetch());
+      if (row0 < 0 || !in_bounds(row0 + kUnit - 1, total)) continue;
+      const int left = p.len - (p.unit0 + u) * kUnit;
+#pragma unroll 2
+      for (int k = grp; k < kUnit; k += 4) {
+        const bool live = k < left;
+        const int64_t row = row0 + k;
+        LaneRow<TC, D> kr, vr;
+        kr.zero();
+        vr.zero();
+        float ks = 1.f, vs = 1.f;
+        if (live) {
+          kr.load(reinterpret_cast<const TC*>(a.kc) + row * D, i);
+          vr.load(reinterpret_cast<const TC*>(a.vc) + row * D, i);
+          if (kQuant) { ks = __ldg(a.ks + row); vs = __ldg(a.vs + row); }
+        }
+        float f[E], s[HG];
+        kr.get(f);
 #pragma unroll
-    for (int g = 0; g < HG; ++g) {
-      if (i == 0) { sm[warp][g] = m[g]; sl[warp][g] = l[g]; }
+        for (int g = 0; g < HG; ++g) {
+          s[g] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) so[warp][g][LaneRow<TC, D>::element(e, i)] = acc[g][e];
+          for (int e = 0; e < E; ++e) s[g] = fmaf(q[g][e], f[e], s[g]);
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+          for (int g = 0; g < HG; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
+        vr.get(f);
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+          float t = kQuant ? s[g] * ks : s[g];
+          t = live ? t : -INFINITY;
+          if (t > m[g] + kLazy) {
+            const float w = exp2f(m[g] - t);
+            m[g] = t;
+            l[g] *= w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[g][e] *= w;
+          }
+          const float x = exp2f(t - m[g]);
+          l[g] += x;
+          const float pv = kQuant ? x * vs : x;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[g][e] = fmaf(pv, f[e], acc[g][e]);
+        }
+      }
+    }
+    // join the four groups of the warp
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+#pragma unroll
+      for (int g = 0; g < HG; ++g) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m[g], o), lo = __shfl_xor_sync(0xffffffffu, l[g], o);
+        const float mm = fmaxf(m[g], mo), wa = exp2f(m[g] - mm), wb = exp2f(mo - mm);
+        m[g] = mm;
+        l[g] = l[g] * wa + lo * wb;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float x = __shfl_xor_sync(0xffffffffu, acc[g][e], o);
+          acc[g][e] = acc[g][e] * wa + x * wb;
+        }
+      }
     }
   }
-  __syncthreads();
-  for (int x = threadIdx.x; x < gn * D; x += kWarps * 32) {
-    const int g = x / D, d = x - g * D;
-    float mm = kNoMax, ll = 0.f, o = 0.f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[w][g]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(sm[w][g] - mm);
-      ll += sl[w][g] * f;
-      o += so[w][g][d] * f;
+  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
+    (void)heads;
+    if (grp != 0) return;
+#pragma unroll
+    for (int g = 0; g < HG; ++g) {
+      if (g >= gn) break;
+      if (i == 0) ml[g] = make_float2(m[g], l[g]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[g * D + LaneRow<TC, D>::element(e, i)] = acc[g][e];
     }
-    const int hq = h * a.G + g0 + g;
-    reinterpret_cast<TQ*>(a.o)[(int64_t)b * a.o_b + (int64_t)hq * a.o_h + d] = from_f32<TQ>(len == 0 ? 0.f : o / ll);
-    if (d == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = len == 0 ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  }
+  __device__ __forceinline__ void result(const DecodeArgs& a, const Piece& p) const {
+    if (grp != 0) return;
+#pragma unroll
+    for (int g = 0; g < HG; ++g) {
+      if (g >= p.gn) break;
+      const int hq = p.h * a.G + p.g0 + g;
+      if (i == 0 && a.lse) a.lse[(int64_t)p.b * a.H_q + hq] = (m[g] + log2f(l[g])) * kLn2;
+      TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)p.b * a.o_b + (int64_t)hq * a.o_h;
+#pragma unroll
+      for (int e = 0; e < E; ++e) d[LaneRow<TC, D>::element(e, i)] = from_f32<TQ>(acc[g][e] / l[g]);
+    }
+  }
+};
+
+// ------------------------------------------------------------------ the two kernels
+
+template <class Engine, int D, int kCtas>
+__global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid_constant__ DecodeArgs a,
+                                                                    const __grid_constant__ Plan p) {
+  // prefix[b]: units of the sequences before b (of one head)
+  extern __shared__ int64_t prefix[];
+  __shared__ int64_t sums[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t carry = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+    const int b = b0 + threadIdx.x;
+    const int64_t mine = b < a.B ? (length_of(a, b) + kUnit - 1) / kUnit : 0;
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int64_t before = carry;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sums[w];
+      carry += sums[w];
+    }
+    if (b < a.B) prefix[b + 1] = before + x;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) prefix[0] = 0;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= a.B; b += kWarps * 32) p.prefix[b] = prefix[b];
+  // the join may be launched: it waits for the whole of this grid
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int per = a.H_kv * p.groups;                       // items of a sequence
+  const int64_t total = carry * per;
+  if (total == 0) return;
+  const int64_t active = active_warps(p, total), w = (int64_t)blockIdx.x * kWarps + warp;
+  if (w >= active) return;
+  const int64_t begin = first_unit(w, active, total), end = first_unit(w + 1, active, total);
+  int b = 0;
+  {
+    int lo = 0, hi = a.B - 1;                              // the last b with prefix[b] * per <= begin
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] * per <= begin) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+  }
+  Engine e(lane);
+  int64_t at = begin;
+  while (at < end) {
+    while (prefix[b + 1] * per <= at) ++b;
+    const int64_t units = prefix[b + 1] - prefix[b], in_seq = at - prefix[b] * per;
+    const int item = (int)(in_seq / units);
+    const int64_t item0 = prefix[b] * per + item * units;  // the item's first unit
+    Piece pc;
+    pc.b = b;
+    pc.h = item / p.groups;
+    pc.g0 = (item - pc.h * p.groups) * p.heads;
+    pc.gn = min(a.G - pc.g0, p.heads);
+    pc.unit0 = (int)(at - item0);
+    pc.units = (int)(min(end, item0 + units) - at);
+    pc.len = length_of(a, b);
+    e.begin(a, pc);
+    e.run(a, pc);
+    if (pc.units == units) {
+      e.result(a, pc);
+    } else {
+      const int64_t slot = 2 * w + (at == begin ? 0 : 1);
+      e.partial(p.ml + slot * p.heads, p.o + slot * p.heads * D, p.heads, pc.gn);
+    }
+    at += pc.units;
   }
 }
 
-template <typename TQ, typename TC, int D, int HG>
-int run_simt(const DecodeArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.H_kv * ((a.G + HG - 1) / HG));
-  decode_simt_kernel<TQ, TC, D, HG><<<grid, kWarps * 32, 0, st>>>(a);
-  count_launch();
-  return check_launch("attn_decode");
+// One CTA per query head of a sequence: adds the pieces of its item, or writes
+// the result of a sequence without keys.
+template <typename TQ, int D>
+__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeArgs a,
+                                                          const __grid_constant__ Plan p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kLanes = D / 4, kParts = 256 / kLanes;     // threads of a piece's row, pieces at a time
+  __shared__ float4 so[kParts][kLanes];
+  __shared__ float sl[kParts];
+  const int hq = blockIdx.x % a.H_q, b = blockIdx.x / a.H_q;
+  const int h = hq / a.G, gi = (hq - h * a.G) / p.heads, hl = hq - h * a.G - gi * p.heads;
+  const int part = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)b * a.o_b + (int64_t)hq * a.o_h;
+  float* lse = a.lse ? a.lse + (int64_t)b * a.H_q + hq : nullptr;
+  const int64_t before = p.prefix[b], units = p.prefix[b + 1] - before;
+  if (units == 0) {
+    for (int x = threadIdx.x; x < D; x += 256) d[x] = from_f32<TQ>(0.f);
+    if (threadIdx.x == 0 && lse) *lse = -INFINITY;
+    return;
+  }
+  const int per = a.H_kv * p.groups;
+  const int64_t total = p.prefix[a.B] * per, active = active_warps(p, total);
+  const int64_t first = before * per + (h * p.groups + gi) * units;
+  const int64_t w0 = warp_of(first, active, total), w1 = warp_of(first + units - 1, active, total);
+  if (w0 == w1) return;                                    // finished where it was walked
+  // the piece of warp w: in its first slot unless the item begins inside w's range
+  const int64_t skip = first_unit(w0, active, total) == first ? 0 : 1;
+  auto slot = [&](int64_t w) { return 2 * w + (w == w0 ? skip : 0); };
+  float m = kNoMax;
+  for (int64_t w = w0 + (threadIdx.x & 31); w <= w1; w += 32) m = fmaxf(m, p.ml[slot(w) * p.heads + hl].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int64_t w = w0 + part; w <= w1; w += kParts) {
+    const int64_t at = slot(w) * p.heads + hl;
+    const float2 ml = p.ml[at];
+    const float4 x = *reinterpret_cast<const float4*>(p.o + at * D + c * 4);
+    const float f = exp2f(ml.x - m);
+    l += ml.y * f;
+    s.x += x.x * f; s.y += x.y * f; s.z += x.z * f; s.w += x.w * f;
+  }
+  so[part][c] = s;
+  if (c == 0) sl[part] = l;
+  __syncthreads();
+  if (part != 0) return;
+  for (int k = 1; k < kParts; ++k) {
+    const float4 x = so[k][c];
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    l += sl[k];
+  }
+  d[c * 4] = from_f32<TQ>(s.x / l);
+  d[c * 4 + 1] = from_f32<TQ>(s.y / l);
+  d[c * 4 + 2] = from_f32<TQ>(s.z / l);
+  d[c * 4 + 3] = from_f32<TQ>(s.w / l);
+  if (c == 0 && lse) *lse = (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int kMaxWarps = 152 * 16;              // of a launch: slots of the workspace
+
+bool is_matrix(const DecodeArgs& a, bool simt) { return a.dtype == ULYSSES_BF16 && !simt; }
+
+// query heads of a group
+int heads_of(const DecodeArgs& a, bool simt) {
+  if (is_matrix(a, simt)) return a.G <= 8 ? a.G : (a.G <= 16 ? a.G : 16);
+  return a.G < 4 ? (a.G < 2 ? 1 : 2) : 4;
+}
+
+struct WsLayout { size_t prefix, ml, o, total; };
+WsLayout ws_layout(const DecodeArgs& a, int heads) {
+  WsLayout w{};
+  const int b = a.B < kMaxBatch ? a.B : kMaxBatch;
+  w.prefix = 0;
+  w.ml = align256((size_t)(b + 1) * 8);
+  w.o = w.ml + align256((size_t)2 * kMaxWarps * heads * 8);
+  w.total = w.o + align256((size_t)2 * kMaxWarps * heads * a.D * 4);
+  return w;
+}
+
+template <class Engine, int D, int kCtas>
+int run(const DecodeArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int ctas = sms * kCtas;
+  if (ctas * kWarps > kMaxWarps) ctas = kMaxWarps / kWarps;
+  Plan p{};
+  p.heads = a.G < Engine::kHeads ? a.G : Engine::kHeads;
+  p.groups = (a.G + p.heads - 1) / p.heads;
+  p.warps = ctas * kWarps;
+  p.min_units = 2;
+  const WsLayout w = ws_layout(a, p.heads);
+  char* ws = (char*)a.ws;
+  p.prefix = (int64_t*)(ws + w.prefix);
+  p.ml = (float2*)(ws + w.ml);
+  p.o = (float*)(ws + w.o);
+  for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
+    DecodeArgs x = a;
+    x.B = a.B - b0 < kMaxBatch ? a.B - b0 : kMaxBatch;
+    x.q = (const char*)a.q + (int64_t)b0 * a.q_b * sizeof(typename Engine::TQ);
+    x.o = (char*)a.o + (int64_t)b0 * a.o_b * sizeof(typename Engine::TQ);
+    x.lse = a.lse ? a.lse + (int64_t)b0 * a.H_q : nullptr;
+    x.table = a.table + (int64_t)b0 * a.cols;
+    x.lens = a.lens + b0;
+    decode_kernel<Engine, D, kCtas><<<ctas, kWarps * 32, (x.B + 1) * sizeof(int64_t), st>>>(x, p);
+    count_launch();
+    int rc = check_launch("attn_decode");
+    if (rc) return rc;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(x.B * a.H_q));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_join_kernel<typename Engine::TQ, D>, x, p);
+    if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode join: launch failed: %s", cudaGetErrorString(err));
+    count_launch();
+  }
+  return ULYSSES_OK;
+}
+
+template <bool kQuant, int D>
+int run_matrix(const DecodeArgs& a, cudaStream_t st) {
+  if (a.G <= 8) return run<MatrixEngine<kQuant, D, 1>, D, 3>(a, st);
+  return run<MatrixEngine<kQuant, D, 2>, D, 2>(a, st);
 }
 template <typename TQ, typename TC, int D>
-int run_simt_g(const DecodeArgs& a, cudaStream_t st) {
-  if (a.G == 1) return run_simt<TQ, TC, D, 1>(a, st);
-  if (a.G == 2) return run_simt<TQ, TC, D, 2>(a, st);
-  return run_simt<TQ, TC, D, 4>(a, st);
-}
-template <typename TQ, typename TC>
-int run_simt_d(const DecodeArgs& a, cudaStream_t st) {
-  return a.D == 128 ? run_simt_g<TQ, TC, 128>(a, st) : run_simt_g<TQ, TC, 64>(a, st);
+int run_simt(const DecodeArgs& a, cudaStream_t st) {
+  if (a.G == 1) return run<SimtEngine<TQ, TC, D, 1>, D, 4>(a, st);
+  if (a.G <= 3) return run<SimtEngine<TQ, TC, D, 2>, D, 3>(a, st);
+  return run<SimtEngine<TQ, TC, D, 4>, D, 2>(a, st);
 }
 
 }  // namespace
 
-size_t decode_workspace(const DecodeArgs&) { return 0; }
+size_t decode_workspace(const DecodeArgs& a) {
+  if (a.B == 0) return 0;
+  // both engines', whichever the process has chosen when the call is made
+  const size_t x = ws_layout(a, heads_of(a, false)).total, y = ws_layout(a, heads_of(a, true)).total;
+  return x > y ? x : y;
+}
 
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st) {
-  (void)simt;
-  const bool quant = a.cache_dtype == ULYSSES_E4M3;
-  if (a.dtype == ULYSSES_BF16)
-    return quant ? run_simt_d<__nv_bfloat16, uint8_t>(a, st) : run_simt_d<__nv_bfloat16, __nv_bfloat16>(a, st);
-  return quant ? run_simt_d<float, uint8_t>(a, st) : run_simt_d<float, float>(a, st);
+  const bool quant = a.cache_dtype == ULYSSES_E4M3, wide = a.D == 128;
+  if (is_matrix(a, simt)) {
+    if (quant) return wide ? run_matrix<true, 128>(a, st) : run_matrix<true, 64>(a, st);
+    return wide ? run_matrix<false, 128>(a, st) : run_matrix<false, 64>(a, st);
+  }
+  if (a.dtype == ULYSSES_BF16) {
+    if (quant) return wide ? run_simt<__nv_bfloat16, uint8_t, 128>(a, st) : run_simt<__nv_bfloat16, uint8_t, 64>(a, st);
+    return wide ? run_simt<__nv_bfloat16, __nv_bfloat16, 128>(a, st) : run_simt<__nv_bfloat16, __nv_bfloat16, 64>(a, st);
+  }
+  if (quant) return wide ? run_simt<float, uint8_t, 128>(a, st) : run_simt<float, uint8_t, 64>(a, st);
+  return wide ? run_simt<float, float, 128>(a, st) : run_simt<float, float, 64>(a, st);
 }
 
 }  // namespace ulysses
