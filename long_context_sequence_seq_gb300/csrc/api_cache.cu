@@ -178,12 +178,12 @@ int check_cache(int64_t num_pages, int page, int H_kv, int D, int B, int cols, i
   if (D != 64 && D != 128) return set_error(ULYSSES_ERR_UNSUPPORTED, "head dim %d not in {64,128}", D);
   if (page <= 0 || page % 16 || page > (1 << 20))
     return set_error(ULYSSES_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 16 up to 2^20", page);
-  if (num_pages < 0 || num_pages > kMaxTokens || H_kv <= 0 || H_kv > (1 << 20) || B < 0 || cols < 0)
+  if (num_pages < 0 || num_pages > kMaxTokens || H_kv <= 0 || H_kv > 4096 || B < 0 || cols < 0)
     return set_error(ULYSSES_ERR_INVALID, "bad sizes num_pages=%lld H_kv=%d B=%d table_cols=%d", (long long)num_pages, H_kv, B, cols);
   if ((int64_t)cols * page > kMaxPositions)
     return set_error(ULYSSES_ERR_UNSUPPORTED, "table_cols * page_size = %lld above 2^30 positions", (long long)cols * page);
-  if ((num_pages && (double)num_pages * H_kv * page * D * 4 > 4.6e18))
-    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache too large");
+  if ((double)num_pages * H_kv * (page / 16) > 2147483647.0)
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache of more than 2^31 blocks of 16 rows");
   if ((cache_dtype == ULYSSES_E4M3) != (ks != nullptr) || (cache_dtype == ULYSSES_E4M3) != (vs != nullptr))
     return set_error(ULYSSES_ERR_INVALID, "scales go with an E4M3 cache, and only with one");
   if (num_pages && (!kc || !vc)) return set_error(ULYSSES_ERR_INVALID, "NULL cache");

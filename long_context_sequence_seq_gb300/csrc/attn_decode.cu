@@ -37,6 +37,7 @@
 //   SIMT engine (fp32 queries, and by choice): fp32 throughout, 8 lanes a key.
 #include "internal.h"
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace ulysses {
 
@@ -97,32 +98,33 @@ struct Piece {
   int len;               // the sequence's keys
 };
 
-// Walks the pages of a piece, a unit at a time.
+// Walks the pages of a piece, a unit at a time.  Units of the cache are
+// numbered ([num_pages][H_kv][page / 16]); the host keeps that below 2^31.
 struct Walk {
   const int32_t* row;    // the sequence's table row
-  int col, off, page, last_col;
-  int64_t base, head, num_pages;
+  int col, off, per, last_col, head, base, num_pages;
   __device__ __forceinline__ Walk(const DecodeArgs& a, const Piece& p) {
     row = a.table + (int64_t)p.b * a.cols;
-    page = a.page;
-    const int key = p.unit0 * kUnit;
-    col = key / page;
-    off = key - col * page;
-    last_col = ((p.unit0 + p.units) * kUnit - 1) / page;
-    head = (int64_t)p.h * page;
-    base = (int64_t)a.H_kv * page;
-    num_pages = a.num_pages;
+    per = a.page / kUnit;
+    col = p.unit0 / per;
+    off = p.unit0 - col * per;
+    last_col = (p.unit0 + p.units - 1) / per;
+    head = p.h * per;
+    base = a.H_kv * per;
+    num_pages = (int)a.num_pages;
   }
-  // page id of the next unit (issued ahead of its use)
-  __device__ __forceinline__ int fetch() const { return col <= last_col ? __ldg(row + col) : -1; }
-  // row index of that unit's first key, given its page id; steps to the unit after
-  __device__ __forceinline__ int64_t step(int pg) {
-    const bool bad = pg < 0 || pg >= num_pages;
-    if (bad && col <= last_col) raise_error(kErrPages);
-    const int64_t r = bad ? -1 : (int64_t)pg * base + head + off;
-    off += kUnit;
-    if (off == page) { off = 0; ++col; }
-    return r;
+  // page id of the current unit (0 behind the piece: its units are not loaded)
+  __device__ __forceinline__ int fetch() const { return col <= last_col ? __ldg(row + col) : 0; }
+  // number of the current unit, given its page id; -1 (reported) where that is out of range
+  __device__ __forceinline__ int unit(int pg) const {
+    if ((unsigned)pg >= (unsigned)num_pages) {
+      if (col <= last_col) raise_error(kErrPages);
+      return -1;
+    }
+    return pg * base + head + off;
+  }
+  __device__ __forceinline__ void next() {
+    if (++off == per) { off = 0; ++col; }
   }
 };
 
@@ -225,40 +227,66 @@ struct MatrixEngine {
     }
   }
 
-  // rows of unit u of the step: keys [key, key + 16), the first at `row` (-1: none)
+  // rows of the units of a step; `unit` is its number in the cache, `keys` how
+  // many of its 16 the piece has (0: none)
   struct Rows { uint4 k[kSub][2][kKW]; uint32_t v[kSub][4][kVW * kVB / 4]; float ks[kSub][2], vs[kSub][2]; };
 
-  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int u, int64_t row, int keys) {
+  template <bool kAll>
+  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int u, int unit, int keys) {
+    const char* p = reinterpret_cast<const char*>(a.kc) + ((int64_t)unit * kUnit + g) * kRowB + j * 16;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const bool ok = row >= 0 && g + 8 * x < keys;
-      const char* p = reinterpret_cast<const char*>(a.kc) + (row + g + 8 * x) * kRowB + j * 16;
+      const bool ok = kAll || g + 8 * x < keys;
 #pragma unroll
-      for (int w = 0; w < kKW; ++w) r.k[u][x][w] = ok ? ld16(p + w * 64) : make_uint4(0, 0, 0, 0);
-      if (kQuant) {
-        r.ks[u][x] = ok ? __ldg(a.ks + row + g + 8 * x) : 0.f;
-        r.vs[u][x] = ok ? __ldg(a.vs + row + g + 8 * x) : 0.f;
+      for (int w = 0; w < kKW; ++w) r.k[u][x][w] = ok ? ld16(p + x * 8 * kRowB + w * 64) : make_uint4(0, 0, 0, 0);
+    }
+    if (kQuant) {
+      const int64_t s = (int64_t)unit * kUnit + g;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool ok = kAll || g + 8 * x < keys;
+        r.ks[u][x] = ok ? __ldg(a.ks + s + 8 * x) : 0.f;
+        r.vs[u][x] = ok ? __ldg(a.vs + s + 8 * x) : 0.f;
       }
     }
   }
-  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int u, int64_t row, int keys) {
+  template <bool kAll>
+  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int u, int unit, int keys) {
+    const char* p = reinterpret_cast<const char*>(a.vc) + ((int64_t)unit * kUnit + 2 * j) * kRowB + g * kVB;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int key = 2 * j + (x & 1) + (x >> 1) * 8;
-      const bool ok = row >= 0 && key < keys;
-      const char* p = reinterpret_cast<const char*>(a.vc) + (row + key) * kRowB + g * kVB;
+      const int key = (x & 1) + (x >> 1) * 8;              // from 2 j on
+      const bool ok = kAll || 2 * j + key < keys;
 #pragma unroll
       for (int w = 0; w < kVW; ++w) {
         if (kVB == 16) {
-          const uint4 t = ok ? ld16(p + w * 128) : make_uint4(0, 0, 0, 0);
+          const uint4 t = ok ? ld16(p + key * kRowB + w * 128) : make_uint4(0, 0, 0, 0);
           r.v[u][x][w * 4] = t.x; r.v[u][x][w * 4 + 1] = t.y; r.v[u][x][w * 4 + 2] = t.z; r.v[u][x][w * 4 + 3] = t.w;
         } else {
-          const uint2 t = ok ? ld8(p) : make_uint2(0, 0);
+          const uint2 t = ok ? ld8(p + key * kRowB) : make_uint2(0, 0);
           r.v[u][x][0] = t.x; r.v[u][x][1] = t.y;
         }
       }
     }
   }
+  // whole units take the path without predicates (warp-uniform)
+  struct Next {
+    MatrixEngine& e; const DecodeArgs& a; const int (&unit)[kSub]; const int (&keys)[kSub];
+    __device__ __forceinline__ void load_k(Rows& r) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        if (keys[u] == kUnit) e.template load_k<true>(a, r, u, unit[u], kUnit);
+        else e.template load_k<false>(a, r, u, unit[u], keys[u]);
+      }
+    }
+    __device__ __forceinline__ void load_v(Rows& r) {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        if (keys[u] == kUnit) e.template load_v<true>(a, r, u, unit[u], kUnit);
+        else e.template load_v<false>(a, r, u, unit[u], keys[u]);
+      }
+    }
+  };
 
   // two elements (x, x + 1 for e = 2x) of V's word registers as 16-bit pairs
   __device__ __forceinline__ static uint32_t v_pair(const uint32_t* w, int e2) {   // elements 2 e2, 2 e2 + 1
@@ -383,43 +411,42 @@ struct MatrixEngine {
     next.load_v(r);
   }
 
-  struct Next {
-    MatrixEngine& e; const DecodeArgs& a; const int64_t (&row)[kSub]; const int (&keys)[kSub];
-    __device__ __forceinline__ void load_k(Rows& r) {
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) e.load_k(a, r, u, row[u], keys[u]);
-    }
-    __device__ __forceinline__ void load_v(Rows& r) {
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) e.load_v(a, r, u, row[u], keys[u]);
-    }
-  };
-
   __device__ __forceinline__ void run(const DecodeArgs& a, const Piece& p) {
     const int64_t total = a.num_pages * a.H_kv * a.page;
     Walk walk(a, p);
     Rows r;
-    int64_t row[kSub];
-    int keys[kSub], nkeys[kSub], pg[kSub];
-    int left = p.len - p.unit0 * kUnit;                    // keys from the step on, of this piece
-    if (left > p.units * kUnit) left = p.units * kUnit;
-    // page ids run one step ahead of the rows, the rows one step ahead of their use
+    int unit[kSub], keys[kSub], nkeys[kSub], pg[kSub];
+    int left = min(p.len - p.unit0 * kUnit, p.units * kUnit);   // keys of the piece from the step on
+    // page ids are read a step ahead of the rows, rows a step ahead of their use
     auto places = [&](int keys_left, int (&n)[kSub]) {
+      Walk w = walk;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        pg[u] = walk.fetch();
-        row[u] = walk.step(pg[u]);
-        n[u] = row[u] >= 0 && in_bounds(row[u] + kUnit - 1, total) ? min(max(keys_left - u * kUnit, 0), kUnit) : 0;
+        unit[u] = w.unit(pg[u]);
+        n[u] = unit[u] >= 0 && in_bounds((int64_t)unit[u] * kUnit + kUnit - 1, total)
+                   ? min(max(keys_left - u * kUnit, 0), kUnit) : 0;
+        w.next();
+      }
+      walk = w;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        pg[u] = w.fetch();
+        w.next();
       }
     };
+    {
+      Walk w = walk;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) { pg[u] = w.fetch(); w.next(); }
+    }
     places(left, keys);
-    Next now{*this, a, row, keys};
+    Next now{*this, a, unit, keys};
     now.load_k(r);
     now.load_v(r);
     while (left > 0) {
       left -= kSub * kUnit;
       places(left, nkeys);
-      Next next{*this, a, row, nkeys};
+      Next next{*this, a, unit, nkeys};
       step(a, r, keys, next);
 #pragma unroll
       for (int u = 0; u < kSub; ++u) keys[u] = nkeys[u];
@@ -588,8 +615,10 @@ struct SimtEngine {
     const int64_t total = a.num_pages * a.H_kv * a.page;
     Walk walk(a, p);
     for (int u = 0; u < p.units; ++u) {
-      const int64_t row0 = walk.step(walk.fetch());
-      if (row0 < 0 || !in_bounds(row0 + kUnit - 1, total)) continue;
+      const int n = walk.unit(walk.fetch());
+      const int64_t row0 = (int64_t)n * kUnit;
+      walk.next();
+      if (n < 0 || !in_bounds(row0 + kUnit - 1, total)) continue;
       const int left = p.len - (p.unit0 + u) * kUnit;
 #pragma unroll 2
       for (int k = grp; k < kUnit; k += 4) {
@@ -680,6 +709,22 @@ struct SimtEngine {
 
 // ------------------------------------------------------------------ the two kernels
 
+// Shared memory of CTA `rank` of the cluster, at this CTA's address `at`.
+__device__ __forceinline__ float2 cluster_ld2(uint32_t at, int rank) {
+  uint32_t p;
+  float2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
+  uint32_t p;
+  float4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
+  return v;
+}
+
 template <class Engine, int D, int kCtas>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid_constant__ DecodeArgs a,
                                                                     const __grid_constant__ Plan p) {
@@ -756,6 +801,67 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
   }
 }
 
+// Short caches: a cluster per item.  Its warps take equal ranges of the item's
+// units and leave their sums in shared memory; each CTA joins a part of the
+// item's outputs from the shared memories of all.  One launch, no workspace.
+template <class Engine, int D, int kCtas>
+__global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(const __grid_constant__ DecodeArgs a,
+                                                                            int groups, int heads, int ctas) {
+  constexpr int kH = Engine::kHeads;
+  __shared__ __align__(16) float so[kWarps][kH][D];
+  __shared__ __align__(8) float2 sml[kWarps][kH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tc::cluster_ctarank(), item = blockIdx.x / ctas;
+  Piece pc;
+  const int hg = item % (a.H_kv * groups);
+  pc.b = item / (a.H_kv * groups);
+  pc.h = hg / groups;
+  pc.g0 = (hg - pc.h * groups) * heads;
+  pc.gn = min(a.G - pc.g0, heads);
+  pc.len = length_of(a, pc.b);
+  const int units = (pc.len + kUnit - 1) / kUnit, warps = ctas * kWarps, w = rank * kWarps + warp;
+  pc.unit0 = (int)first_unit(w, warps, units);
+  pc.units = (int)first_unit(w + 1, warps, units) - pc.unit0;
+  Engine e(lane);
+  e.begin(a, pc);
+  if (pc.units > 0) e.run(a, pc);
+  e.partial(sml[warp], &so[warp][0][0], kH, pc.gn);
+  __syncwarp();
+  tc::cluster_sync();
+  const int total = pc.gn * D / 4, each = (total + ctas - 1) / ctas;
+  const uint32_t o_at = tc::smem_u32(&so[0][0][0]), ml_at = tc::smem_u32(&sml[0][0]);
+  for (int i = rank * each + threadIdx.x; i < min(total, (rank + 1) * each); i += kWarps * 32) {
+    const int hl = i / (D / 4), c = i - hl * (D / 4);
+    float m = kNoMax, l = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < ctas; ++r) {
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) m = fmaxf(m, cluster_ld2(ml_at + (k * kH + hl) * 8, r).x);
+    }
+    for (int r = 0; r < ctas; ++r) {
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 ml = cluster_ld2(ml_at + (k * kH + hl) * 8, r);
+        const float4 x = cluster_ld4(o_at + ((k * kH + hl) * D + c * 4) * 4, r);
+        const float f = exp2f(ml.x - m);
+        l += ml.y * f;
+        s.x += x.x * f; s.y += x.y * f; s.z += x.z * f; s.w += x.w * f;
+      }
+    }
+    using TQ = typename Engine::TQ;
+    const int hq = pc.h * a.G + pc.g0 + hl;
+    TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)pc.b * a.o_b + (int64_t)hq * a.o_h + c * 4;
+    const bool none = pc.len == 0;
+    d[0] = from_f32<TQ>(none ? 0.f : s.x / l);
+    d[1] = from_f32<TQ>(none ? 0.f : s.y / l);
+    d[2] = from_f32<TQ>(none ? 0.f : s.z / l);
+    d[3] = from_f32<TQ>(none ? 0.f : s.w / l);
+    if (c == 0 && a.lse) a.lse[(int64_t)pc.b * a.H_q + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+  __syncwarp();
+  tc::cluster_sync();                                      // no CTA leaves while another reads its sums
+}
+
 // One CTA per query head of a sequence: adds the pieces of its item, or writes
 // the result of a sequence without keys.
 template <typename TQ, int D>
@@ -827,6 +933,20 @@ int heads_of(const DecodeArgs& a, bool simt) {
   return a.G < 4 ? (a.G < 2 ? 1 : 2) : 4;
 }
 
+// CTAs of a cluster for each item, or 0: split the keys over the whole launch.
+// A cluster pays while its warps stay short of units: at most kClusterUnits
+// each when the table is full, and all clusters resident at once.
+constexpr int kClusterUnits = 4;
+int cluster_of(const DecodeArgs& a, int heads) {
+  const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
+  const int64_t units = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit;
+  int c = 8;
+  while (c > 1 && items * c > 152 * 2) c /= 2;
+  if (items * c > 152 * 2 || units > (int64_t)c * kWarps * kClusterUnits) return 0;
+  while (c > 1 && units <= (int64_t)(c / 2) * kWarps) c /= 2;   // no more warps than units
+  return c;
+}
+
 struct WsLayout { size_t prefix, ml, o, total; };
 WsLayout ws_layout(const DecodeArgs& a, int heads) {
   WsLayout w{};
@@ -850,6 +970,22 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   p.groups = (a.G + p.heads - 1) / p.heads;
   p.warps = ctas * kWarps;
   p.min_units = 2;
+  if (const int c = cluster_of(a, p.heads)) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<Engine, D, kCtas>, a, p.groups, p.heads, c);
+    if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode: launch failed: %s", cudaGetErrorString(err));
+    count_launch();
+    return ULYSSES_OK;
+  }
   const WsLayout w = ws_layout(a, p.heads);
   char* ws = (char*)a.ws;
   p.prefix = (int64_t*)(ws + w.prefix);
@@ -900,8 +1036,13 @@ int run_simt(const DecodeArgs& a, cudaStream_t st) {
 size_t decode_workspace(const DecodeArgs& a) {
   if (a.B == 0) return 0;
   // both engines', whichever the process has chosen when the call is made
-  const size_t x = ws_layout(a, heads_of(a, false)).total, y = ws_layout(a, heads_of(a, true)).total;
-  return x > y ? x : y;
+  size_t most = 0;
+  for (const bool simt : {false, true}) {
+    const int heads = heads_of(a, simt);
+    const size_t n = cluster_of(a, heads) ? 0 : ws_layout(a, heads).total;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st) {

@@ -11,9 +11,9 @@
 //
 // Bound by HBM: rows are read and written once.  A CTA takes a block of tokens
 // with all their heads, K and V: it resolves each token's place once (sequence
-// by bisection in cu, page from the table) and streams the rows; D / 8 lanes
-// hold a row, 8 elements each, so the row's largest magnitude is a 3- or
-// 4-step shuffle.
+// by bisection in cu, page from the table) and streams the rows; D / 16 lanes
+// hold a row, 16 elements each, so the row's largest magnitude is a 2- or
+// 3-step shuffle.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -67,24 +67,13 @@ __device__ __forceinline__ void check_cu(const CacheArgs& a) {
   }
 }
 
-__device__ __forceinline__ float max_nan(float x, float y) {   // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-  return r;
-}
-
-// Row r of the CTA's tokens x heads x {K, V}: which token, head and tensor.
-// Rows that lie together in memory are neighbours: heads of one token when the
-// tokens' tensor has them closer, else tokens of one head.
-struct RowIndex { int t, h, v; };
-__device__ __forceinline__ RowIndex row_index(int r, int tokens, int heads, bool heads_fast) {
-  const int per = tokens * heads;
-  RowIndex x;
-  x.v = r >= per;
-  r -= x.v ? per : 0;
-  if (heads_fast) { x.t = r / heads; x.h = r - x.t * heads; } else { x.h = r / tokens; x.t = r - x.h * tokens; }
-  return x;
-}
+// The rows of a CTA's tokens x heads, K's and then V's, in an order in which
+// rows that lie together in the tokens' tensor are neighbours: heads of one
+// token where those are closer, else tokens of one head.
+// Rows that a lane has in work at once: 64 bytes of loads or more in flight.
+// A lane holds 16 elements of a row, the 8-element words lane and lane + D / 16.
+template <typename T, bool kQuant, bool kWrite>
+constexpr int rows_in_work() { return kWrite ? (sizeof(T) == 2 ? 4 : 2) : (kQuant ? 4 : (sizeof(T) == 2 ? 2 : 1)); }
 
 template <typename T, bool kQuant>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, int tb) {
@@ -94,41 +83,67 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   check_cu(a);
   if ((int)threadIdx.x < tokens) place[threadIdx.x] = place_of(a, t0 + threadIdx.x, true);
   __syncthreads();
-  const int lanes = a.D / 8, lane = threadIdx.x % lanes;
+  constexpr int kRows = rows_in_work<T, kQuant, true>();
+  const int lanes = a.D / 16, lane = threadIdx.x % lanes, e0 = lane * 8, e1 = (lane + lanes) * 8;
   const bool heads_fast = a.k_h <= a.k_s;
-  const int rows = 2 * tokens * a.H, step = kThreads / lanes;
+  const int ni = heads_fast ? a.H : tokens, no = heads_fast ? tokens : a.H;
+  RowWalk walk(threadIdx.x / lanes, kThreads / lanes, ni);
   // every lane of a warp runs the same number of rounds: the row maximum is a shuffle
-  for (int r0 = 0; r0 < rows; r0 += step) {
-    const int r = r0 + threadIdx.x / lanes;
-    const RowIndex x = row_index(r < rows ? r : 0, tokens, a.H, heads_fast);
-    const int64_t at = place[x.t];
-    const bool live = r < rows && at >= 0;
-    const int64_t row = at + (int64_t)x.h * a.page;
-    Row8<T> w;
-    w.set((const float[8]){0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f});
-    if (live)
-      w.load(reinterpret_cast<const T*>(x.v ? a.v : a.k) + (t0 + x.t) * (x.v ? a.v_s : a.k_s) +
-             x.h * (x.v ? a.v_h : a.k_h) + lane * 8);
-    const bool ok = live && in_bounds(row, a.num_pages * a.H * a.page);
-    if (!kQuant) {
-      if (ok) w.store(reinterpret_cast<T*>(x.v ? a.vc : a.kc) + row * a.D + lane * 8);
-    } else {
-      float f[8];
-      w.get(f);
-      float amax = fabsf(f[0]);
+  for (int left = 2 * no * ni; left > 0; left -= kRows * (kThreads / lanes)) {
+    Row8<T> w[kRows][2];
+    int64_t row[kRows];
+    bool second[kRows];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) amax = max_nan(amax, fabsf(f[i]));
-      for (int o = lanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      amax = max_nan(amax, 7.888609052210118e-31f);   // 2^-100
-      const float inv = 448.0f / amax;
-      const float scale = amax <= 3.4028234663852886e38f ? amax / 448.0f : __int_as_float(0x7fc00000);
-      uint2 codes;
-      codes.x = f32_to_e4m3x2(f[0] * inv, f[1] * inv) | (uint32_t)f32_to_e4m3x2(f[2] * inv, f[3] * inv) << 16;
-      codes.y = f32_to_e4m3x2(f[4] * inv, f[5] * inv) | (uint32_t)f32_to_e4m3x2(f[6] * inv, f[7] * inv) << 16;
-      if (ok) {
-        st8(reinterpret_cast<uint8_t*>(x.v ? a.vc : a.kc) + row * a.D + lane * 8, codes);
-        if (lane == 0) (x.v ? a.vs : a.ks)[row] = scale;
+    for (int u = 0; u < kRows; ++u) {
+      row[u] = -1;
+      w[u][0].zero();
+      w[u][1].zero();
+      second[u] = walk.o >= no;
+      if (walk.o < 2 * no) {
+        const int o = second[u] ? walk.o - no : walk.o;
+        const int t = heads_fast ? o : walk.i, h = heads_fast ? walk.i : o;
+        const int64_t at = place[t];
+        if (at >= 0 && in_bounds(at + (int64_t)h * a.page, a.num_pages * a.H * a.page)) {
+          row[u] = at + (int64_t)h * a.page;
+          const int64_t off = second[u] ? (t0 + t) * a.v_s + h * a.v_h : (t0 + t) * a.k_s + h * a.k_h;
+          const T* src = reinterpret_cast<const T*>(second[u] ? a.v : a.k) + off;
+          w[u][0].load(src + e0);
+          w[u][1].load(src + e1);
+        }
       }
+      walk.next();
+    }
+    if (!kQuant) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (row[u] < 0) continue;
+        T* dst = reinterpret_cast<T*>(second[u] ? a.vc : a.kc) + row[u] * a.D;
+        w[u][0].store(dst + e0);
+        w[u][1].store(dst + e1);
+      }
+      continue;
+    }
+    // the rows' largest magnitudes; lane u of a row's lanes keeps row u's
+    float mine = 0.f;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      float amax = max_nan(w[u][0].amax(), w[u][1].amax());
+      for (int o = lanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      mine = lane % kRows == u ? amax : mine;
+    }
+    // so one pair of divisions serves kRows rows
+    mine = max_nan(mine, 7.888609052210118e-31f);   // 2^-100
+    const float inv = 448.0f / mine;
+    const float scale = mine <= 3.4028234663852886e38f ? mine / 448.0f : __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const float by = __shfl_sync(0xffffffffu, inv, u, lanes);
+      const uint2 c0 = w[u][0].codes(by), c1 = w[u][1].codes(by);
+      if (row[u] < 0) continue;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(second[u] ? a.vc : a.kc) + row[u] * a.D;
+      st8(dst + e0, c0);
+      st8(dst + e1, c1);
+      if (lane == u) (second[u] ? a.vs : a.ks)[row[u]] = scale;
     }
   }
 }
@@ -141,29 +156,57 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   check_cu(a);
   if ((int)threadIdx.x < tokens) place[threadIdx.x] = place_of(a, t0 + threadIdx.x, false);
   __syncthreads();
-  const int lanes = a.D / 8, lane = threadIdx.x % lanes;
+  constexpr int kRows = rows_in_work<T, kQuant, false>();
+  const int lanes = a.D / 16, lane = threadIdx.x % lanes, e0 = lane * 8, e1 = (lane + lanes) * 8;
   const bool heads_fast = a.k_h <= a.k_s;
-  for (int r = threadIdx.x / lanes; r < 2 * tokens * a.H; r += kThreads / lanes) {
-    const RowIndex x = row_index(r, tokens, a.H, heads_fast);
-    const int64_t at = place[x.t];
-    if (at < 0) continue;
-    const int64_t row = at + (int64_t)x.h * a.page;
-    if (!in_bounds(row, a.num_pages * a.H * a.page)) continue;
-    T* dst = reinterpret_cast<T*>(x.v ? a.v : a.k) + (t0 + x.t) * (x.v ? a.v_s : a.k_s) + x.h * (x.v ? a.v_h : a.k_h) + lane * 8;
-    Row8<T> w;
-    if (!kQuant) {
-      w.load(reinterpret_cast<const T*>(x.v ? a.vc : a.kc) + row * a.D + lane * 8);
-    } else {
-      const uint2 codes = ld8(reinterpret_cast<const uint8_t*>(x.v ? a.vc : a.kc) + row * a.D + lane * 8);
-      const float scale = (x.v ? a.vs : a.ks)[row];
-      float f[8];
-      e4m3x4_to_f32(codes.x, f);
-      e4m3x4_to_f32(codes.y, f + 4);
+  const int ni = heads_fast ? a.H : tokens, no = heads_fast ? tokens : a.H;
+  RowWalk walk(threadIdx.x / lanes, kThreads / lanes, ni);
+  while (walk.o < 2 * no) {
+    Row8<T> w[kRows][2];
+    uint2 codes[kRows][2];
+    float scale[kRows];
+    T* dst[kRows];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= scale;
-      w.set(f);
+    for (int u = 0; u < kRows; ++u) {
+      dst[u] = nullptr;
+      if (walk.o < 2 * no) {
+        const bool second = walk.o >= no;
+        const int o = second ? walk.o - no : walk.o;
+        const int t = heads_fast ? o : walk.i, h = heads_fast ? walk.i : o;
+        const int64_t at = place[t], row = at + (int64_t)h * a.page;
+        if (at >= 0 && in_bounds(row, a.num_pages * a.H * a.page)) {
+          const int64_t off = second ? (t0 + t) * a.v_s + h * a.v_h : (t0 + t) * a.k_s + h * a.k_h;
+          dst[u] = reinterpret_cast<T*>(second ? a.v : a.k) + off;
+          if (kQuant) {
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(second ? a.vc : a.kc) + row * a.D;
+            codes[u][0] = ld8(src + e0);
+            codes[u][1] = ld8(src + e1);
+            scale[u] = __ldg((second ? a.vs : a.ks) + row);
+          } else {
+            const T* src = reinterpret_cast<const T*>(second ? a.vc : a.kc) + row * a.D;
+            w[u][0].load(src + e0);
+            w[u][1].load(src + e1);
+          }
+        }
+        walk.next();
+      }
     }
-    w.store(dst);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (dst[u] == nullptr) continue;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (kQuant) {
+          float f[8];
+          e4m3x4_to_f32(codes[u][x].x, f);
+          e4m3x4_to_f32(codes[u][x].y, f + 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= scale[u];
+          w[u][x].set(f);
+        }
+        w[u][x].store(dst[u] + (x ? e1 : e0));
+      }
+    }
   }
 }
 

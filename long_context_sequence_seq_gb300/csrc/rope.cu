@@ -34,14 +34,17 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int64_t n0 = (int64_t)blockIdx.x * tb;
   const int tokens = (int)(a.N - n0 < tb ? a.N - n0 : tb);
   const int half = a.half;
-  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-    const int t = i / half, p = i - t * half;
-    const int32_t pos = __ldg(a.pos + (int64_t)a.axis[p] * a.N + n0 + t);
-    const uint64_t turn = (uint64_t)(int64_t)pos * a.freq[p];
-    float s, c;
-    sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // half turns: * 2^-31
-    cos_s[i] = c;
-    sin_s[i] = a.inverse ? -s : s;
+  // a thread forms one pair's angles, for every fourth token
+  if (const int p = threadIdx.x % kMaxRopePairs; p < half) {
+    const uint64_t freq = a.freq[p];
+    const int32_t* pos = a.pos + (int64_t)a.axis[p] * a.N + n0;
+    for (int t = threadIdx.x / kMaxRopePairs; t < tokens; t += kThreads / kMaxRopePairs) {
+      const uint64_t turn = (uint64_t)(int64_t)__ldg(pos + t) * freq;
+      float s, c;
+      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // half turns: * 2^-31
+      cos_s[t * half + p] = c;
+      sin_s[t * half + p] = a.inverse ? -s : s;
+    }
   }
   __syncthreads();
   const int h0 = blockIdx.y * heads_cta;
@@ -51,52 +54,72 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // the two words of this thread: 8 pairs, or 16 elements that are copied
   const int oa = (turned && a.pairs == ULYSSES_PAIRS_HALF) ? 8 * c : 16 * c;
   const int ob = (turned && a.pairs == ULYSSES_PAIRS_HALF) ? half + 8 * c : 16 * c + 8;
-  for (int r = threadIdx.x / chunks; r < tokens * hn; r += kThreads / chunks) {
-    int t, h;
-    if (a.heads_fast) { t = r / hn; h = r - t * hn; } else { h = r / tokens; t = r - h * tokens; }
-    h += h0;
-    int j = 0;
+  // rows that lie together in memory are neighbours; kRows of them are loaded
+  // before the first is turned (64 bytes a thread in flight)
+  const int ni = a.heads_fast ? hn : tokens, no = a.heads_fast ? tokens : hn;
+  RowWalk walk(threadIdx.x / chunks, kThreads / chunks, ni);
+  constexpr int kRows = sizeof(Tin) == 2 ? 2 : 1;
+  while (walk.o < no) {
+    Row8<Tin> wa[kRows], wb[kRows];
+    Tout* dst[kRows];
+    int tok[kRows];
 #pragma unroll
-    for (int k = 1; k < kMaxRopeItems; ++k)
-      if (k < a.njobs && h >= a.job[k].head0) j = k;
-    const RopeJob& jb = a.job[j];
-    const int64_t n = n0 + t, b = n / a.S, s = n - b * a.S;
-    const int64_t si = b * jb.src_b + s * jb.src_s + (int64_t)(h - jb.head0) * jb.src_h;
-    const int64_t di = b * jb.dst_b + s * jb.dst_s + (int64_t)(h - jb.head0) * jb.dst_h;
-    if (!in_bounds(si + ob + 7, jb.src_n) || !in_bounds(di + ob + 7, jb.dst_n)) continue;
-    const Tin* src = reinterpret_cast<const Tin*>(jb.src) + si;
-    Tout* dst = reinterpret_cast<Tout*>(jb.dst) + di;
-    Row8<Tin> wa, wb;
-    wa.load(src + oa);
-    wb.load(src + ob);
-    float x[16];
-    wa.get(x);
-    wb.get(x + 8);
-    if (turned) {
-      const float4* cp = reinterpret_cast<const float4*>(cos_s + t * half + 8 * c);
-      const float4* sp = reinterpret_cast<const float4*>(sin_s + t * half + 8 * c);
-      const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
-      const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-      const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    for (int u = 0; u < kRows; ++u) {
+      dst[u] = nullptr;
+      if (walk.o < no) {
+        const int t = a.heads_fast ? walk.o : walk.i, h = h0 + (a.heads_fast ? walk.i : walk.o);
+        int j = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // half pairs: (x[i], x[i + 8]); adjacent pairs: (x[2i], x[2i + 1])
-        if (a.pairs == ULYSSES_PAIRS_HALF) {
-          const float u = x[i], v = x[i + 8];
-          x[i] = u * cs[i] - v * sn[i];
-          x[i + 8] = u * sn[i] + v * cs[i];
-        } else {
-          const float u = x[2 * i], v = x[2 * i + 1];
-          x[2 * i] = u * cs[i] - v * sn[i];
-          x[2 * i + 1] = u * sn[i] + v * cs[i];
+        for (int k = 1; k < kMaxRopeItems; ++k)
+          if (k < a.njobs && h >= a.job[k].head0) j = k;
+        const RopeJob& jb = a.job[j];
+        const int64_t n = n0 + t;
+        // one division of 64 bits only where there is more than one batch entry
+        const int64_t b = a.S == a.N ? 0 : n / a.S, s = n - b * a.S;
+        const int64_t si = b * jb.src_b + s * jb.src_s + (int64_t)(h - jb.head0) * jb.src_h;
+        const int64_t di = b * jb.dst_b + s * jb.dst_s + (int64_t)(h - jb.head0) * jb.dst_h;
+        if (in_bounds(si + ob + 7, jb.src_n) && in_bounds(di + ob + 7, jb.dst_n)) {
+          const Tin* src = reinterpret_cast<const Tin*>(jb.src) + si;
+          wa[u].load(src + oa);
+          wb[u].load(src + ob);
+          dst[u] = reinterpret_cast<Tout*>(jb.dst) + di;
+          tok[u] = t;
         }
+        walk.next();
       }
     }
-    Row8<Tout> ya, yb;
-    ya.set(x);
-    yb.set(x + 8);
-    ya.store(dst + oa);
-    yb.store(dst + ob);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (dst[u] == nullptr) continue;
+      float x[16];
+      wa[u].get(x);
+      wb[u].get(x + 8);
+      if (turned) {
+        const float4* cp = reinterpret_cast<const float4*>(cos_s + tok[u] * half + 8 * c);
+        const float4* sp = reinterpret_cast<const float4*>(sin_s + tok[u] * half + 8 * c);
+        const float4 c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+        const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // half pairs: (x[i], x[i + 8]); adjacent pairs: (x[2i], x[2i + 1])
+          if (a.pairs == ULYSSES_PAIRS_HALF) {
+            const float p = x[i], q = x[i + 8];
+            x[i] = p * cs[i] - q * sn[i];
+            x[i + 8] = p * sn[i] + q * cs[i];
+          } else {
+            const float p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = p * cs[i] - q * sn[i];
+            x[2 * i + 1] = p * sn[i] + q * cs[i];
+          }
+        }
+      }
+      Row8<Tout> ya, yb;
+      ya.set(x);
+      yb.set(x + 8);
+      ya.store(dst[u] + oa);
+      yb.store(dst[u] + ob);
+    }
   }
 }
 
@@ -106,7 +129,10 @@ int launch_rope(const RopeArgs& a, cudaStream_t st) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int tb = kMaxTokens;
+  // tokens of a CTA: enough that each thread moves about four rows, few enough
+  // that the last wave is short (64 tokens' worth of waves cost 10% at 17100)
+  int tb = 1;
+  while (tb < kMaxTokens && tb * a.heads * (a.D / 16) < 4 * kThreads) tb *= 2;
   while (tb > 1 && (a.N + tb - 1) / tb < 4 * sms) tb /= 2;
   const int64_t gx = (a.N + tb - 1) / tb;
   // few tokens: split the heads too, down to 8 heads (one round of the CTA's threads or two)

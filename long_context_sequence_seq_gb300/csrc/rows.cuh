@@ -56,12 +56,42 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
   }
 }
 
+__device__ __forceinline__ float max_nan(float x, float y) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// Eight fp32 values times `by` as e4m3 codes.
+__device__ __forceinline__ uint2 to_codes(const float* f, float by) {
+  uint2 c;
+  c.x = f32_to_e4m3x2(f[0] * by, f[1] * by) | (uint32_t)f32_to_e4m3x2(f[2] * by, f[3] * by) << 16;
+  c.y = f32_to_e4m3x2(f[4] * by, f[5] * by) | (uint32_t)f32_to_e4m3x2(f[6] * by, f[7] * by) << 16;
+  return c;
+}
+
 // Eight elements of type T: 16 bytes of bf16, two 16-byte words of fp32.
 template <typename T> struct Row8;
 template <> struct Row8<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = ld16(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { st16(p, w); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  // largest magnitude, NaN if any is (two elements an instruction)
+  __device__ __forceinline__ float amax() const {
+    const uint32_t s = 0x7fff7fffu;
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(w.x & s, w.y & s), max_nan_bf16x2(w.z & s, w.w & s));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  __device__ __forceinline__ uint2 codes(float by) const {
+    float f[8];
+    get(f);
+    return to_codes(f, by);
+  }
   __device__ __forceinline__ void get(float* f) const {
     bf16x2_to_f32(w.x, f); bf16x2_to_f32(w.y, f + 2); bf16x2_to_f32(w.z, f + 4); bf16x2_to_f32(w.w, f + 6);
   }
@@ -74,6 +104,20 @@ template <> struct Row8<float> {
   uint4 a, b;
   __device__ __forceinline__ void load(const float* p) { a = ld16(p); b = ld16(p + 4); }
   __device__ __forceinline__ void store(float* p) const { st16(p, a); st16(p + 4, b); }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float amax() const {
+    float f[8];
+    get(f);
+    float m = fabsf(f[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+    return m;
+  }
+  __device__ __forceinline__ uint2 codes(float by) const {
+    float f[8];
+    get(f);
+    return to_codes(f, by);
+  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
     f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
@@ -81,6 +125,23 @@ template <> struct Row8<float> {
   __device__ __forceinline__ void set(const float* f) {
     a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  }
+};
+
+// Rows r, r + step, r + 2 step, ... of a block of `no` x `ni` rows, as (outer,
+// inner) indexes: one division at the start, none per row.
+struct RowWalk {
+  int o, i, ni, step_o, step_i;
+  __device__ __forceinline__ RowWalk(int r, int step, int ni_) : ni(ni_) {
+    o = r / ni;
+    i = r - o * ni;
+    step_o = step / ni;
+    step_i = step - step_o * ni;
+  }
+  __device__ __forceinline__ void next() {
+    i += step_i;
+    o += step_o;
+    if (i >= ni) { i -= ni; ++o; }
   }
 };
 

@@ -11,7 +11,9 @@ head layout [B, n, S, D] (the n heads of one UPipe stage, or all heads).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -97,7 +99,7 @@ def lib():
     L.ulysses_layer_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32,
                                     i32, i32, vp, i32, i32, f32, i32, vp, sz, vp]
     for fn in (L.ulysses_rope_fwd, L.ulysses_rope_bwd):
-        fn.argtypes = [ctypes.POINTER(RopeItem), i32, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32, i32, vp]
+        fn.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, i64, i32, i32, i32, i32, vp]
     L.ulysses_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, i64, i32,
                                       i32, i32, i32, i32, vp]
     L.ulysses_cache_read.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i64, i32,
@@ -508,8 +510,15 @@ def layer_bwd_fused(q_seq, k_seq, v_seq, o_seq, do_seq, lse, P, head_chunk, cu_s
 # "head": heads, tokens, D; D contiguous).  They run on the device of their
 # tensors, whichever is current, on `stream` or that device's current stream;
 # outputs and workspaces made here belong to that stream.
+# A call's kernels take a few microseconds at decode sizes, so these functions
+# read each tensor property once and make no objects besides the results.
 
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float8_e4m3fn: E4M3}
+_BF16, _F32, _F64, _I32, _U8, _F8 = (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8,
+                                     torch.float8_e4m3fn)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda idx: torch.cuda.current_stream(idx).cuda_stream)
 
 
 def _code(dtype, what):
@@ -519,65 +528,72 @@ def _code(dtype, what):
     return c
 
 
-def _device_of(*tensors):
-    """The one CUDA device of the tensors (None entries left out)."""
-    dev = None
+def _device_of(tensors):
+    """Index of the one CUDA device of the tensors (None entries left out)."""
+    idx = -2
     for t in tensors:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError("expected a CUDA tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return dev
+            i = t.get_device()
+            if i != idx:
+                if i < 0:
+                    raise ValueError("expected a CUDA tensor")
+                if idx >= 0:
+                    raise ValueError(f"tensors on different devices: cuda:{idx} and cuda:{i}")
+                idx = i
+    return idx
 
 
 def _flat(t, dtype, what):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, layout, what, dims=3):
-    """(token stride, head stride, tokens, heads) of a 3-D tensor of rows."""
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions")
-    if t.stride(-1) != 1 and t.numel():
+def _rows(t, layout, what):
+    """(token stride, head stride, tokens, heads, D) of a tensor of rows, its
+    last three dimensions."""
+    sh, st = t.shape, t.stride()
+    if len(sh) < 3:
+        raise ValueError(f"{what} must have three dimensions")
+    if st[-1] != 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
     if layout == "seq":
-        return t.stride(-3), t.stride(-2), t.shape[-3], t.shape[-2]
+        return st[-3], st[-2], sh[-3], sh[-2], sh[-1]
     if layout == "head":
-        return t.stride(-2), t.stride(-3), t.shape[-2], t.shape[-3]
+        return st[-2], st[-3], sh[-2], sh[-3], sh[-1]
     raise ValueError(f"unknown layout {layout!r}")
 
 
-def _launch(fn, dev, stream, tensors, *args):
-    """fn(*args, stream) on device dev.  A stream other than the device's
-    current one is recorded on the tensors, so that freeing one of them does
-    not hand its memory on while the call still runs."""
-    def go():
-        cur = torch.cuda.current_stream(dev)
-        if stream is None or stream == cur:
-            return fn(*args, cur.cuda_stream)
+def _rows3(t, layout, what):
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have three dimensions")
+    return _rows(t, layout, what)
+
+
+def _launch(fn, idx, stream, tensors, args):
+    """fn(*args, stream) on device idx.  A stream given by the caller is
+    recorded on the tensors, so that freeing one of them does not hand its
+    memory on while the call still runs."""
+    if stream is not None:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-        return fn(*args, stream.cuda_stream)
-    if dev.index == torch.cuda.current_device():
-        _ck(go())
+    if idx == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(idx) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            _ck(go())
+        with torch.cuda.device(idx):
+            rc = fn(*args, _raw_stream(idx) if stream is None else stream.cuda_stream)
+    if rc != OK:
+        _ck(rc)
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(like, shape, dtype, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 # --------------------------------------------------------------- rotary positions
@@ -595,51 +611,57 @@ def rope_frequencies(rot_dim, base=10000.0, sections=None):
     return inv, torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.int32)
 
 
+_PACK_ITEM = struct.Struct("@PPi6q").pack     # ulysses_rope_item
+_PAIRS = {"half": PAIRS_HALF, "adjacent": PAIRS_ADJACENT}
+
+
 def _rope(fn, q, k, positions, inv_freq, axes, layout, pairs, dtype, out, stream):
-    given = [t for t in (q, k) if t is not None]
-    if not given:
+    given = (q,) if k is None else (k,) if q is None else (q, k)
+    first = given[0]
+    if first is None:
         raise ValueError("rope: no tensor given")
-    if out is not None:
-        out = list(out) if isinstance(out, (tuple, list)) else [out]
+    if out is None:
+        out = (None,) * len(given)
+    else:
+        out = tuple(out) if isinstance(out, (tuple, list)) else (out,)
         if len(out) != len(given):
             raise ValueError("rope: one output for each tensor")
-    dev = _device_of(*given, positions, *(out or ()))
-    first = given[0]
-    dt = first.dtype if dtype is None else dtype
-    D = first.shape[-1]
-    items = (RopeItem * len(given))()
-    results = []
-    S = B = None
-    for i, t in enumerate(given):
-        four = t.dim() == 4
-        ss, sh, n, H = _rows(t, layout, "rope input", 4 if four else 3)
-        nb, sb = (t.shape[0], t.stride(0)) if four else (1, 0)
+    idx = _device_of((*given, positions, *out))
+    din, dims = first.dtype, first.dim()
+    dout = din if dtype is None else dtype
+    if dims not in (3, 4):
+        raise ValueError("rope: tensors have three or four dimensions")
+    items, results, S, B, D = b"", [], None, 1, 0
+    for t, o in zip(given, out):
+        ss, sh, n, H, d = _rows(t, layout, "rope input")
+        nb, sb = (t.shape[0], t.stride(0)) if dims == 4 else (1, 0)
         if S is None:
-            S, B = n, nb
-        if (n, nb, t.shape[-1], t.dtype, t.dim()) != (S, B, D, first.dtype, first.dim()):
+            S, B, D = n, nb, d
+        elif n != S or nb != B or d != D or t.dtype is not din or t.dim() != dims:
             raise ValueError("rope: tensors of one call share their tokens, D and dtype")
-        o = _empty(t.shape, dt, dev, stream) if out is None else out[i]
-        if o.shape != t.shape or o.dtype != dt:
+        if o is None:
+            o = _empty(t, t.shape, dout, stream)
+        elif o.shape != t.shape or o.dtype is not dout:
             raise ValueError("rope: an output must have its input's shape and the call's dtype")
-        os_, oh, _, _ = _rows(o, layout, "rope output", 4 if four else 3)
-        items[i] = RopeItem(t.data_ptr(), o.data_ptr(), H, sb, ss, sh, o.stride(0) if four else 0, os_, oh)
+        os_, oh, _, _, _ = _rows(o, layout, "rope output")
+        items += _PACK_ITEM(t.data_ptr(), o.data_ptr(), H, sb, ss, sh, o.stride(0) if dims == 4 else 0, os_, oh)
         results.append(o)
-    n_axes, rest = (1, tuple(positions.shape)) if positions.dim() == first.dim() - 2 else \
-        (positions.shape[0], tuple(positions.shape[1:]))
-    if rest != ((B, S) if first.dim() == 4 else (S,)):
+    n_axes, rest = (1, positions.shape) if positions.dim() == dims - 2 else (positions.shape[0], positions.shape[1:])
+    if tuple(rest) != ((B, S) if dims == 4 else (S,)):
         raise ValueError(f"rope: positions {tuple(positions.shape)} do not match {B} x {S} tokens")
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
+    half = inv_freq.numel()
+    if inv_freq.dtype is not _F64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor in host memory")
-    if axes is not None and (axes.dtype != torch.int32 or axes.is_cuda or not axes.is_contiguous()
-                             or axes.numel() != inv_freq.numel()):
+    if axes is not None and (axes.dtype is not _I32 or axes.is_cuda or not axes.is_contiguous()
+                             or axes.numel() != half):
         raise ValueError("axes must be a contiguous int32 tensor in host memory, one entry for each frequency")
-    if pairs not in ("half", "adjacent"):
+    if pairs not in _PAIRS:
         raise ValueError(f"unknown pair order {pairs!r}")
-    _launch(fn, dev, stream, (*given, positions, *results), items, len(given),
-            _flat(positions, torch.int32, "positions"), n_axes, inv_freq.data_ptr(),
-            None if axes is None else axes.data_ptr(), 2 * inv_freq.numel(),
-            PAIRS_HALF if pairs == "half" else PAIRS_ADJACENT, S, B, D, _code(first.dtype, "rope"), _code(dt, "rope"))
-    return results[0] if len(given) == 1 else tuple(results)
+    _launch(fn, idx, stream, (*given, positions, *results),
+            (items, len(given), _flat(positions, _I32, "positions"), n_axes, inv_freq.data_ptr(),
+             None if axes is None else axes.data_ptr(), 2 * half, _PAIRS[pairs], S, B, D, _code(din, "rope"),
+             _code(dout, "rope")))
+    return results[0] if len(results) == 1 else tuple(results)
 
 
 def rope_fwd(q, k, positions, inv_freq, axes=None, layout="seq", pairs="half", out=None, stream=None):
@@ -678,23 +700,30 @@ def kv_cache(num_pages, page_size, H_kv, D, dtype=torch.bfloat16, device="cuda")
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Pointers of the cache's buffers, in the C calls' order, after the checks
-    that need the tensors."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    """Pointers of the cache's buffers and its sizes, after the checks that
+    need the tensors."""
+    sh, dt = k_cache.shape, k_cache.dtype
+    if len(sh) != 4 or sh != v_cache.shape or dt is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must be [num_pages, H_kv, page_size, D] of one shape and dtype")
-    for t in (k_scale, v_scale):
-        if t is not None and t.shape != k_cache.shape[:3]:
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
+    ks = vs = None
+    if k_scale is not None:
+        if k_scale.shape != sh[:3]:
             raise ValueError("scales must be [num_pages, H_kv, page_size]")
-    dt = k_cache.dtype
-    return (_flat(k_cache, dt, "k_cache"), _flat(v_cache, dt, "v_cache"),
-            None if k_scale is None else _flat(k_scale, torch.float32, "k_scale"),
-            None if v_scale is None else _flat(v_scale, torch.float32, "v_scale"))
+        ks = _flat(k_scale, _F32, "k_scale")
+    if v_scale is not None:
+        if v_scale.shape != sh[:3]:
+            raise ValueError("scales must be [num_pages, H_kv, page_size]")
+        vs = _flat(v_scale, _F32, "v_scale")
+    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, sh
 
 
 def _batch_table(page_table, n, what):
-    if page_table.dim() != 2 or page_table.shape[0] != n:
+    sh = page_table.shape
+    if len(sh) != 2 or sh[0] != n:
         raise ValueError(f"page_table must be [B, columns], B = {n} as {what}")
-    return _flat(page_table, torch.int32, "page_table"), page_table.shape[1]
+    return _flat(page_table, _I32, "page_table"), sh[1]
 
 
 def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_scale=None, v_scale=None, layout="seq",
@@ -707,24 +736,26 @@ def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_sca
     rows [cu_new[b], cu_new[b+1]); None: one token per sequence, and a length
     of 0 marks an empty place of the batch.  An e4m3 cache (with its scales) is
     quantised row by row on the way.  Bad positions or pages raise in check()."""
-    ks, kh, T, H = _rows(k, layout, "k")
-    vs, vh, Tv, Hv = _rows(v, layout, "v")
-    if (T, H, k.shape[-1], k.dtype) != (Tv, Hv, v.shape[-1], v.dtype):
+    ks, kh, T, H, D = _rows3(k, layout, "k")
+    vs, vh, Tv, Hv, Dv = _rows3(v, layout, "v")
+    dt = k.dtype
+    if T != Tv or H != Hv or D != Dv or dt is not v.dtype:
         raise ValueError("k and v must have one shape and dtype")
-    if (H, k.shape[-1]) != (k_cache.shape[1], k_cache.shape[-1]):
+    tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new)
+    pk, pv, pks, pvs, sh = _cache(k_cache, v_cache, k_scale, v_scale)
+    if H != sh[1] or D != sh[3]:
         raise ValueError("rows and cache differ in heads or D")
-    dev = _device_of(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new)
-    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
+    idx = _device_of(tensors)
     B = seq_lens.numel()
     tab, cols = _batch_table(page_table, B, "seq_lens")
-    if cu_new is not None and cu_new.numel() != B + 1:
-        raise ValueError("cu_new must have B + 1 entries")
-    _launch(lib().ulysses_cache_write, dev, stream,
-            (k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new),
-            k.data_ptr(), v.data_ptr(), ks, kh, vs, vh, T, B,
-            None if cu_new is None else _flat(cu_new, torch.int32, "cu_new"), tab, cols,
-            _flat(seq_lens, torch.int32, "seq_lens"), pk, pv, pks, pvs, k_cache.shape[0], k_cache.shape[2], H,
-            k.shape[-1], _code(k.dtype, "k"), _code(k_cache.dtype, "k_cache"))
+    cu = None
+    if cu_new is not None:
+        if cu_new.numel() != B + 1:
+            raise ValueError("cu_new must have B + 1 entries")
+        cu = _flat(cu_new, _I32, "cu_new")
+    _launch(lib().ulysses_cache_write, idx, stream, tensors,
+            (k.data_ptr(), v.data_ptr(), ks, kh, vs, vh, T, B, cu, tab, cols, _flat(seq_lens, _I32, "seq_lens"), pk, pv,
+             pks, pvs, sh[0], sh[2], H, D, _code(dt, "k"), _code(k_cache.dtype, "k_cache")))
 
 
 def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=None, v_scale=None, dtype=None,
@@ -734,38 +765,47 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=
     cu_seqlens[b] (first None: 0).  Returns (k, v) with T tokens, [T, H_kv, D]
     or [H_kv, T, D]; rows from cu_seqlens[B] on are left as they were.  dtype:
     the cache's, or bf16 (default) / fp32 from an e4m3 cache."""
-    dev = _device_of(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first, *(out or ()))
-    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
-    n_pages, H, page, D = k_cache.shape
+    pk, pv, pks, pvs, (n_pages, H, page, D) = _cache(k_cache, v_cache, k_scale, v_scale)
+    held = k_cache.dtype
     if dtype is None:
-        dtype = out[0].dtype if out is not None else torch.bfloat16 if k_cache.dtype == torch.float8_e4m3fn else \
-            k_cache.dtype
+        dtype = out[0].dtype if out is not None else _BF16 if held is _F8 else held
     B = cu_seqlens.numel() - 1
     tab, cols = _batch_table(page_table, B, "cu_seqlens")
-    if first is not None and first.numel() != B:
-        raise ValueError("first must have B entries")
+    at = None
+    if first is not None:
+        if first.numel() != B:
+            raise ValueError("first must have B entries")
+        at = _flat(first, _I32, "first")
     shape = (T, H, D) if layout == "seq" else (H, T, D)
-    k, v = out if out is not None else (_empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream))
-    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.dtype != dtype or v.dtype != dtype:
-        raise ValueError(f"cache_read: outputs must be {shape} of {dtype}")
-    ks, kh, _, _ = _rows(k, layout, "k")
-    vs, vh, _, _ = _rows(v, layout, "v")
-    _launch(lib().ulysses_cache_read, dev, stream,
-            (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first),
-            pk, pv, pks, pvs, tab, cols, _flat(cu_seqlens, torch.int32, "cu_seqlens"),
-            None if first is None else _flat(first, torch.int32, "first"), k.data_ptr(), v.data_ptr(), ks, kh, vs, vh,
-            T, B, n_pages, page, H, D, _code(dtype, "k"), _code(k_cache.dtype, "k_cache"))
+    idx = _device_of((k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first, *(out or ())))
+    if out is None:
+        k, v = _empty(k_cache, shape, dtype, stream), _empty(k_cache, shape, dtype, stream)
+    else:
+        k, v = out
+        if k.shape != shape or v.shape != shape or k.dtype is not dtype or v.dtype is not dtype:
+            raise ValueError(f"cache_read: outputs must be {shape} of {dtype}")
+    tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first)
+    ks, kh, _, _, _ = _rows3(k, layout, "k")
+    vs, vh, _, _, _ = _rows3(v, layout, "v")
+    _launch(lib().ulysses_cache_read, idx, stream, tensors,
+            (pk, pv, pks, pvs, tab, cols, _flat(cu_seqlens, _I32, "cu_seqlens"), at, k.data_ptr(), v.data_ptr(), ks, kh,
+             vs, vh, T, B, n_pages, page, H, D, _code(dtype, "k"), _code(held, "k_cache")))
     return k, v
 
 
 # --------------------------------------------------------------- single-token attention
 
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(*sizes):
+    return lib().ulysses_attn_decode_workspace(*sizes)
+
+
 def attn_decode_workspace(q, k_cache, page_table, layout="seq"):
     """Workspace for attn_decode on tensors of these shapes (uint8, on their
     device; empty where the call needs none)."""
-    _, _, B, H_q = _rows(q, layout, "q")
-    n = lib().ulysses_attn_decode_workspace(B, H_q, k_cache.shape[1], q.shape[-1], page_table.shape[1],
-                                            k_cache.shape[2], _code(q.dtype, "q"), _code(k_cache.dtype, "k_cache"))
+    _, _, B, H_q, D = _rows3(q, layout, "q")
+    n = _decode_bytes(B, H_q, k_cache.shape[1], D, page_table.shape[1], k_cache.shape[2], _code(q.dtype, "q"),
+                      _code(k_cache.dtype, "k_cache"))
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
@@ -779,31 +819,30 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     cached positions; length 0 gives O = 0, LSE = -inf.  Returns (O shaped as
     q, LSE [B, H_q] fp32).  workspace: attn_decode_workspace(), for calls that
     do not overlap on the GPU; made per call if not given."""
-    qb, qh, B, H_q = _rows(q, layout, "q")
-    dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse)
-    pk, pv, pks, pvs = _cache(k_cache, v_cache, k_scale, v_scale)
-    n_pages, H_kv, page, D = k_cache.shape
-    if q.shape[-1] != D or seq_lens.numel() != B:
+    qb, qh, B, H_q, D = _rows3(q, layout, "q")
+    pk, pv, pks, pvs, (n_pages, H_kv, page, Dc) = _cache(k_cache, v_cache, k_scale, v_scale)
+    if D != Dc or seq_lens.numel() != B:
         raise ValueError("attn_decode: q, cache and seq_lens differ in D or B")
+    idx = _device_of((q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse))
     tab, cols = _batch_table(page_table, B, "q")
-    L = lib()
-    dq, dc = _code(q.dtype, "q"), _code(k_cache.dtype, "k_cache")
+    dt = q.dtype
+    dq, dc = _code(dt, "q"), _code(k_cache.dtype, "k_cache")
     if out is None:
-        out = _empty(q.shape, q.dtype, dev, stream)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = _empty(q, q.shape, dt, stream)
+    elif out.shape != q.shape or out.dtype is not dt:
         raise ValueError("attn_decode: out must have q's shape and dtype")
-    ob, oh, _, _ = _rows(out, layout, "out")
+    ob, oh, _, _, _ = _rows3(out, layout, "out")
     if lse is None:
-        lse = _empty((B, H_q), torch.float32, dev, stream)
-    elif tuple(lse.shape) != (B, H_q):
+        lse = _empty(q, (B, H_q), _F32, stream)
+    elif lse.shape != (B, H_q):
         raise ValueError("attn_decode: lse must be [B, H_q]")
     if workspace is None:
-        n = L.ulysses_attn_decode_workspace(B, H_q, H_kv, D, cols, page, dq, dc)
-        workspace = _empty((n,), torch.uint8, dev, stream) if n else None
-    ws, n = (None, 0) if workspace is None else (_flat(workspace, torch.uint8, "workspace"), workspace.numel())
-    _launch(L.ulysses_attn_decode, dev, stream,
+        n = _decode_bytes(B, H_q, H_kv, D, cols, page, dq, dc)
+        if n:
+            workspace = _empty(q, (n,), _U8, stream)
+    ws, n = (None, 0) if workspace is None else (_flat(workspace, _U8, "workspace"), workspace.numel())
+    _launch(lib().ulysses_attn_decode, idx, stream,
             (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse),
-            q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, torch.int32, "seq_lens"),
-            out.data_ptr(), ob, oh, _flat(lse, torch.float32, "lse"), B, H_q, H_kv, D, n_pages, page,
-            float(scale or 0.0), dq, dc, ws, n)
+            (q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, _I32, "seq_lens"), out.data_ptr(), ob, oh,
+             _flat(lse, _F32, "lse"), B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n))
     return out, lse
