@@ -413,6 +413,10 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * the table, and a page id outside [0, num_pages), are reported by
  * ulysses_check as ULYSSES_ERR_BAD_PAGES (the keys concerned are left out).
  * Results do not depend on the order in which the GPU runs the call's blocks.
+ * Scales of an E4M3 cache are positive (or NaN).  With FP32 queries products
+ * are formed of two 11-bit parts of each operand: rounded as in fp32, but an
+ * infinite element gives NaN (a K element in its key's score, a V element in
+ * its output element).
  * B * H_q <= 2^24; strides and alignment as for ulysses_cache_write. */
 size_t ulysses_attn_decode_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
                                      int cache_dtype);

@@ -161,7 +161,7 @@ struct MatrixEngine {
   using TQ = __nv_bfloat16;
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRowB = kQuant ? D : 2 * D;        // bytes of a row
-  static constexpr int kSub = 256 / kRowB;                // units of a step: 32 registers of K and of V
+  static constexpr int kSub = kRowB == 256 ? 1 : 2;       // units of a step: 32 registers of K and of V, or 16
   static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
   static constexpr int kVB = kRowB / 8 < 16 ? 8 : 16;     // V: bytes of a word
   static constexpr int kVW = kRowB / (8 * kVB);           //    words of a row per lane
@@ -517,6 +517,229 @@ struct MatrixEngine {
   }
 };
 
+// ------------------------------------------------------------------ fp32 matrix engine
+
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {   // nearest, 11 significant bits
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = to_tf32(x);
+  lo = to_tf32(x - __uint_as_float(hi));
+}
+
+template <bool kQuant, int D>
+struct SplitEngine {
+  using TQ = float;
+  static constexpr int kHeads = 8;
+  static constexpr int kHalf = 8;                         // keys of a step
+  static constexpr int kRowB = kQuant ? D : 4 * D;
+  static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
+  static constexpr int kKE = D / 4;                       //    elements of a row per lane
+  static constexpr int kVB = kRowB / 8 < 16 ? 8 : 16;     // V: bytes of a word
+  static constexpr int kVW = kRowB / (8 * kVB);
+  static constexpr int kVE = D / 8;                       //    elements of a row per lane
+  static constexpr int kWE = kVE / kVW;                   //    elements of a word
+
+  uint32_t q[kKE / 2][4];
+  float acc[kVE][4];
+  float m, l;
+  int lane, g, j;
+
+  struct Rows { uint4 k[kKW]; uint32_t v[2][kVW * kVB / 4]; float2 ks, vs; };
+
+  __device__ __forceinline__ SplitEngine(int lane_) : lane(lane_), g(lane_ >> 2), j(lane_ & 3) {}
+
+  // the d of K's element e in lane j
+  __device__ __forceinline__ static int k_index(int e, int j) {
+    constexpr int w = kQuant ? 16 : 4;
+    return (e / w * 4 + j) * w + e % w;
+  }
+  __device__ __forceinline__ void begin(const DecodeArgs& a, const Piece& p) {
+    const bool live = g < p.gn;
+    const float* qp = reinterpret_cast<const float*>(a.q) + (int64_t)p.b * a.q_b + (int64_t)(p.h * a.G + p.g0 + (live ? g : 0)) * a.q_h;
+#pragma unroll
+    for (int i = 0; i < kKE / 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        split_tf32(live ? qp[k_index(2 * i + x, j)] * a.scale_log2 : 0.f, q[i][2 * x], q[i][2 * x + 1]);
+#pragma unroll
+    for (int i = 0; i < kVE; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+    m = kNoMax;
+    l = 0.f;
+  }
+  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int64_t row, int keys) {
+    const char* p = reinterpret_cast<const char*>(a.kc) + (row + g) * kRowB + j * 16;
+    const bool ok = g < keys;
+#pragma unroll
+    for (int w = 0; w < kKW; ++w) r.k[w] = ok ? ld16(p + w * 64) : make_uint4(0, 0, 0, 0);
+    if (kQuant) {
+      r.ks.x = 2 * j < keys ? __ldg(a.ks + row + 2 * j) : 0.f;
+      r.ks.y = 2 * j + 1 < keys ? __ldg(a.ks + row + 2 * j + 1) : 0.f;
+      r.vs.x = 2 * j < keys ? __ldg(a.vs + row + 2 * j) : 0.f;
+      r.vs.y = 2 * j + 1 < keys ? __ldg(a.vs + row + 2 * j + 1) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int64_t row, int keys) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const char* p = reinterpret_cast<const char*>(a.vc) + (row + 2 * j + x) * kRowB + g * kVB;
+      const bool ok = 2 * j + x < keys;
+#pragma unroll
+      for (int w = 0; w < kVW; ++w) {
+        if (kVB == 16) {
+          const uint4 t = ok ? ld16(p + w * 128) : make_uint4(0, 0, 0, 0);
+          r.v[x][w * 4] = t.x; r.v[x][w * 4 + 1] = t.y; r.v[x][w * 4 + 2] = t.z; r.v[x][w * 4 + 3] = t.w;
+        } else {
+          const uint2 t = ok ? ld8(p) : make_uint2(0, 0);
+          r.v[x][0] = t.x; r.v[x][1] = t.y;
+        }
+      }
+    }
+  }
+  // elements e, e + 1 of a lane's words
+  __device__ __forceinline__ static void pair(const uint32_t* w, int e, float* f) {
+    if (!kQuant) {
+      f[0] = __uint_as_float(w[e]);
+      f[1] = __uint_as_float(w[e + 1]);
+    } else {
+      const uint32_t h = e4m3x2_to_f16x2((uint16_t)(w[e / 4] >> (8 * (e % 4))));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[0] = v.x;
+      f[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void run(const DecodeArgs& a, const Piece& p) {
+    const int64_t total = a.num_pages * a.H_kv * a.page;
+    Walk walk(a, p);
+    Rows r;
+    // steps are half units: `half` is the one that `row` and `keys` stand for
+    int half = 0, left = min(p.len - p.unit0 * kUnit, p.units * kUnit);
+    int64_t row = 0;
+    int keys = 0, pg = walk.fetch();
+    auto place = [&]() {
+      if ((half & 1) == 0) {
+        const int n = walk.unit(pg);
+        row = (int64_t)n * kUnit;
+        keys = n >= 0 && in_bounds(row + kUnit - 1, total) ? min(max(left - half * kHalf, 0), kUnit) : 0;
+        walk.next();
+        pg = walk.fetch();
+      } else {
+        row += kHalf;
+        keys = max(keys - kHalf, 0);
+      }
+      ++half;
+    };
+    place();
+    load_k(a, r, row, keys);
+    load_v(a, r, row, keys);
+    for (int at = 0; at < left; at += kHalf) {
+      const int mine = min(keys, kHalf);
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        uint32_t kw[kKW * 4];
+#pragma unroll
+        for (int w = 0; w < kKW; ++w) { kw[4 * w] = r.k[w].x; kw[4 * w + 1] = r.k[w].y; kw[4 * w + 2] = r.k[w].z; kw[4 * w + 3] = r.k[w].w; }
+#pragma unroll
+        for (int i = 0; i < kKE / 2; ++i) {
+          float f[2];
+          pair(kw, 2 * i, f);
+          if (kQuant) {
+            mma_tf32(s, q[i], __float_as_uint(f[0]), __float_as_uint(f[1]));
+          } else {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(f[0], h0, l0);
+            split_tf32(f[1], h1, l1);
+            mma_tf32(s, q[i], h0, h1);
+            mma_tf32(s, q[i], l0, l1);
+          }
+        }
+      }
+      const float2 ks = r.ks, vs = r.vs;
+      place();
+      load_k(a, r, row, keys);
+      // rows g and g + 8 of the product: the high and the low parts of head g
+      float t0 = s[0] + s[2], t1 = s[1] + s[3];
+      if (kQuant) { t0 *= ks.x; t1 *= ks.y; }
+      t0 = 2 * j < mine ? t0 : -INFINITY;
+      t1 = 2 * j + 1 < mine ? t1 : -INFINITY;
+      if (__any_sync(0xffffffffu, fmaxf(t0, t1) > m + kLazy)) {
+        float mm = fmaxf(t0, t1);
+        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 1));
+        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
+        mm = fmaxf(mm, m);
+        const float f = exp2f(m - mm);
+        m = mm;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < kVE; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][c] *= f;
+      }
+      float p0 = exp2f(t0 - m), p1 = exp2f(t1 - m);
+      l += p0 + p1;
+      if (kQuant) { p0 *= vs.x; p1 *= vs.y; }
+      uint32_t w[4];
+      split_tf32(p0, w[0], w[1]);
+      split_tf32(p1, w[2], w[3]);
+#pragma unroll
+      for (int e = 0; e < kVE; e += 2) {
+        float a0[2], a1[2];                               // elements e, e + 1 of rows 2j, 2j + 1
+        pair(r.v[0], e, a0);
+        pair(r.v[1], e, a1);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (kQuant) {
+            mma_tf32(acc[e + x], w, __float_as_uint(a0[x]), __float_as_uint(a1[x]));
+          } else {
+            uint32_t h0, l0, h1, l1;
+            split_tf32(a0[x], h0, l0);
+            split_tf32(a1[x], h1, l1);
+            mma_tf32(acc[e + x], w, h0, h1);
+            mma_tf32(acc[e + x], w, l0, l1);
+          }
+        }
+      }
+      load_v(a, r, row, keys);
+    }
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+  }
+  // the sums of head g: element e of V's lanes 2j + x
+  template <class Store>
+  __device__ __forceinline__ void each_word(float by, Store&& store) const {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < kVE; e += 4) {
+        const int d = ((e / kWE) * 8 + 2 * j + x) * kWE + e % kWE;
+        store(d, make_float4((acc[e][x] + acc[e][x + 2]) * by, (acc[e + 1][x] + acc[e + 1][x + 2]) * by,
+                             (acc[e + 2][x] + acc[e + 2][x + 2]) * by, (acc[e + 3][x] + acc[e + 3][x + 2]) * by));
+      }
+  }
+  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
+    (void)heads;
+    if (g >= gn) return;
+    if (j == 0) ml[g] = make_float2(m, l);
+    each_word(1.f, [&](int d, float4 v) { *reinterpret_cast<float4*>(o + g * D + d) = v; });
+  }
+  __device__ __forceinline__ void result(const DecodeArgs& a, const Piece& p) const {
+    if (g >= p.gn) return;
+    const int hq = p.h * a.G + p.g0 + g;
+    if (j == 0 && a.lse) a.lse[(int64_t)p.b * a.H_q + hq] = (m + log2f(l)) * kLn2;
+    float* out = reinterpret_cast<float*>(a.o) + (int64_t)p.b * a.o_b + (int64_t)hq * a.o_h;
+    each_word(1.f / l, [&](int d, float4 v) { *reinterpret_cast<float4*>(out + d) = v; });
+  }
+};
+
 // ------------------------------------------------------------------ SIMT engine
 
 // One lane's part of a row: 8 lanes hold D values, lane i the 16-byte words
@@ -862,81 +1085,114 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   tc::cluster_sync();                                      // no CTA leaves while another reads its sums
 }
 
-// One CTA per query head of a sequence: adds the pieces of its item, or writes
-// the result of a sequence without keys.
-template <typename TQ, int D>
-__global__ void __launch_bounds__(256) decode_join_kernel(const __grid_constant__ DecodeArgs a,
-                                                          const __grid_constant__ Plan p) {
+// Running sum of pieces: the largest m so far, and l and the values in its units.
+struct Sum { float m, l; float4 s; };
+__device__ __forceinline__ void add_piece(Sum& x, float m, float l, float4 s) {
+  const float top = fmaxf(x.m, m), fa = exp2f(x.m - top), fb = exp2f(m - top);
+  x.m = top;
+  x.l = x.l * fa + l * fb;
+  x.s.x = x.s.x * fa + s.x * fb;
+  x.s.y = x.s.y * fa + s.y * fb;
+  x.s.z = x.s.z * fa + s.z * fb;
+  x.s.w = x.s.w * fa + s.w * fb;
+}
+__device__ __forceinline__ void add_lanes(Sum& x, int o) {   // with lane ^ o, in one order on both
+  Sum y;
+  y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
+  y.l = __shfl_xor_sync(0xffffffffu, x.l, o);
+  y.s.x = __shfl_xor_sync(0xffffffffu, x.s.x, o);
+  y.s.y = __shfl_xor_sync(0xffffffffu, x.s.y, o);
+  y.s.z = __shfl_xor_sync(0xffffffffu, x.s.z, o);
+  y.s.w = __shfl_xor_sync(0xffffffffu, x.s.w, o);
+  if (threadIdx.x & o) {
+    add_piece(y, x.m, x.l, x.s);
+    x = y;
+  } else {
+    add_piece(x, y.m, y.l, y.s);
+  }
+}
+
+// Adds the pieces of an item, for one of its heads, or writes the result of a
+// sequence without keys.  kPart: a CTA for 32 of the head's values, 32 pieces
+// at a time (few items, hundreds of pieces each); kRow: a CTA for the head;
+// kWarp: a warp for it (many items, of a few pieces or none).
+constexpr int kJoin = 256;
+enum Join { kPart, kRow, kWarp };
+template <typename TQ, int D, Join kHow>
+__global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constant__ DecodeArgs a,
+                                                            const __grid_constant__ Plan p) {
+  constexpr int kLanes = kHow == kPart ? 8 : D / 4;                // threads across the values, four each
+  constexpr int kParts = (kHow == kWarp ? 32 : kJoin) / kLanes;    // pieces at a time
+  __shared__ Sum sums[kJoin / 32][kLanes];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bh = kHow == kPart ? blockIdx.x / (D / 32) : (kHow == kRow ? blockIdx.x : blockIdx.x * (kJoin / 32) + warp);
+  const int c = (kHow == kPart ? (blockIdx.x % (D / 32)) * 8 : 0) + threadIdx.x % kLanes;
+  const int part = (kHow == kWarp ? lane : threadIdx.x) / kLanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kLanes = D / 4, kParts = 256 / kLanes;     // threads of a piece's row, pieces at a time
-  __shared__ float4 so[kParts][kLanes];
-  __shared__ float sl[kParts];
-  const int hq = blockIdx.x % a.H_q, b = blockIdx.x / a.H_q;
+  if (bh >= a.B * a.H_q) return;                           // a whole warp (or CTA)
+  const int b = bh / a.H_q, hq = bh - b * a.H_q;
   const int h = hq / a.G, gi = (hq - h * a.G) / p.heads, hl = hq - h * a.G - gi * p.heads;
-  const int part = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
-  TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)b * a.o_b + (int64_t)hq * a.o_h;
-  float* lse = a.lse ? a.lse + (int64_t)b * a.H_q + hq : nullptr;
-  const int64_t before = p.prefix[b], units = p.prefix[b + 1] - before;
-  if (units == 0) {
-    for (int x = threadIdx.x; x < D; x += 256) d[x] = from_f32<TQ>(0.f);
-    if (threadIdx.x == 0 && lse) *lse = -INFINITY;
+  TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)b * a.o_b + (int64_t)hq * a.o_h + c * 4;
+  const int64_t before = p.prefix[b], after = p.prefix[b + 1], all = p.prefix[a.B];
+  const int64_t units = after - before;
+  Sum x{kNoMax, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (units > 0) {
+    const int per = a.H_kv * p.groups;
+    const int64_t total = all * per, active = active_warps(p, total);
+    const int64_t first = before * per + (h * p.groups + gi) * units;
+    const int64_t w0 = warp_of(first, active, total), w1 = warp_of(first + units - 1, active, total);
+    if (w0 == w1) return;                                  // finished where it was walked
+    // the piece of warp w: in its first slot unless the item begins inside w's range
+    const int64_t skip = first_unit(w0, active, total) == first ? 0 : 1;
+#pragma unroll 4
+    for (int64_t w = w0 + part; w <= w1; w += kParts) {
+      const int64_t at = (2 * w + (w == w0 ? skip : 0)) * p.heads + hl;
+      const float2 ml = p.ml[at];
+      add_piece(x, ml.x, ml.y, *reinterpret_cast<const float4*>(p.o + at * D + c * 4));
+    }
+  }
+#pragma unroll
+  for (int o = kLanes; o < 32; o <<= 1) add_lanes(x, o);
+  if (kHow != kWarp) {
+    if (lane < kLanes) sums[warp][lane] = x;
+    __syncthreads();
+    if (threadIdx.x >= kLanes) return;
+    for (int k = 1; k < kJoin / 32; ++k) add_piece(x, sums[k][lane].m, sums[k][lane].l, sums[k][lane].s);
+  } else if (lane >= kLanes) {
     return;
   }
-  const int per = a.H_kv * p.groups;
-  const int64_t total = p.prefix[a.B] * per, active = active_warps(p, total);
-  const int64_t first = before * per + (h * p.groups + gi) * units;
-  const int64_t w0 = warp_of(first, active, total), w1 = warp_of(first + units - 1, active, total);
-  if (w0 == w1) return;                                    // finished where it was walked
-  // the piece of warp w: in its first slot unless the item begins inside w's range
-  const int64_t skip = first_unit(w0, active, total) == first ? 0 : 1;
-  auto slot = [&](int64_t w) { return 2 * w + (w == w0 ? skip : 0); };
-  float m = kNoMax;
-  for (int64_t w = w0 + (threadIdx.x & 31); w <= w1; w += 32) m = fmaxf(m, p.ml[slot(w) * p.heads + hl].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int64_t w = w0 + part; w <= w1; w += kParts) {
-    const int64_t at = slot(w) * p.heads + hl;
-    const float2 ml = p.ml[at];
-    const float4 x = *reinterpret_cast<const float4*>(p.o + at * D + c * 4);
-    const float f = exp2f(ml.x - m);
-    l += ml.y * f;
-    s.x += x.x * f; s.y += x.y * f; s.z += x.z * f; s.w += x.w * f;
-  }
-  so[part][c] = s;
-  if (c == 0) sl[part] = l;
-  __syncthreads();
-  if (part != 0) return;
-  for (int k = 1; k < kParts; ++k) {
-    const float4 x = so[k][c];
-    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-    l += sl[k];
-  }
-  d[c * 4] = from_f32<TQ>(s.x / l);
-  d[c * 4 + 1] = from_f32<TQ>(s.y / l);
-  d[c * 4 + 2] = from_f32<TQ>(s.z / l);
-  d[c * 4 + 3] = from_f32<TQ>(s.w / l);
-  if (c == 0 && lse) *lse = (m + log2f(l)) * kLn2;
+  const bool none = units == 0;
+  d[0] = from_f32<TQ>(none ? 0.f : x.s.x / x.l);
+  d[1] = from_f32<TQ>(none ? 0.f : x.s.y / x.l);
+  d[2] = from_f32<TQ>(none ? 0.f : x.s.z / x.l);
+  d[3] = from_f32<TQ>(none ? 0.f : x.s.w / x.l);
+  if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = none ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
 
 constexpr int kMaxWarps = 152 * 16;              // of a launch: slots of the workspace
 
-bool is_matrix(const DecodeArgs& a, bool simt) { return a.dtype == ULYSSES_BF16 && !simt; }
+// fp32 queries of one or two heads a key are SIMT work: at 1-2 flops a byte the
+// FMA pipe keeps up (30 x 10277 keys, 1 head of 128: 57 us, 70 us by the fp32
+// matrix engine), from 3 heads on it does not (4 heads: 152 and 146 us, 8
+// heads: 206 and 74 us).
+bool use_simt(const DecodeArgs& a, bool chosen) { return chosen || (a.dtype == ULYSSES_FP32 && a.G <= 2); }
 
 // query heads of a group
 int heads_of(const DecodeArgs& a, bool simt) {
-  if (is_matrix(a, simt)) return a.G <= 8 ? a.G : (a.G <= 16 ? a.G : 16);
+  const int most = a.dtype == ULYSSES_BF16 ? 16 : 8;
+  if (!use_simt(a, simt)) return a.G < most ? a.G : most;
   return a.G < 4 ? (a.G < 2 ? 1 : 2) : 4;
 }
 
 // CTAs of a cluster for each item, or 0: split the keys over the whole launch.
-// A cluster pays while its warps stay short of units: at most kClusterUnits
-// each when the table is full, and all clusters resident at once.
-constexpr int kClusterUnits = 4;
+// A cluster saves the join and its launch, but waits for the longest item: it
+// pays while its warps have at most kClusterUnits units when the table is full
+// and all clusters are resident at once (8 kv heads of 4: 1 x 777 keys 7.2 us
+// by clusters, 10.0 split; 1 x 6000 13.1 and 20.2; 16 x 4000 ragged 32.7 and
+// 20.8, 4 x 16000 ragged 36.9 and 29.9, which twice as many would take).
+constexpr int kClusterUnits = 16;
 int cluster_of(const DecodeArgs& a, int heads) {
   const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
   const int64_t units = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit;
@@ -1003,16 +1259,23 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     count_launch();
     int rc = check_launch("attn_decode");
     if (rc) return rc;
+    const int rows = x.B * a.H_q;
+    // 1 x 48000 keys (32 rows): 38.9 us by parts, 45.0 by rows, 106 by warps; 16 x 4000 (512 rows): 52.9, 45.9,
+    // 49.8; 95 ragged of up to 8096, D = 64 (3040 rows): 89.9, 77.3, 68.8
+    const Join how = rows <= 256 ? kPart : (rows <= 152 * 16 ? kRow : kWarp);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(x.B * a.H_q));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(how == kPart ? rows * (D / 32) : (how == kRow ? rows : (rows + kJoin / 32 - 1) / (kJoin / 32))));
+    cfg.blockDim = dim3(kJoin);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_join_kernel<typename Engine::TQ, D>, x, p);
+    using TQ = typename Engine::TQ;
+    const cudaError_t err = how == kPart  ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kPart>, x, p)
+                            : how == kRow ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kRow>, x, p)
+                                          : cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kWarp>, x, p);
     if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode join: launch failed: %s", cudaGetErrorString(err));
     count_launch();
   }
@@ -1047,9 +1310,13 @@ size_t decode_workspace(const DecodeArgs& a) {
 
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st) {
   const bool quant = a.cache_dtype == ULYSSES_E4M3, wide = a.D == 128;
-  if (is_matrix(a, simt)) {
-    if (quant) return wide ? run_matrix<true, 128>(a, st) : run_matrix<true, 64>(a, st);
-    return wide ? run_matrix<false, 128>(a, st) : run_matrix<false, 64>(a, st);
+  if (!use_simt(a, simt)) {
+    if (a.dtype == ULYSSES_BF16) {
+      if (quant) return wide ? run_matrix<true, 128>(a, st) : run_matrix<true, 64>(a, st);
+      return wide ? run_matrix<false, 128>(a, st) : run_matrix<false, 64>(a, st);
+    }
+    if (quant) return wide ? run<SplitEngine<true, 128>, 128, 2>(a, st) : run<SplitEngine<true, 64>, 64, 3>(a, st);
+    return wide ? run<SplitEngine<false, 128>, 128, 2>(a, st) : run<SplitEngine<false, 64>, 64, 3>(a, st);
   }
   if (a.dtype == ULYSSES_BF16) {
     if (quant) return wide ? run_simt<__nv_bfloat16, uint8_t, 128>(a, st) : run_simt<__nv_bfloat16, uint8_t, 64>(a, st);

@@ -26,27 +26,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;   // tokens of one CTA
 
+// 64 bytes of loads in flight a thread, and the CTAs an SM holds of it: fewer
+// or more of either lose (a video's 17100 tokens: 65 us; one row and 5 CTAs 70,
+// four rows and 2 CTAs 81, two rows and 5 CTAs, with spills, 89; fp32 gradients
+// of 65536: 294 us; 4 CTAs 302, two rows and 2 CTAs 355).
+template <typename Tin> constexpr int kRows = sizeof(Tin) == 2 ? 2 : 1;
+template <typename Tin> constexpr int kCtas = sizeof(Tin) == 2 ? 4 : 5;
+
 template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int tb, int heads_cta) {
+__global__ void __launch_bounds__(kThreads, kCtas<Tin>) rope_kernel(const __grid_constant__ RopeArgs a, int tb, int heads_cta) {
   using namespace rows;
   __shared__ __align__(16) float cos_s[kMaxTokens * kMaxRopePairs];
   __shared__ __align__(16) float sin_s[kMaxTokens * kMaxRopePairs];
   const int64_t n0 = (int64_t)blockIdx.x * tb;
   const int tokens = (int)(a.N - n0 < tb ? a.N - n0 : tb);
   const int half = a.half;
-  // a thread forms one pair's angles, for every fourth token
-  if (const int p = threadIdx.x % kMaxRopePairs; p < half) {
-    const uint64_t freq = a.freq[p];
-    const int32_t* pos = a.pos + (int64_t)a.axis[p] * a.N + n0;
-    for (int t = threadIdx.x / kMaxRopePairs; t < tokens; t += kThreads / kMaxRopePairs) {
-      const uint64_t turn = (uint64_t)(int64_t)__ldg(pos + t) * freq;
-      float s, c;
-      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // half turns: * 2^-31
-      cos_s[t * half + p] = c;
-      sin_s[t * half + p] = a.inverse ? -s : s;
-    }
-  }
-  __syncthreads();
   const int h0 = blockIdx.y * heads_cta;
   const int hn = a.heads - h0 < heads_cta ? a.heads - h0 : heads_cta;
   const int chunks = a.D / 16, c = threadIdx.x % chunks;
@@ -54,42 +48,64 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // the two words of this thread: 8 pairs, or 16 elements that are copied
   const int oa = (turned && a.pairs == ULYSSES_PAIRS_HALF) ? 8 * c : 16 * c;
   const int ob = (turned && a.pairs == ULYSSES_PAIRS_HALF) ? half + 8 * c : 16 * c + 8;
-  // rows that lie together in memory are neighbours; kRows of them are loaded
-  // before the first is turned (64 bytes a thread in flight)
+  // rows that lie together in memory are neighbours
   const int ni = a.heads_fast ? hn : tokens, no = a.heads_fast ? tokens : hn;
   RowWalk walk(threadIdx.x / chunks, kThreads / chunks, ni);
-  constexpr int kRows = sizeof(Tin) == 2 ? 2 : 1;
-  while (walk.o < no) {
-    Row8<Tin> wa[kRows], wb[kRows];
-    Tout* dst[kRows];
-    int tok[kRows];
+  constexpr int R = kRows<Tin>;
+  Row8<Tin> wa[R], wb[R];
+  Tout* dst[R];
+  int tok[R];
+  auto load = [&]() {
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < R; ++u) {
       dst[u] = nullptr;
-      if (walk.o < no) {
-        const int t = a.heads_fast ? walk.o : walk.i, h = h0 + (a.heads_fast ? walk.i : walk.o);
-        int j = 0;
+      if (walk.o >= no) continue;
+      const int t = a.heads_fast ? walk.o : walk.i, h = h0 + (a.heads_fast ? walk.i : walk.o);
+      int j = 0;
 #pragma unroll
-        for (int k = 1; k < kMaxRopeItems; ++k)
-          if (k < a.njobs && h >= a.job[k].head0) j = k;
-        const RopeJob& jb = a.job[j];
-        const int64_t n = n0 + t;
-        // one division of 64 bits only where there is more than one batch entry
-        const int64_t b = a.S == a.N ? 0 : n / a.S, s = n - b * a.S;
-        const int64_t si = b * jb.src_b + s * jb.src_s + (int64_t)(h - jb.head0) * jb.src_h;
-        const int64_t di = b * jb.dst_b + s * jb.dst_s + (int64_t)(h - jb.head0) * jb.dst_h;
-        if (in_bounds(si + ob + 7, jb.src_n) && in_bounds(di + ob + 7, jb.dst_n)) {
-          const Tin* src = reinterpret_cast<const Tin*>(jb.src) + si;
-          wa[u].load(src + oa);
-          wb[u].load(src + ob);
-          dst[u] = reinterpret_cast<Tout*>(jb.dst) + di;
-          tok[u] = t;
-        }
-        walk.next();
+      for (int k = 1; k < kMaxRopeItems; ++k)
+        if (k < a.njobs && h >= a.job[k].head0) j = k;
+      const RopeJob& jb = a.job[j];
+      const int64_t n = n0 + t;
+      // one division of 64 bits only where there is more than one batch entry
+      const int64_t b = a.S == a.N ? 0 : n / a.S, s = n - b * a.S;
+      const int64_t si = b * jb.src_b + s * jb.src_s + (int64_t)(h - jb.head0) * jb.src_h;
+      const int64_t di = b * jb.dst_b + s * jb.dst_s + (int64_t)(h - jb.head0) * jb.dst_h;
+      if (in_bounds(si + ob + 7, jb.src_n) && in_bounds(di + ob + 7, jb.dst_n)) {
+        const Tin* src = reinterpret_cast<const Tin*>(jb.src) + si;
+        wa[u].load(src + oa);
+        wb[u].load(src + ob);
+        dst[u] = reinterpret_cast<Tout*>(jb.dst) + di;
+        tok[u] = t;
       }
+      walk.next();
     }
+  };
+  // fp32: the first rows are on their way while the angles are formed (302 ->
+  // 291 us); bf16 has no registers left for that (61 us, 66 with spills)
+  constexpr bool kAhead = sizeof(Tin) == 4;
+  bool more = false;
+  if (kAhead) {
+    more = walk.o < no;
+    load();
+  }
+  // a thread forms one pair's angles, for every fourth token
+  if (const int p = threadIdx.x % kMaxRopePairs; p < half) {
+    const uint64_t freq = a.freq[p];
+    const int32_t* pos = a.pos + (int64_t)a.axis[p] * a.N + n0;
+    for (int t = threadIdx.x / kMaxRopePairs; t < tokens; t += kThreads / kMaxRopePairs) {
+      const uint64_t turn = (uint64_t)(int64_t)__ldg(pos + t) * freq;
+      float s, co;
+      sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &co);   // half turns: * 2^-31
+      cos_s[t * half + p] = co;
+      sin_s[t * half + p] = a.inverse ? -s : s;
+    }
+  }
+  __syncthreads();
+  while (kAhead ? more : walk.o < no) {
+    if (!kAhead) load();
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < R; ++u) {
       if (dst[u] == nullptr) continue;
       float x[16];
       wa[u].get(x);
@@ -120,6 +136,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       ya.store(dst[u] + oa);
       yb.store(dst[u] + ob);
     }
+    if (kAhead) {
+      more = walk.o < no;
+      load();
+    }
   }
 }
 
@@ -129,10 +149,11 @@ int launch_rope(const RopeArgs& a, cudaStream_t st) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // tokens of a CTA: enough that each thread moves about four rows, few enough
-  // that the last wave is short (64 tokens' worth of waves cost 10% at 17100)
+  // tokens of a CTA: 256 bytes a thread, so that the angles' latency is small
+  // beside them, and no more, so that the last wave is short
+  const int need = (a.dtype == ULYSSES_BF16 ? 8 : 4) * kThreads;
   int tb = 1;
-  while (tb < kMaxTokens && tb * a.heads * (a.D / 16) < 4 * kThreads) tb *= 2;
+  while (tb < kMaxTokens && (int64_t)tb * a.heads * (a.D / 16) < need) tb *= 2;
   while (tb > 1 && (a.N + tb - 1) / tb < 4 * sms) tb /= 2;
   const int64_t gx = (a.N + tb - 1) / tb;
   // few tokens: split the heads too, down to 8 heads (one round of the CTA's threads or two)

@@ -7,7 +7,9 @@ weight by p_j (2 max ds + 8 e) with exp2f's 2 ulp; the sums over n keys round
 n times: |do| <= (2 max ds + (n + 16) e + u) sum_j p_j |v_j|, plus half a step
 of the output's type.  u is the rounding of the weights where the kernel feeds
 them to the matrix pipe in 16 bits (bf16 2^-8 with a bf16 cache, f16 2^-11
-with an e4m3 cache), and 0 in fp32.  With an e4m3 cache the weights carry V's
+with an e4m3 cache); in fp32 the operands are pairs of 11-bit parts, 2^-22
+each, so u = 2^-21 and scores are off by 2^-21 scale sum |q_d k_jd| more; the
+SIMT kernels have u = 0.  With an e4m3 cache the weights carry V's
 scale, so f16's smallest step (2^-25 of the largest weighted scale) adds
 n 448 2^-25 max_j(p_j scale_j), and q, scaled by a power of two into f16,
 2^-25 max|q| in each element of it.  LSE: max ds + (n + 16) e + e |lse|."""
@@ -80,6 +82,17 @@ def build(lens, Hq, Hkv, D, page, dtype, cache, layout, seed=0, gain=1.0, slack=
                 layout=layout), rows
 
 
+def widen(args, positions=1 << 20):
+    """The same call with a table of room for many more positions: its unused
+    entries are never read, and the keys are split over the whole launch
+    instead of a cluster for each item."""
+    tab = args["page_table"]
+    wide = torch.full((tab.shape[0], max(tab.shape[1], positions // args["k_cache"].shape[2])), -5, dtype=torch.int32,
+                      device="cuda")
+    wide[:, :tab.shape[1]] = tab
+    return {**args, "page_table": wide}
+
+
 def check(o, lse, rows, dtype, cache, layout, scale=None, simt=False):
     o = f64(o)
     o = o if layout == "seq" else o.transpose(1, 0, 2)
@@ -95,12 +108,13 @@ def check(o, lse, rows, dtype, cache, layout, scale=None, simt=False):
         mma = dtype == "bf16" and not simt
         for h in range(Hq):
             K, V = k[:, h // G], v[:, h // G]
-            ds = sc * (D + 4) * E * (np.abs(K) @ np.abs(q[h])).max()
+            split = dtype == "fp32" and not simt
+            ds = sc * ((D + 4) * E + (2.0 ** -21 if split else 0.0)) * (np.abs(K) @ np.abs(q[h])).max()
             if mma and cache == "e4m3":
                 ds += sc * 2.0 ** -25 * np.abs(q[h]).max() * np.abs(K).sum(-1).max()
             s = sc * (K @ q[h])
             p = np.exp(s - rl[h])
-            u = (2.0 ** -11 if cache == "e4m3" else 2.0 ** -8) if mma else 0.0
+            u = (2.0 ** -11 if cache == "e4m3" else 2.0 ** -8) if mma else 2.0 ** -21 if split else 0.0
             lim = (2 * ds + (n + 16) * E + u) * (p @ np.abs(V))
             if mma and cache == "e4m3":
                 lim = lim + n * 2.0 ** -25 * (p * np.abs(V).max(-1)).max()
@@ -132,6 +146,11 @@ CASES = [
     ([4097, 1, 2500], 8, 2, 128, 64, "bf16", "bf16", "head"),
     ([20001], 2, 1, 64, 16, "bf16", "bf16", "seq"),
     ([20001], 4, 1, 128, 32, "bf16", "e4m3", "seq"),
+    ([4001, 0, 3, 2048], 20, 2, 128, 32, "fp32", "fp32", "head"),
+    ([4001, 0, 3, 2048], 9, 1, 64, 16, "fp32", "e4m3", "seq"),
+    ([15, 16, 17, 23, 24, 25], 8, 1, 128, 48, "fp32", "fp32", "seq"),
+    ([15, 16, 17, 23, 24, 25], 1, 1, 128, 16, "fp32", "e4m3", "seq"),
+    ([3000, 2999], 24, 2, 128, 16, "bf16", "e4m3", "seq"),
     ([3] * 70 + [0] * 3 + [129] * 9, 4, 2, 64, 16, "bf16", "bf16", "seq"),
 ]
 
@@ -145,18 +164,28 @@ def test_against_the_definition(lens, Hq, Hkv, D, page, dtype, cache, layout):
     check(o, lse, rows, dtype, cache, layout)
     o2, lse2 = U.attn_decode(**args)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)          # no order of the GPU's in it
+    args = widen(args)
+    assert U.attn_decode_workspace(args["q"], args["k_cache"], args["page_table"], layout=layout).numel() > 0
+    o, lse = U.attn_decode(**args)
+    U.check()
+    check(o, lse, rows, dtype, cache, layout)
+    o2, lse2 = U.attn_decode(**args)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3")])
-def test_simt_kernels(dtype, cache):
-    args, rows = build([0, 1, 40, 333], 12, 2, 128, 16, dtype, cache, "head")
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32"), ("fp32", "e4m3")])
+@pytest.mark.parametrize("Hq,D,lens", [(12, 128, [0, 1, 40, 333]), (6, 64, [17, 2500]), (2, 128, [130])])
+def test_simt_kernels(dtype, cache, Hq, D, lens):
+    args, rows = build(lens, Hq, 2, D, 16, dtype, cache, "head")
     U.set_kernel(U.KERNEL_SIMT)
     try:
         o, lse = U.attn_decode(**args)
+        o2, lse2 = U.attn_decode(**widen(args))
         U.check()
     finally:
         U.set_kernel(U.KERNEL_AUTO)
     check(o, lse, rows, dtype, cache, "head", simt=True)
+    check(o2, lse2, rows, dtype, cache, "head", simt=True)
 
 
 @pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32")])
@@ -179,9 +208,10 @@ def test_running_maximum(dtype, cache, order):
         if cache == "e4m3":
             r = r * so.cache_rows(f64(args["k_scale"])[..., None], tab, b, n)
         new.append((rows[b][0], r, rows[b][2]))
-    o, lse = U.attn_decode(**args)
-    U.check()
-    check(o, lse, new, dtype, cache, "seq")
+    for x in (args, widen(args)):
+        o, lse = U.attn_decode(**x)
+        U.check()
+        check(o, lse, new, dtype, cache, "seq")
 
 
 @pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32")])
@@ -191,9 +221,11 @@ def test_scale_out_lse_workspace_and_strides(dtype, cache):
     wide[:, :8] = args["q"]
     out = torch.full((3, 9, 64), 9.0, dtype=DT[dtype], device="cuda")
     lse = torch.empty((3, 8), device="cuda")
+    args = widen(args)
     ws = U.attn_decode_workspace(wide[:, :8], args["k_cache"], args["page_table"])
+    assert ws.numel() > 0
     args["q"] = wide[:, :8]
-    o, l2 = U.attn_decode(**args, scale=0.03, out=out[:, :8], lse=lse, workspace=ws if ws.numel() else None)
+    o, l2 = U.attn_decode(**args, scale=0.03, out=out[:, :8], lse=lse, workspace=ws)
     U.check()
     assert o.data_ptr() == out.data_ptr() and l2 is lse and bool((out[:, 8] == 9.0).all())
     check(o, lse, rows, dtype, cache, "seq", scale=0.03)
@@ -210,14 +242,15 @@ def test_not_finite_values_where_they_count():
     args["k_cache"][pg, 1, sl, :] = 0
     args["k_cache"][pg, 1, sl, 0] = float("-inf")
     args["q"][2, 2:, 0] = 1.0                        # heads 2, 3: -inf
-    o, lse = U.attn_decode(**args)
-    U.check()
-    bad = torch.isnan(o)
-    assert bool(bad[1, :2, 3].all()) and int(bad.sum()) == 2
     q2, k2, v2 = rows[2]
     q2 = f64(args["q"][2])
     ro, rl = so.decode(q2, k2[1:], v2[1:])           # as if the key were not there
-    assert np.max(np.abs(f64(o[2, 2:]) - ro[2:])) <= 0.05 and np.max(np.abs(f64(lse[2, 2:]) - rl[2:])) <= 1e-4
+    for x in (args, widen(args)):
+        o, lse = U.attn_decode(**x)
+        U.check()
+        bad = torch.isnan(o)
+        assert bool(bad[1, :2, 3].all()) and int(bad.sum()) == 2
+        assert np.max(np.abs(f64(o[2, 2:]) - ro[2:])) <= 0.05 and np.max(np.abs(f64(lse[2, 2:]) - rl[2:])) <= 1e-4
 
 
 @pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp32", "fp32")])
@@ -244,18 +277,22 @@ def test_bad_pages_and_lengths_are_reported(dtype, cache):
     U.check()
 
 
-def test_other_streams_and_captured_graphs():
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_other_streams_and_captured_graphs(how):
     """One call on a stream of its own, and a captured one replayed with new
     lengths, queries and pages in the same tensors; two graphs with one
     workspace, replayed in turn."""
-    a, ra = build([600, 30], 8, 2, 128, 16, "bf16", "bf16", "seq", seed=7)
-    b, rb = build([17, 601], 8, 2, 128, 16, "bf16", "bf16", "seq", seed=8)
+    a, ra = build([6000, 30], 8, 2, 128, 16, "bf16", "bf16", "seq", seed=7)
+    b, rb = build([17, 6000], 8, 2, 128, 16, "bf16", "bf16", "seq", seed=8)
+    if how == "split":
+        a, b = widen(a), widen(b)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     o, lse = U.attn_decode(**a, stream=st)
     st.synchronize()
     check(o, lse, ra, "bf16", "bf16", "seq")
     ws = U.attn_decode_workspace(a["q"], a["k_cache"], a["page_table"])
+    assert (ws.numel() > 0) == (how == "split")
     kw = dict(workspace=ws) if ws.numel() else {}
     graphs, outs = [], []
     for args in (a, b):
