@@ -837,13 +837,16 @@ struct SimtEngine {
   __device__ __forceinline__ void run(const DecodeArgs& a, const Piece& p) {
     const int64_t total = a.num_pages * a.H_kv * a.page;
     Walk walk(a, p);
+    constexpr int kAtOnce = HG * E <= 16 && sizeof(LaneRow<TC, D>) <= 32 ? 4 : 2;   // keys of a lane group whose rows load together
+    int pg = walk.fetch();
     for (int u = 0; u < p.units; ++u) {
-      const int n = walk.unit(walk.fetch());
+      const int n = walk.unit(pg);
       const int64_t row0 = (int64_t)n * kUnit;
       walk.next();
+      pg = walk.fetch();
       if (n < 0 || !in_bounds(row0 + kUnit - 1, total)) continue;
       const int left = p.len - (p.unit0 + u) * kUnit;
-#pragma unroll 2
+#pragma unroll kAtOnce
       for (int k = grp; k < kUnit; k += 4) {
         const bool live = k < left;
         const int64_t row = row0 + k;

@@ -567,9 +567,16 @@ def _rows(t, layout, what):
 
 
 def _rows3(t, layout, what):
-    if t.dim() != 3:
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3:
         raise ValueError(f"{what} must have three dimensions")
-    return _rows(t, layout, what)
+    if st[2] != 1 and t.numel():
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if layout == "head":
+        return st[1], st[0], sh[1], sh[0], sh[2]
+    if layout == "seq":
+        return st[0], st[1], sh[0], sh[1], sh[2]
+    raise ValueError(f"unknown layout {layout!r}")
 
 
 def _launch(fn, idx, stream, tensors, args):
@@ -620,48 +627,66 @@ def _rope(fn, q, k, positions, inv_freq, axes, layout, pairs, dtype, out, stream
     first = given[0]
     if first is None:
         raise ValueError("rope: no tensor given")
-    if out is None:
-        out = (None,) * len(given)
-    else:
+    if out is not None:
         out = tuple(out) if isinstance(out, (tuple, list)) else (out,)
         if len(out) != len(given):
             raise ValueError("rope: one output for each tensor")
-    idx = _device_of((*given, positions, *out))
-    din, dims = first.dtype, first.dim()
+    idx = _device_of((*given, positions) if out is None else (*given, positions, *out))
+    din = first.dtype
     dout = din if dtype is None else dtype
-    if dims not in (3, 4):
-        raise ValueError("rope: tensors have three or four dimensions")
-    items, results, S, B, D = b"", [], None, 1, 0
-    for t, o in zip(given, out):
-        ss, sh, n, H, d = _rows(t, layout, "rope input")
-        nb, sb = (t.shape[0], t.stride(0)) if dims == 4 else (1, 0)
-        if S is None:
-            S, B, D = n, nb, d
-        elif n != S or nb != B or d != D or t.dtype is not din or t.dim() != dims:
+    code_in, code_out = _code(din, "rope"), _code(dout, "rope")
+    head = layout == "head"
+    if not head and layout != "seq":
+        raise ValueError(f"unknown layout {layout!r}")
+    items, results, tokens = b"", [], None
+    for i, t in enumerate(given):
+        sh, st = t.shape, t.stride()
+        if len(sh) == 3:
+            B, sb = 1, 0
+            n, H, D = sh if not head else (sh[1], sh[0], sh[2])
+            ss, sn, sd = st if not head else (st[1], st[0], st[2])
+        elif len(sh) == 4:
+            B, n, H, D = sh if not head else (sh[0], sh[2], sh[1], sh[3])
+            sb, ss, sn, sd = st if not head else (st[0], st[2], st[1], st[3])
+        else:
+            raise ValueError("rope: tensors have three or four dimensions")
+        if sd != 1 and t.numel():
+            raise ValueError("rope input: the last dimension must be contiguous")
+        if tokens is None:
+            tokens = (len(sh), B, n, D)
+        elif tokens != (len(sh), B, n, D) or t.dtype is not din:
             raise ValueError("rope: tensors of one call share their tokens, D and dtype")
-        if o is None:
-            o = _empty(t, t.shape, dout, stream)
-        elif o.shape != t.shape or o.dtype is not dout:
-            raise ValueError("rope: an output must have its input's shape and the call's dtype")
-        os_, oh, _, _, _ = _rows(o, layout, "rope output")
-        items += _PACK_ITEM(t.data_ptr(), o.data_ptr(), H, sb, ss, sh, o.stride(0) if dims == 4 else 0, os_, oh)
+        if out is None:
+            o = _empty(t, sh, dout, stream)
+            os_, on = (D, n * D) if head else (H * D, D)
+            ob = n * H * D
+        else:
+            o = out[i]
+            if o.shape != sh or o.dtype is not dout:
+                raise ValueError("rope: an output must have its input's shape and the call's dtype")
+            os_, on, _, _, _ = _rows(o, layout, "rope output")
+            ob = o.stride(0) if len(sh) == 4 else 0
+        items += _PACK_ITEM(t.data_ptr(), o.data_ptr(), H, sb, ss, sn, ob, os_, on)
         results.append(o)
-    n_axes, rest = (1, positions.shape) if positions.dim() == dims - 2 else (positions.shape[0], positions.shape[1:])
-    if tuple(rest) != ((B, S) if dims == 4 else (S,)):
+    dims, B, S, D = tokens
+    psh = positions.shape
+    n_axes, psh = (1, psh) if len(psh) == dims - 2 else (psh[0], psh[1:])
+    if psh != ((S,) if dims == 3 else (B, S)):
         raise ValueError(f"rope: positions {tuple(positions.shape)} do not match {B} x {S} tokens")
     half = inv_freq.numel()
     if inv_freq.dtype is not _F64 or inv_freq.is_cuda or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 tensor in host memory")
-    if axes is not None and (axes.dtype is not _I32 or axes.is_cuda or not axes.is_contiguous()
-                             or axes.numel() != half):
-        raise ValueError("axes must be a contiguous int32 tensor in host memory, one entry for each frequency")
+    ax = None
+    if axes is not None:
+        if axes.dtype is not _I32 or axes.is_cuda or not axes.is_contiguous() or axes.numel() != half:
+            raise ValueError("axes must be a contiguous int32 tensor in host memory, one entry for each frequency")
+        ax = axes.data_ptr()
     if pairs not in _PAIRS:
         raise ValueError(f"unknown pair order {pairs!r}")
     _launch(fn, idx, stream, (*given, positions, *results),
-            (items, len(given), _flat(positions, _I32, "positions"), n_axes, inv_freq.data_ptr(),
-             None if axes is None else axes.data_ptr(), 2 * half, _PAIRS[pairs], S, B, D, _code(din, "rope"),
-             _code(dout, "rope")))
-    return results[0] if len(results) == 1 else tuple(results)
+            (items, len(given), _flat(positions, _I32, "positions"), n_axes, inv_freq.data_ptr(), ax, 2 * half,
+             _PAIRS[pairs], S, B, D, code_in, code_out))
+    return results[0] if k is None or q is None else (results[0], results[1])
 
 
 def rope_fwd(q, k, positions, inv_freq, axes=None, layout="seq", pairs="half", out=None, stream=None):
@@ -776,17 +801,20 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=
         if first.numel() != B:
             raise ValueError("first must have B entries")
         at = _flat(first, _I32, "first")
+    if layout != "seq" and layout != "head":
+        raise ValueError(f"unknown layout {layout!r}")
     shape = (T, H, D) if layout == "seq" else (H, T, D)
     idx = _device_of((k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first, *(out or ())))
     if out is None:
         k, v = _empty(k_cache, shape, dtype, stream), _empty(k_cache, shape, dtype, stream)
+        ks, kh = vs, vh = (H * D, D) if layout == "seq" else (D, T * D)
     else:
         k, v = out
         if k.shape != shape or v.shape != shape or k.dtype is not dtype or v.dtype is not dtype:
             raise ValueError(f"cache_read: outputs must be {shape} of {dtype}")
+        ks, kh, _, _, _ = _rows3(k, layout, "k")
+        vs, vh, _, _, _ = _rows3(v, layout, "v")
     tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first)
-    ks, kh, _, _, _ = _rows3(k, layout, "k")
-    vs, vh, _, _, _ = _rows3(v, layout, "v")
     _launch(lib().ulysses_cache_read, idx, stream, tensors,
             (pk, pv, pks, pvs, tab, cols, _flat(cu_seqlens, _I32, "cu_seqlens"), at, k.data_ptr(), v.data_ptr(), ks, kh,
              vs, vh, T, B, n_pages, page, H, D, _code(dtype, "k"), _code(held, "k_cache")))
@@ -829,13 +857,18 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     dq, dc = _code(dt, "q"), _code(k_cache.dtype, "k_cache")
     if out is None:
         out = _empty(q, q.shape, dt, stream)
+        ob, oh = (H_q * D, D) if layout == "seq" else (D, B * D)
     elif out.shape != q.shape or out.dtype is not dt:
         raise ValueError("attn_decode: out must have q's shape and dtype")
-    ob, oh, _, _, _ = _rows3(out, layout, "out")
+    else:
+        ob, oh, _, _, _ = _rows3(out, layout, "out")
     if lse is None:
         lse = _empty(q, (B, H_q), _F32, stream)
+        pl = lse.data_ptr()
     elif lse.shape != (B, H_q):
         raise ValueError("attn_decode: lse must be [B, H_q]")
+    else:
+        pl = _flat(lse, _F32, "lse")
     if workspace is None:
         n = _decode_bytes(B, H_q, H_kv, D, cols, page, dq, dc)
         if n:
@@ -844,5 +877,5 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     _launch(lib().ulysses_attn_decode, idx, stream,
             (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse),
             (q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, _I32, "seq_lens"), out.data_ptr(), ob, oh,
-             _flat(lse, _F32, "lse"), B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n))
+             pl, B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n))
     return out, lse
