@@ -24,7 +24,8 @@ ULYSSES_ERROR_READER(read_error_rope)
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;   // tokens of one CTA
+constexpr int kMaxTokens = 64;     // of a CTA
+constexpr int kMaxAngles = 2048;   // tokens x pairs of a CTA
 
 // 64 bytes of loads in flight a thread, and the CTAs an SM holds of it: fewer
 // or more of either lose (a video's 17100 tokens: 65 us; one row and 5 CTAs 70,
@@ -36,8 +37,8 @@ template <typename Tin> constexpr int kCtas = sizeof(Tin) == 2 ? 4 : 5;
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(kThreads, kCtas<Tin>) rope_kernel(const __grid_constant__ RopeArgs a, int tb, int heads_cta) {
   using namespace rows;
-  __shared__ __align__(16) float cos_s[kMaxTokens * kMaxRopePairs];
-  __shared__ __align__(16) float sin_s[kMaxTokens * kMaxRopePairs];
+  __shared__ __align__(16) float cos_s[kMaxAngles];
+  __shared__ __align__(16) float sin_s[kMaxAngles];
   const int64_t n0 = (int64_t)blockIdx.x * tb;
   const int tokens = (int)(a.N - n0 < tb ? a.N - n0 : tb);
   const int half = a.half;
@@ -153,7 +154,7 @@ int launch_rope(const RopeArgs& a, cudaStream_t st) {
   // beside them, and no more, so that the last wave is short
   const int need = (a.dtype == ULYSSES_BF16 ? 8 : 4) * kThreads;
   int tb = 1;
-  while (tb < kMaxTokens && (int64_t)tb * a.heads * (a.D / 16) < need) tb *= 2;
+  while (tb < kMaxTokens && 2 * tb * a.half <= kMaxAngles && (int64_t)tb * a.heads * (a.D / 16) < need) tb *= 2;
   while (tb > 1 && (a.N + tb - 1) / tb < 4 * sms) tb /= 2;
   const int64_t gx = (a.N + tb - 1) / tb;
   // few tokens: split the heads too, down to 8 heads (one round of the CTA's threads or two)

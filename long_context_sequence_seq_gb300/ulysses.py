@@ -597,10 +597,14 @@ def _launch(fn, idx, stream, tensors, args):
 
 
 def _empty(like, shape, dtype, stream):
+    # empty_strided: the shortest way through torch's dispatcher (a microsecond less than empty)
+    n = len(shape)
+    strides = (shape[1] * shape[2], shape[2], 1) if n == 3 else (1,) if n == 1 else (shape[1], 1) if n == 2 else \
+        (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
 
 
 # --------------------------------------------------------------- rotary positions
