@@ -29,6 +29,8 @@
 //     O^T += V^T P^T   it holds rows 2j, 2j+1, 2j+8, 2j+9, words g, g+8, ..; pairs
 //                 of rows are interleaved by byte permutes, and P turns from
 //                 S's layout to the operand's by movmatrix
+//   bf16 weights go in as a value and its rounding error (2^-16 instead of 2^-8:
+//   the output is then off by its own rounding alone, and the pipe has room).
 //   E4m3 codes become f16 exactly.  q is scaled by a power of two into f16's
 //   range (exact, but for elements 2^-24 below its largest); the rows' scales
 //   enter in fp32: K's times the score, V's in the weight, as 2^(s + log2 vs - M)
@@ -385,13 +387,22 @@ struct MatrixEngine {
       }
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][2], pl[NT][2];                       // weights; bf16: and what their rounding left
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          pb[t][x] = transpose8x8(kQuant ? f32_to_f16x2(s[u][t][2 * x], s[u][t][2 * x + 1])
-                                         : f32_to_bf16x2(s[u][t][2 * x], s[u][t][2 * x + 1]));
+        for (int x = 0; x < 2; ++x) {
+          const float p0 = s[u][t][2 * x], p1 = s[u][t][2 * x + 1];
+          if (kQuant) {
+            pb[t][x] = transpose8x8(f32_to_f16x2(p0, p1));
+          } else {
+            const uint32_t hi = f32_to_bf16x2(p0, p1);
+            float h[2];
+            bf16x2_to_f32(hi, h);
+            pb[t][x] = transpose8x8(hi);
+            pl[t][x] = transpose8x8(f32_to_bf16x2(p0 - h[0], p1 - h[1]));
+          }
+        }
 #pragma unroll
       for (int w = 0; w < kVW; ++w)
 #pragma unroll
@@ -404,7 +415,10 @@ struct MatrixEngine {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (kQuant) mma_f16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
-            else mma_bf16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
+            else {
+              mma_bf16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
+              mma_bf16(acc[t][w * (kVE / 2) + e], f, pl[t][0], pl[t][1]);
+            }
           }
         }
     }

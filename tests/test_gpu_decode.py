@@ -6,8 +6,8 @@ a score of D products is off by ds_j = (D + 4) e scale sum |q_d k_jd|, so its
 weight by p_j (2 max ds + 8 e) with exp2f's 2 ulp; the sums over n keys round
 n times: |do| <= (2 max ds + (n + 16) e + u) sum_j p_j |v_j|, plus half a step
 of the output's type.  u is the rounding of the weights where the kernel feeds
-them to the matrix pipe in 16 bits (bf16 2^-8 with a bf16 cache, f16 2^-11
-with an e4m3 cache); in fp32 the operands are pairs of 11-bit parts, 2^-22
+them to the matrix pipe in 16 bits (with a bf16 cache as a bf16 value and the bf16
+rest, 2^-16; f16 2^-11 with an e4m3 cache); in fp32 the operands are pairs of 11-bit parts, 2^-22
 each, so u = 2^-21 and scores are off by 2^-21 scale sum |q_d k_jd| more; the
 SIMT kernels have u = 0.  With an e4m3 cache the weights carry V's
 scale, so f16's smallest step (2^-25 of the largest weighted scale) adds
@@ -114,7 +114,7 @@ def check(o, lse, rows, dtype, cache, layout, scale=None, simt=False):
                 ds += sc * 2.0 ** -25 * np.abs(q[h]).max() * np.abs(K).sum(-1).max()
             s = sc * (K @ q[h])
             p = np.exp(s - rl[h])
-            u = (2.0 ** -11 if cache == "e4m3" else 2.0 ** -8) if mma else 2.0 ** -21 if split else 0.0
+            u = (2.0 ** -11 if cache == "e4m3" else 2.0 ** -16) if mma else 2.0 ** -21 if split else 0.0
             lim = (2 * ds + (n + 16) * E + u) * (p @ np.abs(V))
             if mma and cache == "e4m3":
                 lim = lim + n * 2.0 ** -25 * (p * np.abs(V).max(-1)).max()
@@ -392,3 +392,115 @@ def test_a_decode_loop_as_it_is_used(cache):
             # the bf16 tolerances of the layer's own attention tests
             assert np.max(np.abs(f64(o[:, b]) - ro[:, -1])) <= 2e-2
             assert np.max(np.abs(f64(lse[b]) - rl[:, -1])) <= 1e-3
+
+
+def test_more_sequences_than_one_launch_takes():
+    B = 2100                                          # 2048 a launch
+    lens = [(7 * i) % 37 for i in range(B)]
+    args, rows = build(lens, 2, 1, 64, 16, "bf16", "bf16", "head", seed=11)
+    o, lse = U.attn_decode(**args)
+    U.check()
+    check(o, lse, rows, "bf16", "bf16", "head")
+
+
+@pytest.mark.parametrize("spread,gain", [(18.0, 2.0), (30.0, 60.0), (3.0, 1e-4)])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_e4m3_rows_of_very_different_scales(spread, gain, how):
+    """V's scales over 2^-spread .. 2^spread, queries from nearly uniform to
+    nearly one-hot weights: f16 weights follow the largest contribution."""
+    args, rows = build([333, 40], 6, 2, 128, 16, "bf16", "e4m3", "seq", seed=12)
+    g = torch.Generator().manual_seed(13)
+    f = torch.exp2((torch.rand(args["v_scale"].shape, generator=g) * 2 - 1) * spread).cuda()
+    args["v_scale"] *= f
+    args["q"] = (args["q"].float() * gain / 2).bfloat16()
+    tab = args["page_table"].cpu().numpy()
+    new = []
+    for b, n in enumerate((333, 40)):
+        v = so.cache_rows(f64(args["v_cache"]), tab, b, n) * so.cache_rows(f64(args["v_scale"])[..., None], tab, b, n)
+        new.append((f64(args["q"][b]), rows[b][1], v))
+    o, lse = U.attn_decode(**(widen(args) if how == "split" else args))
+    U.check()
+    check(o, lse, new, "bf16", "e4m3", "seq")
+
+
+def test_nothing_outside_outputs_and_workspace_is_written():
+    """Windows with guard bytes on both sides, in both ways of a launch."""
+    pat, guard, bufs = 0xA5, 4096, []
+
+    def window(shape, dtype):
+        n = torch.Size(shape).numel() * torch.empty((), dtype=dtype).element_size()
+        raw = torch.full((2 * guard + (n + 255) // 256 * 256,), pat, dtype=torch.uint8, device="cuda")
+        bufs.append((raw, n))
+        return raw[guard:guard + n].view(dtype).view(shape)
+
+    for dtype, cache, D, Hq in (("bf16", "bf16", 128, 24), ("bf16", "e4m3", 64, 6), ("fp32", "fp32", 64, 10),
+                                ("fp32", "fp32", 128, 2)):
+        args, rows = build([1, 0, 700, 33], Hq, 2, D, 16, dtype, cache, "head", seed=14)
+        for x in (args, widen(args)):
+            n = U.attn_decode_workspace(x["q"], x["k_cache"], x["page_table"], layout="head").numel()
+            o, lse = U.attn_decode(**x, out=window(x["q"].shape, DT[dtype]), lse=window((4, Hq), torch.float32),
+                                   workspace=window((n,), torch.uint8) if n else None)
+            U.check()
+            check(o, lse, rows, dtype, cache, "head")
+    for raw, n in bufs:
+        assert bool((raw[:guard] == pat).all()) and bool((raw[guard + n:] == pat).all())
+
+
+def test_two_calls_at_once_on_two_streams():
+    a, ra = build([5000, 100, 1], 8, 2, 128, 16, "bf16", "bf16", "seq", seed=15)
+    b, rb = build([31, 4000], 8, 2, 128, 16, "bf16", "e4m3", "seq", seed=16)
+    a, b = widen(a), widen(b)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    t.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(20):
+        got.append((U.attn_decode(**a, stream=s), U.attn_decode(**b, stream=t)))
+    torch.cuda.synchronize()
+    U.check()
+    for x, y in got:
+        assert torch.equal(x[0], got[0][0][0]) and torch.equal(y[0], got[0][1][0])
+    check(*got[0][0], ra, "bf16", "bf16", "seq")
+    check(*got[0][1], rb, "bf16", "e4m3", "seq")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_a_captured_step_replayed_with_an_empty_place(cache):
+    """Rotary positions, cache write and attention of one step in a CUDA graph;
+    the lengths grow in it, and one place of the batch is empty.  Replays equal
+    the calls one by one."""
+    Hq, Hkv, D, page, B = 8, 2, 128, 16, 4
+    inv, axes = U.rope_frequencies(D)
+    start = torch.tensor([15, 40, 0, 1], dtype=torch.int32, device="cuda")
+    used = (start > 0).to(torch.int32)
+    tab = torch.arange(B * 6, dtype=torch.int32, device="cuda").view(B, 6)
+    g = torch.Generator().manual_seed(17)
+    steps = torch.randn((5, B, Hq + 2 * Hkv, D), generator=g).bfloat16().cuda()
+
+    def fresh():
+        bufs = U.kv_cache(B * 6, page, Hkv, D, DT[cache])
+        return bufs, start.clone()
+
+    def step(x, bufs, lens):
+        q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        q, k = U.rope_fwd(q, k, lens, inv, axes)
+        lens.add_(used)
+        U.cache_write(k, v, bufs[0], bufs[1], tab, lens, k_scale=bufs[2], v_scale=bufs[3])
+        return U.attn_decode(q, bufs[0], bufs[1], tab, lens, k_scale=bufs[2], v_scale=bufs[3])
+
+    bufs, lens = fresh()
+    want = [tuple(t.clone() for t in step(x, bufs, lens)) for x in steps]
+    bufs2, lens2 = fresh()
+    x = steps[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, bufs2, lens2)
+    for i in range(5):
+        x.copy_(steps[i])
+        graph.replay()
+        assert torch.equal(out[0], want[i][0]) and torch.equal(out[1], want[i][1]), i
+        assert bool((out[0][2] == 0).all()) and bool(torch.isneginf(out[1][2]).all())
+    U.check()
+    assert torch.equal(lens, lens2)
+    for p, r in zip(bufs, bufs2):
+        assert p is None or torch.equal(p.view(torch.uint8), r.view(torch.uint8))

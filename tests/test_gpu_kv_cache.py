@@ -249,3 +249,32 @@ def test_pages_beyond_32_bit_offsets():
     for x, y in ((k, a), (v, b)):
         err = (x.float() - y.float()).abs()
         assert bool((err <= x.float().abs() * (2.0 ** -4 + 2.0 ** -8) + x.float().abs().amax(-1, keepdim=True) / 448 * 2.0 ** -10).all())
+
+
+def test_write_and_read_on_a_stream_of_their_own():
+    st = torch.cuda.Stream()
+    kc, vc, _, _ = U.kv_cache(8, 16, 2, 64)
+    k, v = normal((2, 100, 64), 8, "bf16"), normal((2, 100, 64), 9, "bf16")
+    tab = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    cu = torch.tensor([0, 100], dtype=torch.int32, device="cuda")
+    st.wait_stream(torch.cuda.current_stream())
+    U.cache_write(k, v, kc, vc, tab, cu[1:], cu_new=cu, layout="head", stream=st)
+    a, b = U.cache_read(kc, vc, tab, cu, 100, layout="head", stream=st)
+    st.synchronize()
+    assert torch.equal(a, k) and torch.equal(b, v)
+
+
+def test_many_heads_and_many_tokens_of_a_block():
+    """Blocks of the largest and of the smallest number of tokens."""
+    for T, H, D in ((40000, 1, 64), (3, 300, 128)):
+        kc, vc, ks, vs = U.kv_cache(-(-T // 64), 64, H, D, torch.float8_e4m3fn)
+        k, v = normal((T, H, D), 10, "bf16"), normal((T, H, D), 11, "bf16")
+        tab = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+        cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        U.cache_write(k, v, kc, vc, tab, cu[1:], cu_new=cu, k_scale=ks, v_scale=vs)
+        a, b = U.cache_read(kc, vc, tab, cu, T, k_scale=ks, v_scale=vs, dtype=torch.float32)
+        U.check()
+        for x, y in ((k, a), (v, b)):
+            x = x.float()
+            lim = torch.maximum(x.abs() * 2.0 ** -4, x.abs().amax(-1, keepdim=True) / 448 * 2.0 ** -10) + x.abs() * 2.0 ** -21
+            assert bool(((x - y).abs() <= lim).all())
