@@ -335,8 +335,8 @@ int ulysses_attn_bwd_noalloc(const void* q_h, const void* k_h, const void* v_h, 
  *   dtype, out_dtype  of src and dst: equal, or FP32 -> BF16 (rounded once).
  *   D in {64, 128}; rot_dim a multiple of 16, <= D; base pointers 16-byte
  *   aligned and strides multiples of 16 bytes.
- * Angles are formed as turns in 64-bit fixed point (pos * round(inv_freq /
- * (2 pi) * 2^64) mod 2^64), so far positions lose nothing. */
+ * Angles are formed as turns in 64-bit fixed point (pos * (inv_freq / (2 pi) *
+ * 2^64) mod 2^64), so far positions lose nothing. */
 enum { ULYSSES_PAIRS_HALF = 0, ULYSSES_PAIRS_ADJACENT = 1 };
 typedef struct {
   const void* src;

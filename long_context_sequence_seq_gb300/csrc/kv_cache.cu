@@ -13,7 +13,11 @@
 // with all their heads, K and V: it resolves each token's place once (sequence
 // by bisection in cu, page from the table) and streams the rows; D / 16 lanes
 // hold a row, 16 elements each, so the row's largest magnitude is a 2- or
-// 3-step shuffle.
+// 3-step shuffle.  Instruction issue is next to HBM here: 8 elements a lane
+// with a division for each row took 186 us where this takes 130 (131072 tokens
+// of 8 heads of 128, bf16 to e4m3, K and V: 814 MB, 94% of the measured copy
+// rate), so bf16 maxima are taken two at a time and one pair of divisions
+// serves four rows.  Reading 65536 such tokens back: 65 us (407 MB, 93%).
 #include "internal.h"
 #include "rows.cuh"
 
