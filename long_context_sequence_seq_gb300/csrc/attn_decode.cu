@@ -70,6 +70,7 @@ constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr float kLazy = 8.f;                    // a maximum moves when exceeded by 2^8
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                       // of a CTA
+constexpr int kMinUnits = 2;                    // of a warp, where there are enough for all
 constexpr int kMaxBatch = 2048;                 // sequences of one launch (their prefix sums sit in shared memory)
 
 // How a launch is split (host), the same for both of its kernels.
@@ -77,7 +78,6 @@ struct Plan {
   int groups;       // query-head groups of a kv head
   int heads;        // query heads of a group (the last may have fewer)
   int warps;        // of the launch
-  int min_units;    // a warp takes at least this many units
   int64_t* prefix;  // [B + 1] units before each sequence (one head); workspace
   float2* ml;       // [2 * warps][heads] (m, l); workspace
   float* o;         // [2 * warps][heads][D] sums; workspace
@@ -94,19 +94,24 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   return (int)n;
 }
 
-// Warps that share `total` units, and the first unit of each.
+// a / b of numbers that mostly fit 32 bits, where the division is several times shorter.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+// Warps that share `total` units (each at least kMinUnits), the first unit of
+// warp w, and the warp that has a unit.
 __device__ __forceinline__ int64_t active_warps(const Plan& p, int64_t total) {
-  const int64_t w = (total + p.min_units - 1) / p.min_units;
+  const int64_t w = (total + kMinUnits - 1) / kMinUnits;
   return w < p.warps ? w : p.warps;
 }
 __device__ __forceinline__ int64_t first_unit(int64_t w, int64_t active, int64_t total) {
-  // w * total / active, without leaving 64 bits
-  const int64_t each = total / active, rest = total - each * active;
+  const int64_t each = quotient(total, active), rest = total - each * active;
   return w * each + (w < rest ? w : rest);
 }
-__device__ __forceinline__ int64_t warp_of(int64_t unit, int64_t active, int64_t total) {   // the w above
-  const int64_t each = total / active, rest = total - each * active;
-  return unit < rest * (each + 1) ? unit / (each + 1) : rest + (unit - rest * (each + 1)) / each;
+__device__ __forceinline__ int64_t warp_of(int64_t unit, int64_t active, int64_t total) {
+  const int64_t each = quotient(total, active), rest = total - each * active;
+  return unit < rest * (each + 1) ? quotient(unit, each + 1) : rest + quotient(unit - rest * (each + 1), each);
 }
 
 // The piece of an item that a warp walks.
@@ -193,14 +198,14 @@ struct MatrixEngine {
 
   __device__ __forceinline__ MatrixEngine(int lane_) : lane(lane_), g(lane_ >> 2), j(lane_ & 3) {}
 
+  // q as it is; scale_q() makes it the operand, behind the first rows' loads
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Piece& p) {
+    constexpr int kE = kQuant ? 16 : 8;                    // elements of a K word
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int hl = t * 8 + g;
       const bool live = hl < p.gn;
       const TQ* qp = reinterpret_cast<const TQ*>(a.q) + (int64_t)p.b * a.q_b + (int64_t)(p.h * a.G + p.g0 + (live ? hl : 0)) * a.q_h;
-      constexpr int kE = kQuant ? 16 : 8;                  // elements of a K word
-      float big = 0.f;
 #pragma unroll
       for (int w = 0; w < kKW; ++w) {
 #pragma unroll
@@ -210,38 +215,41 @@ struct MatrixEngine {
           d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
         }
       }
-      float f = a.scale_log2;
-      if (kQuant) {
-        constexpr int kN = sizeof(q[0]) / 4;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          float e[2];
-          bf16x2_to_f32(q[t][i], e);
-          big = fmaxf(big, fmaxf(fabsf(e[0]), fabsf(e[1])));
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // the power of two below the head's largest element
-        int e = (int)(__float_as_uint(big) >> 23) - 127;
-        e = e < -100 ? -100 : (e > 126 ? 126 : e);
-        const float down = __int_as_float((127 - e) << 23);
-        f *= __int_as_float((127 + e) << 23);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          float x[2];
-          bf16x2_to_f32(q[t][i], x);
-          q[t][i] = f32_to_f16x2(x[0] * down, x[1] * down);
-        }
-      }
-      // from head g's lanes to those that hold the scores of heads 2j, 2j + 1
-      sc[t][0] = __shfl_sync(0xffffffffu, f, 8 * j);
-      sc[t][1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) { m[t][c] = kNoMax; l[t][c] = 0.f; mw[t][c] = kNoMax; }
+      for (int c = 0; c < 2; ++c) { m[t][c] = kNoMax; l[t][c] = 0.f; mw[t][c] = kNoMax; sc[t][c] = a.scale_log2; }
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[t][i][c] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void scale_q() {
+    if (!kQuant) return;
+    constexpr int kN = sizeof(q[0]) / 4;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        float e[2];
+        bf16x2_to_f32(q[t][i], e);
+        big = fmaxf(big, fmaxf(fabsf(e[0]), fabsf(e[1])));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // the power of two below the head's largest element
+      int e = (int)(__float_as_uint(big) >> 23) - 127;
+      e = e < -100 ? -100 : (e > 126 ? 126 : e);
+      const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        float x[2];
+        bf16x2_to_f32(q[t][i], x);
+        q[t][i] = f32_to_f16x2(x[0] * down, x[1] * down);
+      }
+      // from head g's lanes to those that hold the scores of heads 2j, 2j + 1
+      sc[t][0] *= __shfl_sync(0xffffffffu, up, 8 * j);
+      sc[t][1] *= __shfl_sync(0xffffffffu, up, 8 * j + 4);
     }
   }
 
@@ -473,6 +481,7 @@ struct MatrixEngine {
     Next now{*this, a, unit, keys};
     now.load_k(r);
     now.load_v(r);
+    scale_q();
     while (left > 0) {
       left -= kSub * kUnit;
       places(left, nkeys);
@@ -598,7 +607,7 @@ struct SplitEngine {
     for (int i = 0; i < kKE / 2; ++i)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
-        split_tf32(live ? qp[k_index(2 * i + x, j)] * a.scale_log2 : 0.f, q[i][2 * x], q[i][2 * x + 1]);
+        q[i][2 * x] = __float_as_uint(live ? qp[k_index(2 * i + x, j)] : 0.f);   // split behind the first rows' loads
 #pragma unroll
     for (int i = 0; i < kVE; ++i)
 #pragma unroll
@@ -671,6 +680,10 @@ struct SplitEngine {
     place();
     load_k(a, r, row, keys);
     load_v(a, r, row, keys);
+#pragma unroll
+    for (int i = 0; i < kKE / 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) split_tf32(__uint_as_float(q[i][2 * x]) * a.scale_log2, q[i][2 * x], q[i][2 * x + 1]);
     for (int at = 0; at < left; at += kHalf) {
       const int mine = min(keys, kHalf);
       float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -859,7 +872,7 @@ struct SimtEngine {
                      (int64_t)(p.h * a.G + p.g0 + (g < p.gn ? g : 0)) * a.q_h;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        q[g][e] = to_f32<TQ>(qp[LaneRow<TC, D>::element(e, i)]) * a.scale_log2;
+        q[g][e] = to_f32<TQ>(qp[LaneRow<TC, D>::element(e, i)]);
         acc[g][e] = 0.f;
       }
     }
@@ -904,7 +917,7 @@ struct SimtEngine {
         vr.get(f);
 #pragma unroll
         for (int g = 0; g < HG; ++g) {
-          float t = kQuant ? s[g] * ks : s[g];
+          float t = s[g] * (kQuant ? a.scale_log2 * ks : a.scale_log2);
           t = live ? t : -INFINITY;
           if (t > m[g] + kLazy) {
             const float w = exp2f(m[g] - t);
@@ -1035,7 +1048,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
   while (at < end) {
     while (prefix[b + 1] * per <= at) ++b;
     const int64_t units = prefix[b + 1] - prefix[b], in_seq = at - prefix[b] * per;
-    const int item = (int)(in_seq / units);
+    const int item = (int)quotient(in_seq, units);
     const int64_t item0 = prefix[b] * per + item * units;  // the item's first unit
     Piece pc;
     pc.b = b;
@@ -1149,9 +1162,8 @@ __device__ __forceinline__ void add_lanes(Sum& x, int o) {   // with lane ^ o, i
 // sequence without keys.  kPart: a CTA for 32 of the head's values, 32 pieces
 // at a time (few items, hundreds of pieces each); kRow: a CTA for the head;
 // kWarp: a warp for it (many items, of a few pieces or none).
-constexpr int kJoin = 256;
 enum Join { kPart, kRow, kWarp };
-template <typename TQ, int D, Join kHow>
+template <typename TQ, int D, Join kHow, int kJoin>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constant__ DecodeArgs a,
                                                             const __grid_constant__ Plan p) {
   constexpr int kLanes = kHow == kPart ? 8 : D / 4;                // threads across the values, four each
@@ -1177,11 +1189,34 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
     if (w0 == w1) return;                                  // finished where it was walked
     // the piece of warp w: in its first slot unless the item begins inside w's range
     const int64_t skip = first_unit(w0, active, total) == first ? 0 : 1;
-#pragma unroll 4
-    for (int64_t w = w0 + part; w <= w1; w += kParts) {
-      const int64_t at = (2 * w + (w == w0 ? skip : 0)) * p.heads + hl;
-      const float2 ml = p.ml[at];
-      add_piece(x, ml.x, ml.y, *reinterpret_cast<const float4*>(p.o + at * D + c * 4));
+    // kBatch pieces load before the first is added: hundreds of pieces are one or two waits
+    constexpr int kBatch = kHow == kPart ? 8 : 4;
+    const int n = (int)(w1 - w0) + 1;
+    const float2* ml = p.ml + 2 * w0 * p.heads + hl;
+    const float* o = p.o + (2 * w0 * p.heads + hl) * D + c * 4;
+    for (int i0 = part; i0 < n; i0 += kBatch * kParts) {
+      float2 t[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kParts;
+        const int64_t at = (int64_t)(2 * i + (i == 0 ? (int)skip : 0)) * p.heads;
+        t[k] = i < n ? ml[at] : make_float2(kNoMax, 0.f);
+        v[k] = i < n ? *reinterpret_cast<const float4*>(o + at * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = x.m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, t[k].x);
+      const float f = exp2f(x.m - top);
+      x.m = top;
+      x.l *= f;
+      x.s = make_float4(x.s.x * f, x.s.y * f, x.s.z * f, x.s.w * f);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float u = exp2f(t[k].x - top);
+        x.l += t[k].y * u;
+        x.s.x += v[k].x * u; x.s.y += v[k].y * u; x.s.z += v[k].z * u; x.s.w += v[k].w * u;
+      }
     }
   }
 #pragma unroll
@@ -1190,7 +1225,17 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
     if (lane < kLanes) sums[warp][lane] = x;
     __syncthreads();
     if (threadIdx.x >= kLanes) return;
-    for (int k = 1; k < kJoin / 32; ++k) add_piece(x, sums[k][lane].m, sums[k][lane].l, sums[k][lane].s);
+    float top = x.m;
+#pragma unroll
+    for (int k = 1; k < kJoin / 32; ++k) top = fmaxf(top, sums[k][lane].m);
+    x = Sum{top, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+    for (int k = 0; k < kJoin / 32; ++k) {
+      const Sum y = sums[k][lane];
+      const float u = exp2f(y.m - top);
+      x.l += y.l * u;
+      x.s.x += y.s.x * u; x.s.y += y.s.y * u; x.s.z += y.s.z * u; x.s.w += y.s.w * u;
+    }
   } else if (lane >= kLanes) {
     return;
   }
@@ -1258,7 +1303,6 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   p.heads = a.G < Engine::kHeads ? a.G : Engine::kHeads;
   p.groups = (a.G + p.heads - 1) / p.heads;
   p.warps = ctas * kWarps;
-  p.min_units = 2;
   if (const int c = cluster_of(a, p.heads)) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
@@ -1294,11 +1338,15 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     if (rc) return rc;
     const int rows = x.B * a.H_q;
     // 1 x 48000 keys (32 rows): 38.9 us by parts, 45.0 by rows, 106 by warps; 16 x 4000 (512 rows): 52.9, 45.9,
-    // 49.8; 95 ragged of up to 8096, D = 64 (3040 rows): 89.9, 77.3, 68.8
+    // 49.8; 95 ragged of up to 8096, D = 64 (3040 rows): 89.9, 77.3, 68.8.  CTAs of 256 threads take more pieces
+    // at a time, of 128 find room beside the last of the split kernel's: 1 x 48000 38.6 and 40.3 us, 30 ragged of
+    // up to 8000 (240 rows, by parts) 23.1 and 20.6, 16 x 4000 ragged (512 rows) 19.5 and 21.2, 37 x 4000 ragged
+    // (1184 rows) 34.6 and 32.6
     const Join how = rows <= 256 ? kPart : (rows <= 152 * 16 ? kRow : kWarp);
+    const int threads = how == kWarp || (how == kPart ? rows <= 128 : rows <= 608) ? 256 : 128;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(how == kPart ? rows * (D / 32) : (how == kRow ? rows : (rows + kJoin / 32 - 1) / (kJoin / 32))));
-    cfg.blockDim = dim3(kJoin);
+    cfg.gridDim = dim3((unsigned)(how == kPart ? rows * (D / 32) : (how == kRow ? rows : (rows + 7) / 8)));
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1306,9 +1354,12 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     using TQ = typename Engine::TQ;
-    const cudaError_t err = how == kPart  ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kPart>, x, p)
-                            : how == kRow ? cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kRow>, x, p)
-                                          : cudaLaunchKernelEx(&cfg, decode_join_kernel<TQ, D, kWarp>, x, p);
+    const auto join = how == kWarp                      ? decode_join_kernel<TQ, D, kWarp, 256>
+                      : how == kPart && threads == 256 ? decode_join_kernel<TQ, D, kPart, 256>
+                      : how == kPart                   ? decode_join_kernel<TQ, D, kPart, 128>
+                      : threads == 256                 ? decode_join_kernel<TQ, D, kRow, 256>
+                                                       : decode_join_kernel<TQ, D, kRow, 128>;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, join, x, p);
     if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode join: launch failed: %s", cudaGetErrorString(err));
     count_launch();
   }
