@@ -320,11 +320,15 @@ struct MatrixEngine {
     return e4m3x2_to_f16x2((uint16_t)(w[e2 >> 1] >> (16 * (e2 & 1))));
   }
 
+  // two sums of half the row each: half the chain of dependent products
   __device__ __forceinline__ void scores(const Rows& r, int u, float (&s)[NT][4]) {
+    float h[2][NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[t][c] = 0.f;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) h[k][t][c] = 0.f;
 #pragma unroll
     for (int w = 0; w < kKW; ++w) {
       const uint32_t lo[4] = {r.k[u][0][w].x, r.k[u][0][w].y, r.k[u][0][w].z, r.k[u][0][w].w};
@@ -334,7 +338,7 @@ struct MatrixEngine {
         for (int x = 0; x < 2; ++x) {
           const uint32_t f[4] = {lo[2 * x], hi[2 * x], lo[2 * x + 1], hi[2 * x + 1]};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_bf16(s[t], f, q[t][w * 4 + 2 * x], q[t][w * 4 + 2 * x + 1]);
+          for (int t = 0; t < NT; ++t) mma_bf16(h[x & 1][t], f, q[t][w * 4 + 2 * x], q[t][w * 4 + 2 * x + 1]);
         }
       } else {
 #pragma unroll
@@ -342,10 +346,14 @@ struct MatrixEngine {
           const uint32_t f[4] = {e4m3x2_to_f16x2((uint16_t)lo[x]), e4m3x2_to_f16x2((uint16_t)hi[x]),
                                  e4m3x2_to_f16x2((uint16_t)(lo[x] >> 16)), e4m3x2_to_f16x2((uint16_t)(hi[x] >> 16))};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(s[t], f, q[t][w * 8 + 2 * x], q[t][w * 8 + 2 * x + 1]);
+          for (int t = 0; t < NT; ++t) mma_f16(h[x & 1][t], f, q[t][w * 8 + 2 * x], q[t][w * 8 + 2 * x + 1]);
         }
       }
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[t][c] = h[0][t][c] + h[1][t][c];
   }
 
   // the maximum of x over the lanes of a head (equal j)
@@ -686,7 +694,12 @@ struct SplitEngine {
       for (int x = 0; x < 2; ++x) split_tf32(__uint_as_float(q[i][2 * x]) * a.scale_log2, q[i][2 * x], q[i][2 * x + 1]);
     for (int at = 0; at < left; at += kHalf) {
       const int mine = min(keys, kHalf);
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      // four sums: a quarter of the chain of dependent products
+      float s[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[k][c] = 0.f;
       {
         uint32_t kw[kKW * 4];
 #pragma unroll
@@ -696,13 +709,13 @@ struct SplitEngine {
           float f[2];
           pair(kw, 2 * i, f);
           if (kQuant) {
-            mma_tf32(s, q[i], __float_as_uint(f[0]), __float_as_uint(f[1]));
+            mma_tf32(s[i % 4], q[i], __float_as_uint(f[0]), __float_as_uint(f[1]));
           } else {
             uint32_t h0, l0, h1, l1;
             split_tf32(f[0], h0, l0);
             split_tf32(f[1], h1, l1);
-            mma_tf32(s, q[i], h0, h1);
-            mma_tf32(s, q[i], l0, l1);
+            mma_tf32(s[i % 2], q[i], h0, h1);
+            mma_tf32(s[2 + i % 2], q[i], l0, l1);
           }
         }
       }
@@ -710,7 +723,8 @@ struct SplitEngine {
       place();
       load_k(a, r, row, keys);
       // rows g and g + 8 of the product: the high and the low parts of head g
-      float t0 = s[0] + s[2], t1 = s[1] + s[3];
+      float t0 = (s[0][0] + s[1][0]) + (s[2][0] + s[3][0]) + ((s[0][2] + s[1][2]) + (s[2][2] + s[3][2]));
+      float t1 = (s[0][1] + s[1][1]) + (s[2][1] + s[3][1]) + ((s[0][3] + s[1][3]) + (s[2][3] + s[3][3]));
       if (kQuant) { t0 *= ks.x; t1 *= ks.y; }
       t0 = 2 * j < mine ? t0 : -INFINITY;
       t1 = 2 * j + 1 < mine ? t1 : -INFINITY;
