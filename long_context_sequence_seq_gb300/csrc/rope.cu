@@ -159,7 +159,7 @@ int launch_rope(const RopeArgs& a, cudaStream_t st) {
   const int need = (a.dtype == ULYSSES_BF16 ? 8 : 4) * kThreads;
   int tb = 1;
   while (tb < kMaxTokens && 2 * tb * a.half <= kMaxAngles && (int64_t)tb * a.heads * (a.D / 16) < need) tb *= 2;
-  while (tb > 1 && (a.N + tb - 1) / tb < 4 * sms) tb /= 2;
+  while (tb > 1 && (a.N + tb - 1) / tb < 2 * sms) tb /= 2;
   const int64_t gx = (a.N + tb - 1) / tb;
   // few tokens: split the heads too, down to 8 heads (one round of the CTA's threads or two)
   int hc = a.heads;
