@@ -417,7 +417,9 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * are formed of two 11-bit parts of each operand: rounded as in fp32, but an
  * infinite element gives NaN (a K element in its key's score, a V element in
  * its output element).
- * B * H_q <= 2^24; strides and alignment as for ulysses_cache_write. */
+ * B * H_q <= 2^24; table_cols * page_size * H_kv (times H_q / H_kv / 16 where
+ * that is more than one) <= 2^35; strides and alignment as for
+ * ulysses_cache_write. */
 size_t ulysses_attn_decode_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
                                      int cache_dtype);
 int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,

@@ -78,7 +78,7 @@ struct Plan {
   int groups;       // query-head groups of a kv head
   int heads;        // query heads of a group (the last may have fewer)
   int warps;        // of the launch
-  int64_t* prefix;  // [B + 1] units before each sequence (one head); workspace
+  int* prefix;      // [B + 1] units before each sequence (one head); workspace
   float2* ml;       // [2 * warps][heads] (m, l); workspace
   float* o;         // [2 * warps][heads][D] sums; workspace
 };
@@ -94,24 +94,20 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   return (int)n;
 }
 
-// a / b of numbers that mostly fit 32 bits, where the division is several times shorter.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
 // Warps that share `total` units (each at least kMinUnits), the first unit of
-// warp w, and the warp that has a unit.
-__device__ __forceinline__ int64_t active_warps(const Plan& p, int64_t total) {
-  const int64_t w = (total + kMinUnits - 1) / kMinUnits;
-  return w < p.warps ? w : p.warps;
+// warp w, and the warp that has a unit.  The host keeps a launch's units below
+// 2^31: 64-bit divisions here cost a microsecond of every call.
+__device__ __forceinline__ int active_warps(const Plan& p, int total) {
+  return min(p.warps, (total - 1) / kMinUnits + 1);
 }
-__device__ __forceinline__ int64_t first_unit(int64_t w, int64_t active, int64_t total) {
-  const int64_t each = quotient(total, active), rest = total - each * active;
-  return w * each + (w < rest ? w : rest);
+__device__ __forceinline__ int first_unit(int w, int active, int total) {
+  const int each = (unsigned)total / (unsigned)active, rest = total - each * active;
+  return w * each + min(w, rest);
 }
-__device__ __forceinline__ int64_t warp_of(int64_t unit, int64_t active, int64_t total) {
-  const int64_t each = quotient(total, active), rest = total - each * active;
-  return unit < rest * (each + 1) ? quotient(unit, each + 1) : rest + quotient(unit - rest * (each + 1), each);
+__device__ __forceinline__ int warp_of(int unit, int active, int total) {
+  const int each = (unsigned)total / (unsigned)active, rest = total - each * active;
+  const int longer = rest * (each + 1);                    // units of the warps that have one more
+  return unit < longer ? (unsigned)unit / (unsigned)(each + 1) : rest + (unsigned)(unit - longer) / (unsigned)each;
 }
 
 // The piece of an item that a warp walks.
@@ -1012,22 +1008,21 @@ template <class Engine, int D, int kCtas>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid_constant__ DecodeArgs a,
                                                                     const __grid_constant__ Plan p) {
   // prefix[b]: units of the sequences before b (of one head)
-  extern __shared__ int64_t prefix[];
-  __shared__ int64_t sums[kWarps];
+  extern __shared__ int prefix[];
+  __shared__ int sums[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t carry = 0;
+  int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
     const int b = b0 + threadIdx.x;
-    const int64_t mine = b < a.B ? (length_of(a, b) + kUnit - 1) / kUnit : 0;
-    int64_t x = mine;
+    int x = b < a.B ? (length_of(a, b) + kUnit - 1) / kUnit : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
-    int64_t before = carry;
+    int before = carry;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += sums[w];
       carry += sums[w];
@@ -1043,11 +1038,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int per = a.H_kv * p.groups;                       // items of a sequence
-  const int64_t total = carry * per;
+  const int total = carry * per;
   if (total == 0) return;
-  const int64_t active = active_warps(p, total), w = (int64_t)blockIdx.x * kWarps + warp;
+  const int active = active_warps(p, total), w = blockIdx.x * kWarps + warp;
   if (w >= active) return;
-  const int64_t begin = first_unit(w, active, total), end = first_unit(w + 1, active, total);
+  const int begin = first_unit(w, active, total), end = first_unit(w + 1, active, total);
   int b = 0;
   {
     int lo = 0, hi = a.B - 1;                              // the last b with prefix[b] * per <= begin
@@ -1058,19 +1053,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
     b = lo;
   }
   Engine e(lane);
-  int64_t at = begin;
+  int at = begin;
   while (at < end) {
     while (prefix[b + 1] * per <= at) ++b;
-    const int64_t units = prefix[b + 1] - prefix[b], in_seq = at - prefix[b] * per;
-    const int item = (int)quotient(in_seq, units);
-    const int64_t item0 = prefix[b] * per + item * units;  // the item's first unit
+    const int units = prefix[b + 1] - prefix[b], in_seq = at - prefix[b] * per;
+    const int item = (unsigned)in_seq / (unsigned)units;
+    const int item0 = prefix[b] * per + item * units;      // the item's first unit
     Piece pc;
     pc.b = b;
     pc.h = item / p.groups;
     pc.g0 = (item - pc.h * p.groups) * p.heads;
     pc.gn = min(a.G - pc.g0, p.heads);
-    pc.unit0 = (int)(at - item0);
-    pc.units = (int)(min(end, item0 + units) - at);
+    pc.unit0 = at - item0;
+    pc.units = min(end, item0 + units) - at;
     pc.len = length_of(a, b);
     e.begin(a, pc);
     e.run(a, pc);
@@ -1103,8 +1098,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   pc.gn = min(a.G - pc.g0, heads);
   pc.len = length_of(a, pc.b);
   const int units = (pc.len + kUnit - 1) / kUnit, warps = ctas * kWarps, w = rank * kWarps + warp;
-  pc.unit0 = (int)first_unit(w, warps, units);
-  pc.units = (int)first_unit(w + 1, warps, units) - pc.unit0;
+  pc.unit0 = first_unit(w, warps, units);
+  pc.units = first_unit(w + 1, warps, units) - pc.unit0;
   Engine e(lane);
   e.begin(a, pc);
   if (pc.units > 0) e.run(a, pc);
@@ -1192,31 +1187,31 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
   const int b = bh / a.H_q, hq = bh - b * a.H_q;
   const int h = hq / a.G, gi = (hq - h * a.G) / p.heads, hl = hq - h * a.G - gi * p.heads;
   TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)b * a.o_b + (int64_t)hq * a.o_h + c * 4;
-  const int64_t before = p.prefix[b], after = p.prefix[b + 1], all = p.prefix[a.B];
-  const int64_t units = after - before;
+  const int before = p.prefix[b], after = p.prefix[b + 1], all = p.prefix[a.B];
+  const int units = after - before;
   Sum x{kNoMax, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   if (units > 0) {
     const int per = a.H_kv * p.groups;
-    const int64_t total = all * per, active = active_warps(p, total);
-    const int64_t first = before * per + (h * p.groups + gi) * units;
-    const int64_t w0 = warp_of(first, active, total), w1 = warp_of(first + units - 1, active, total);
+    const int total = all * per, active = active_warps(p, total);
+    const int first = before * per + (h * p.groups + gi) * units;
+    const int w0 = warp_of(first, active, total), w1 = warp_of(first + units - 1, active, total);
     if (w0 == w1) return;                                  // finished where it was walked
     // the piece of warp w: in its first slot unless the item begins inside w's range
-    const int64_t skip = first_unit(w0, active, total) == first ? 0 : 1;
+    const int skip = first_unit(w0, active, total) == first ? 0 : 1;
     // kBatch pieces load before the first is added: hundreds of pieces are one or two waits
     constexpr int kBatch = kHow == kPart ? 8 : 4;
-    const int n = (int)(w1 - w0) + 1;
+    const int n = w1 - w0 + 1;
     const float2* ml = p.ml + 2 * w0 * p.heads + hl;
-    const float* o = p.o + (2 * w0 * p.heads + hl) * D + c * 4;
+    const float* o = p.o + (int64_t)(2 * w0 * p.heads + hl) * D + c * 4;
     for (int i0 = part; i0 < n; i0 += kBatch * kParts) {
       float2 t[kBatch];
       float4 v[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k * kParts;
-        const int64_t at = (int64_t)(2 * i + (i == 0 ? (int)skip : 0)) * p.heads;
+        const int at = (2 * i + (i == 0 ? skip : 0)) * p.heads;
         t[k] = i < n ? ml[at] : make_float2(kNoMax, 0.f);
-        v[k] = i < n ? *reinterpret_cast<const float4*>(o + at * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k] = i < n ? *reinterpret_cast<const float4*>(o + (int64_t)at * D) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float top = x.m;
 #pragma unroll
@@ -1300,7 +1295,7 @@ WsLayout ws_layout(const DecodeArgs& a, int heads) {
   WsLayout w{};
   const int b = a.B < kMaxBatch ? a.B : kMaxBatch;
   w.prefix = 0;
-  w.ml = align256((size_t)(b + 1) * 8);
+  w.ml = align256((size_t)(b + 1) * sizeof(int));
   w.o = w.ml + align256((size_t)2 * kMaxWarps * heads * 8);
   w.total = w.o + align256((size_t)2 * kMaxWarps * heads * a.D * 4);
   return w;
@@ -1335,18 +1330,24 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   }
   const WsLayout w = ws_layout(a, p.heads);
   char* ws = (char*)a.ws;
-  p.prefix = (int64_t*)(ws + w.prefix);
+  p.prefix = (int*)(ws + w.prefix);
   p.ml = (float2*)(ws + w.ml);
   p.o = (float*)(ws + w.o);
-  for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
+  // sequences of a launch: their prefix sums fit shared memory, their units 31 bits with every table full
+  const int64_t full = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit * a.H_kv * p.groups;
+  int batch = kMaxBatch;
+  if (full > 0 && 2147483647 / full < batch) batch = (int)(2147483647 / full);
+  if (batch == 0)
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "attn_decode: table_cols * page_size * H_kv of one sequence above 2^35");
+  for (int b0 = 0; b0 < a.B; b0 += batch) {
     DecodeArgs x = a;
-    x.B = a.B - b0 < kMaxBatch ? a.B - b0 : kMaxBatch;
+    x.B = a.B - b0 < batch ? a.B - b0 : batch;
     x.q = (const char*)a.q + (int64_t)b0 * a.q_b * sizeof(typename Engine::TQ);
     x.o = (char*)a.o + (int64_t)b0 * a.o_b * sizeof(typename Engine::TQ);
     x.lse = a.lse ? a.lse + (int64_t)b0 * a.H_q : nullptr;
     x.table = a.table + (int64_t)b0 * a.cols;
     x.lens = a.lens + b0;
-    decode_kernel<Engine, D, kCtas><<<ctas, kWarps * 32, (x.B + 1) * sizeof(int64_t), st>>>(x, p);
+    decode_kernel<Engine, D, kCtas><<<ctas, kWarps * 32, (x.B + 1) * sizeof(int), st>>>(x, p);
     count_launch();
     int rc = check_launch("attn_decode");
     if (rc) return rc;

@@ -139,6 +139,8 @@ def test_decode_refusals(L):
     if need:
         assert _decode(L, n=need - 1) == U.ERR_INVALID
         assert _decode(L, ws=P(264)) == U.ERR_INVALID
+    # more units of 16 keys in one sequence's table than 31 bits count
+    assert _decode(L, Hq=64, Hkv=64, q_b=64 * 128, o_b=64 * 128, o=P(1 << 40), cols=1 << 26) == U.ERR_UNSUPPORTED
     assert _decode(L, B=0) == U.OK
     assert L.ulysses_launch_count() == launches
 
