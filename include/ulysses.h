@@ -47,6 +47,8 @@
  * cu_seqlens contents are validated on the device: a non-monotone table or
  * one that does not end at S sets the device error word (read by
  * ulysses_check) and the attention kernels then write nothing meaningful.
+ * Page tables and cached lengths are checked there too: what lies outside their
+ * range is left out and reported as ULYSSES_ERR_BAD_PAGES.
  */
 #ifndef ULYSSES_H
 #define ULYSSES_H

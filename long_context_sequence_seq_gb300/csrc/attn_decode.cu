@@ -22,8 +22,8 @@
 // programmatic dependency so that its launch overlaps, adds each item's pieces
 // in the order of the warps.  No atomics, nothing to initialise.  (Measured:
 // one CTA an item instead, 64 ragged sequences of 512 to 32768 keys, bf16: 1846
-// us; this way 316 us for 2.10 GB, 99% of the measured copy rate.  A million
-// keys of one sequence in e4m3: 57.3 ms and 337 us for 2.21 GB, 98%.)
+// us; this way 309 us for 2.10 GB, 102% of the measured copy rate.  A million
+// keys of one sequence in e4m3: 57.3 ms and 328 us for 2.21 GB, 101%.)
 // Where the page table has room for a few units a warp only, a cluster of CTAs
 // takes each item and joins through distributed shared memory: one launch.
 //
@@ -50,9 +50,9 @@
 //   11-bit parts on the tf32 pipe; heads are the M side, the high parts of up
 //   to 8 in its rows 0-7 and their low parts in rows 8-15, so one instruction
 //   multiplies both by a part of K or V, and two make the product to 2^-21.
-//   (8 x 8000 keys, 4 heads of 128: 107 us, 73% of the copy rate.)
+//   (8 x 8000 keys, 4 heads of 128: 98 us, 80% of the copy rate.)
 //   SIMT engine (fp32 queries of one or two heads, and by choice): FMA
-//   throughout, 8 lanes a key.  (8 x 8000 keys, 1 head of 128: 84 us, 94%.)
+//   throughout, 8 lanes a key.  (8 x 8000 keys, 1 head of 128: 83 us, 95%.)
 #include "internal.h"
 #include "rows.cuh"
 #include "tc_ptx.cuh"
@@ -1261,9 +1261,9 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
 constexpr int kMaxWarps = 152 * 16;              // of a launch: slots of the workspace
 
 // fp32 queries of one or two heads a key are SIMT work: at 1-2 flops a byte the
-// FMA pipe keeps up (30 x 10277 keys, 1 head of 128: 57 us, 70 us by the fp32
-// matrix engine), from 3 heads on it does not (4 heads: 152 and 146 us, 8
-// heads: 206 and 74 us).
+// FMA pipe keeps up (30 x 10277 keys, 1 head of 128: 52 us, 64 us by the fp32
+// matrix engine), from 3 heads on it does not (2 x 78542 ragged, 4 heads: 146
+// and 132 us; 37 x 4483, 8 heads of 64: 208 and 71 us).
 bool use_simt(const DecodeArgs& a, bool chosen) { return chosen || (a.dtype == ULYSSES_FP32 && a.G <= 2); }
 
 // query heads of a group
@@ -1277,8 +1277,9 @@ int heads_of(const DecodeArgs& a, bool simt) {
 // A cluster saves the join and its launch, but waits for the longest item: it
 // pays while its warps have at most kClusterUnits units when the table is full
 // and all clusters are resident at once (8 kv heads of 4: 1 x 777 keys 7.2 us
-// by clusters, 10.0 split; 1 x 6000 13.1 and 20.2; 16 x 4000 ragged 32.7 and
-// 20.8, 4 x 16000 ragged 36.9 and 29.9, which twice as many would take).
+// by clusters, 8.5 split; 1 x 6000 13.1 and 12.5, but a launch and a workspace
+// less; 16 x 4000 ragged 32.7 and 19.5, 4 x 16000 ragged 37.0 and 22.2, which
+// twice as many units would take).
 constexpr int kClusterUnits = 16;
 int cluster_of(const DecodeArgs& a, int heads) {
   const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
@@ -1352,11 +1353,11 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     int rc = check_launch("attn_decode");
     if (rc) return rc;
     const int rows = x.B * a.H_q;
-    // 1 x 48000 keys (32 rows): 38.9 us by parts, 45.0 by rows, 106 by warps; 16 x 4000 (512 rows): 52.9, 45.9,
-    // 49.8; 95 ragged of up to 8096, D = 64 (3040 rows): 89.9, 77.3, 68.8.  CTAs of 256 threads take more pieces
-    // at a time, of 128 find room beside the last of the split kernel's: 1 x 48000 38.6 and 40.3 us, 30 ragged of
-    // up to 8000 (240 rows, by parts) 23.1 and 20.6, 16 x 4000 ragged (512 rows) 19.5 and 21.2, 37 x 4000 ragged
-    // (1184 rows) 34.6 and 32.6
+    // 1 x 48000 keys (32 rows): 37.0 us by parts, 46.2 by rows, 78.1 by warps; 16 x 4000 (512 rows): 53.5, 46.8,
+    // 48.9; 95 ragged of up to 8096, D = 64 (3040 rows): 89.4, 75.9, 70.8.  CTAs of 256 threads take more pieces
+    // at a time, of 128 find room beside the last of the split kernel's: by parts 1 x 48000 37.0 and 38.6 us, 30
+    // ragged of up to 8000 (240 rows) 21.0 and 18.7; by rows 16 x 4000 ragged (512 rows) 20.4 and 22.0, 37 x 4000
+    // ragged (1184 rows) 32.4 and 31.9
     const Join how = rows <= 256 ? kPart : (rows <= 152 * 16 ? kRow : kWarp);
     const int threads = how == kWarp || (how == kPart ? rows <= 128 : rows <= 608) ? 256 : 128;
     cudaLaunchConfig_t cfg{};
