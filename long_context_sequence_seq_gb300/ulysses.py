@@ -28,6 +28,9 @@ PAIRS_HALF, PAIRS_ADJACENT = 0, 1
 KERNEL_AUTO, KERNEL_SIMT = 0, 1
 
 _lib = None
+# C++ marshalling of the strided calls (_fastcall.so), bound to the loaded
+# library; None where it has not been built: the Python marshalling serves then.
+_fast = None
 
 
 class RelayoutItem(ctypes.Structure):
@@ -114,7 +117,24 @@ def lib():
     L.ulysses_launch_count.restype = ctypes.c_longlong
     L.ulysses_checked_build.restype = ctypes.c_int
     _lib = L
+    _bind_fast(L)
     return L
+
+
+def _bind_fast(L):
+    """Load the C++ marshalling, if it is there, and give it the library's
+    functions.  One built against another torch does not load: it is left out."""
+    global _fast
+    if not os.path.exists(os.path.join(_PKG, "_fastcall.so")):
+        return
+    try:
+        from . import _fastcall
+    except ImportError:
+        return
+    _fastcall.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.ulysses_rope_fwd, L.ulysses_rope_bwd, L.ulysses_cache_write, L.ulysses_cache_read, L.ulysses_attn_decode,
+        L.ulysses_attn_decode_workspace)))
+    _fast = _fastcall
 
 
 def _ck(rc):
@@ -510,8 +530,10 @@ def layer_bwd_fused(q_seq, k_seq, v_seq, o_seq, do_seq, lse, P, head_chunk, cu_s
 # "head": heads, tokens, D; D contiguous).  They run on the device of their
 # tensors, whichever is current, on `stream` or that device's current stream;
 # outputs and workspaces made here belong to that stream.
-# A call's kernels take a few microseconds at decode sizes, so these functions
-# read each tensor property once and make no objects besides the results.
+# A call's kernels take a few microseconds at decode sizes.  Plain calls (no
+# stream given, everything as it should be) are marshalled by _fastcall.so; the
+# Python below serves the others and says what is wrong with a call.  It reads
+# each tensor property once and makes no objects besides the results.
 
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32, torch.float8_e4m3fn: E4M3}
 _BF16, _F32, _F64, _I32, _U8, _F8 = (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8,
@@ -704,6 +726,10 @@ def rope_fwd(q, k, positions, inv_freq, axes=None, layout="seq", pairs="half", o
     pairs (i, i + half) with "half", (2i, 2i+1) with "adjacent"; the others are
     copied.  out: the outputs, q and k themselves for in place.  Returns the
     rotated tensors, in the order given."""
+    if _fast is not None and stream is None:
+        r = _fast.rope(False, q, k, positions, inv_freq, axes, layout, pairs, None, out)
+        if r is not None:
+            return r if type(r) is not int else _ck(r)
     return _rope(lib().ulysses_rope_fwd, q, k, positions, inv_freq, axes, layout, pairs, None, out, stream)
 
 
@@ -711,6 +737,10 @@ def rope_bwd(dq, dk, positions, inv_freq, axes=None, layout="seq", pairs="half",
     """Adjoint of rope_fwd: gradients of the rotated Q and K (as layer_bwd
     gives them, fp32 or bf16) to those of the projection's Q and K.  dtype: the
     outputs' type (default: the gradients'; bf16 from fp32 rounds once)."""
+    if _fast is not None and stream is None:
+        r = _fast.rope(True, dq, dk, positions, inv_freq, axes, layout, pairs, dtype, out)
+        if r is not None:
+            return r if type(r) is not int else _ck(r)
     return _rope(lib().ulysses_rope_bwd, dq, dk, positions, inv_freq, axes, layout, pairs, dtype, out, stream)
 
 
@@ -765,6 +795,10 @@ def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_sca
     rows [cu_new[b], cu_new[b+1]); None: one token per sequence, and a length
     of 0 marks an empty place of the batch.  An e4m3 cache (with its scales) is
     quantised row by row on the way.  Bad positions or pages raise in check()."""
+    if _fast is not None and stream is None:
+        r = _fast.cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, k_scale, v_scale, layout)
+        if r is not None:
+            return _ck(r)
     ks, kh, T, H, D = _rows3(k, layout, "k")
     vs, vh, Tv, Hv, Dv = _rows3(v, layout, "v")
     dt = k.dtype
@@ -794,6 +828,10 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=
     cu_seqlens[b] (first None: 0).  Returns (k, v) with T tokens, [T, H_kv, D]
     or [H_kv, T, D]; rows from cu_seqlens[B] on are left as they were.  dtype:
     the cache's, or bf16 (default) / fp32 from an e4m3 cache."""
+    if _fast is not None and stream is None:
+        r = _fast.cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first, k_scale, v_scale, dtype, layout, out)
+        if r is not None:
+            return r if type(r) is not int else _ck(r)
     pk, pv, pks, pvs, (n_pages, H, page, D) = _cache(k_cache, v_cache, k_scale, v_scale)
     held = k_cache.dtype
     if dtype is None:
@@ -851,6 +889,11 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     cached positions; length 0 gives O = 0, LSE = -inf.  Returns (O shaped as
     q, LSE [B, H_q] fp32).  workspace: attn_decode_workspace(), for calls that
     do not overlap on the GPU; made per call if not given."""
+    if _fast is not None and stream is None:
+        r = _fast.attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, scale, layout, workspace, out,
+                              lse)
+        if r is not None:
+            return r if type(r) is not int else _ck(r)
     qb, qh, B, H_q, D = _rows3(q, layout, "q")
     pk, pv, pks, pvs, (n_pages, H_kv, page, Dc) = _cache(k_cache, v_cache, k_scale, v_scale)
     if D != Dc or seq_lens.numel() != B:
