@@ -46,12 +46,15 @@
 //   enter in fp32: K's times the score, V's in the weight, as 2^(s + log2 vs - M)
 //   with a running maximum M of its own, so f16 weights keep 11 bits of the
 //   largest contribution whatever the rows' scales are.
-//   Split engine (fp32 queries, three heads and more): fp32 operands as two
+//   Split engine (fp32 queries, from two or three heads on): fp32 operands as two
 //   11-bit parts on the tf32 pipe; heads are the M side, the high parts of up
 //   to 8 in its rows 0-7 and their low parts in rows 8-15, so one instruction
-//   multiplies both by a part of K or V, and two make the product to 2^-21.
-//   (8 x 8000 keys, 4 heads of 128: 98 us, 80% of the copy rate.)
-//   SIMT engine (fp32 queries of one or two heads, and by choice): FMA
+//   multiplies both by a part of K or V, and two make the product to 2^-21.  A
+//   step's products are summed from zero and added in fp32: left to accumulate
+//   in the pipe, which cuts instead of rounding, 8 x 30000 keys were 7.5e-6 off
+//   (2-norm) in 338 us; this way 7.8e-7, less than plain fp32, in 392 us (75% of
+//   the copy rate).
+//   SIMT engine (fp32 queries of one head or two, and by choice): FMA
 //   throughout, 8 lanes a key.  (8 x 8000 keys, 1 head of 128: 83 us, 95%.)
 #include "internal.h"
 #include "rows.cuh"
@@ -750,15 +753,19 @@ struct SplitEngine {
         pair(r.v[1], e, a1);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          // a step's sum from zero, added in fp32: the pipe cuts what it accumulates
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
           if (kQuant) {
-            mma_tf32(acc[e + x], w, __float_as_uint(a0[x]), __float_as_uint(a1[x]));
+            mma_tf32(t, w, __float_as_uint(a0[x]), __float_as_uint(a1[x]));
           } else {
             uint32_t h0, l0, h1, l1;
             split_tf32(a0[x], h0, l0);
             split_tf32(a1[x], h1, l1);
-            mma_tf32(acc[e + x], w, h0, h1);
-            mma_tf32(acc[e + x], w, l0, l1);
+            mma_tf32(t, w, l0, l1);
+            mma_tf32(t, w, h0, h1);
           }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[e + x][c] += t[c];
         }
       }
       load_v(a, r, row, keys);
@@ -1260,11 +1267,13 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
 
 constexpr int kMaxWarps = 152 * 16;              // of a launch: slots of the workspace
 
-// fp32 queries of one or two heads a key are SIMT work: at 1-2 flops a byte the
-// FMA pipe keeps up (30 x 10277 keys, 1 head of 128: 52 us, 64 us by the fp32
-// matrix engine), from 3 heads on it does not (2 x 78542 ragged, 4 heads: 146
-// and 132 us; 37 x 4483, 8 heads of 64: 208 and 71 us).
-bool use_simt(const DecodeArgs& a, bool chosen) { return chosen || (a.dtype == ULYSSES_FP32 && a.G <= 2); }
+// fp32 queries of few heads a key are SIMT work: at 1-2 flops a byte the FMA
+// pipe keeps up.  1 head of 128 (8 x 30000 keys): 283 us, 96% of the copy rate;
+// 2 of 128 (8 x 8000): 87 us, 98 by the fp32 matrix engine; but 2 of 64 (8 x
+// 30000) 203 and 186 us, 3 of 128 578 and 392, 8 of 128 734 and 393.
+bool use_simt(const DecodeArgs& a, bool chosen) {
+  return chosen || (a.dtype == ULYSSES_FP32 && a.G <= (a.D == 128 ? 2 : 1));
+}
 
 // query heads of a group
 int heads_of(const DecodeArgs& a, bool simt) {

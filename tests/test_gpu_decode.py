@@ -423,6 +423,24 @@ def test_e4m3_rows_of_very_different_scales(spread, gain, how):
     check(o, lse, new, "bf16", "e4m3", "seq")
 
 
+@pytest.mark.parametrize("Hq,D", [(8, 128), (4, 64)])
+def test_long_fp32_sums_keep_fp32_precision(Hq, D):
+    """20000 keys of nearly equal weights: the 2-norm of the error stays below
+    that of one fp32 rounding a key accumulated at random, sqrt(n) 2^-24 of the
+    weighted values' 2-norm, plus the products' 2^-21."""
+    n = 20000
+    args, rows = build([n], Hq, 1, D, 64, "fp32", "fp32", "seq", seed=18)
+    args["q"] *= 0.05
+    q, k, v = f64(args["q"][0]), rows[0][1], rows[0][2]
+    o, _ = U.attn_decode(**widen(args, 1 << 22))
+    U.check()
+    ro, rl = so.decode(q, k, v)
+    p = np.exp(k[:, 0] @ q.T / math.sqrt(D) - rl)                # [n, Hq]
+    size = np.sqrt((p ** 2).T @ (v[:, 0] ** 2))                   # [Hq, D]: spread of a sum of n products
+    lim = np.linalg.norm(size) * (math.sqrt(n) * E + 2.0 ** -21) + np.linalg.norm(ro) * 2.0 ** -20
+    assert np.linalg.norm(f64(o[0]) - ro) <= lim
+
+
 def test_nothing_outside_outputs_and_workspace_is_written():
     """Windows with guard bytes on both sides, in both ways of a launch."""
     pat, guard, bufs = 0xA5, 4096, []
