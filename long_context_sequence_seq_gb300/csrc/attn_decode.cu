@@ -43,9 +43,13 @@
 //   the output is then off by its own rounding alone, and the pipe has room).
 //   E4m3 codes become f16 exactly.  q is scaled by a power of two into f16's
 //   range (exact, but for elements 2^-24 below its largest); the rows' scales
-//   enter in fp32: K's times the score, V's in the weight, as 2^(s + log2 vs - M)
-//   with a running maximum M of its own, so f16 weights keep 11 bits of the
-//   largest contribution whatever the rows' scales are.
+//   enter in fp32: K's times the score, V's in the weight, as
+//   2^(s + log2 vs - M + 7) with a running maximum M of its own, so that the
+//   largest weights of a piece, whatever the rows' scales are, lie at 2^7 to 2^15
+//   of f16's range (below 2^16), and those 2^-32 below them are still held.
+//   They go in as a value and its rounding error too, 2^-22; as a value alone
+//   (2^-12) the output of a million keys differed from fp32 arithmetic's by
+//   8.8e-4 in norm.
 //   Split engine (fp32 queries, from two or three heads on): fp32 operands as two
 //   11-bit parts on the tf32 pipe; heads are the M side, the high parts of up
 //   to 8 in its rows 0-7 and their low parts in rows 8-15, so one instruction
@@ -71,6 +75,7 @@ using namespace rows;
 constexpr int kUnit = 16;                       // keys of a unit
 constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr float kLazy = 8.f;                    // a maximum moves when exceeded by 2^8
+constexpr float kLift = 7.f;                    // f16 weights are 2^7 at the maximum, so at most 2^15
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                       // of a CTA
 constexpr int kMinUnits = 2;                    // of a warp, where there are enough for all
@@ -178,10 +183,16 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, as exp2f, with
   return r;
 }
 
-template <bool kQuant, int D, int NT>
+// kTwice: up to 4 heads a group, each in two columns of the N side, h and h + 4;
+// the scores of both are the same, and the first takes the weights and the
+// second what their rounding left, so one product has both.  (A million e4m3
+// keys, 4 heads a kv head: 343 us; with two products 390, and with weights as a
+// value alone 339.  Groups of more heads have no columns left: 8 ragged
+// sequences of up to 30000 e4m3 keys, 8 heads a kv head, 46 us, a value alone 42.)
+template <bool kQuant, int D, int NT, bool kTwice>
 struct MatrixEngine {
   using TQ = __nv_bfloat16;
-  static constexpr int kHeads = 8 * NT;
+  static constexpr int kHeads = kTwice ? 4 : 8 * NT;
   static constexpr int kRowB = kQuant ? D : 2 * D;        // bytes of a row
   static constexpr int kSub = kRowB == 256 ? 1 : 2;       // units of a step: 32 registers of K and of V, or 16
   static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
@@ -202,7 +213,7 @@ struct MatrixEngine {
     constexpr int kE = kQuant ? 16 : 8;                    // elements of a K word
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int hl = t * 8 + g;
+      const int hl = kTwice ? g & 3 : t * 8 + g;
       const bool live = hl < p.gn;
       const TQ* qp = reinterpret_cast<const TQ*>(a.q) + (int64_t)p.b * a.q_b + (int64_t)(p.h * a.G + p.g0 + (live ? hl : 0)) * a.q_h;
 #pragma unroll
@@ -402,8 +413,9 @@ struct MatrixEngine {
           l[t][c] *= f;
           if (!kQuant) rescale(t, c, f);
         }
-        if (kQuant && __any_sync(0xffffffffu, topw > mw[t][c] + kLazy)) {
-          const float mm = fmaxf(mw[t][c], max_keys(topw)), f = exp2_fast(mw[t][c] - mm);
+        // mw is kLift below the maximum
+        if (kQuant && __any_sync(0xffffffffu, topw > mw[t][c] + (kLift + kLazy))) {
+          const float mm = fmaxf(mw[t][c], max_keys(topw) - kLift), f = exp2_fast(mw[t][c] - mm);
           mw[t][c] = mm;
           rescale(t, c, f);
         }
@@ -418,20 +430,28 @@ struct MatrixEngine {
       }
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-      uint32_t pb[NT][2], pl[NT][2];                       // weights; bf16: and what their rounding left
+      uint32_t pb[NT][2], pl[NT][2];                       // weights, and what their rounding left
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float p0 = s[u][t][2 * x], p1 = s[u][t][2 * x + 1];
+          uint32_t hi, lo;
           if (kQuant) {
-            pb[t][x] = transpose8x8(f32_to_f16x2(p0, p1));
+            hi = f32_to_f16x2(p0, p1);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            lo = f32_to_f16x2(p0 - h.x, p1 - h.y);
           } else {
-            const uint32_t hi = f32_to_bf16x2(p0, p1);
+            hi = f32_to_bf16x2(p0, p1);
             float h[2];
             bf16x2_to_f32(hi, h);
+            lo = f32_to_bf16x2(p0 - h[0], p1 - h[1]);
+          }
+          if (kTwice) {
+            pb[t][x] = transpose8x8(j < 2 ? hi : lo);
+          } else {
             pb[t][x] = transpose8x8(hi);
-            pl[t][x] = transpose8x8(f32_to_bf16x2(p0 - h[0], p1 - h[1]));
+            pl[t][x] = transpose8x8(lo);
           }
         }
 #pragma unroll
@@ -445,10 +465,13 @@ struct MatrixEngine {
                                  __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            if (kQuant) mma_f16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
-            else {
-              mma_bf16(acc[t][w * (kVE / 2) + e], f, pb[t][0], pb[t][1]);
-              mma_bf16(acc[t][w * (kVE / 2) + e], f, pl[t][0], pl[t][1]);
+            float* sum = acc[t][w * (kVE / 2) + e];
+            if (kQuant) {
+              mma_f16(sum, f, pb[t][0], pb[t][1]);
+              if (!kTwice) mma_f16(sum, f, pl[t][0], pl[t][1]);
+            } else {
+              mma_bf16(sum, f, pb[t][0], pb[t][1]);
+              if (!kTwice) mma_bf16(sum, f, pl[t][0], pl[t][1]);
             }
           }
         }
@@ -504,6 +527,13 @@ struct MatrixEngine {
         l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 4);
         l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 8);
         l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], 16);
+        if (kTwice) {
+#pragma unroll
+          for (int i = 0; i < kMT; ++i) {
+            acc[t][i][c] += __shfl_xor_sync(0xffffffffu, acc[t][i][c], 2);
+            acc[t][i][c + 2] += __shfl_xor_sync(0xffffffffu, acc[t][i][c + 2], 2);
+          }
+        }
         if (kQuant) rescale(t, c, exp2f(mw[t][c] - m[t][c]));   // sums in units of 2^m again
       }
   }
@@ -1393,8 +1423,9 @@ int run(const DecodeArgs& a, cudaStream_t st) {
 
 template <bool kQuant, int D>
 int run_matrix(const DecodeArgs& a, cudaStream_t st) {
-  if (a.G <= 8) return run<MatrixEngine<kQuant, D, 1>, D, 3>(a, st);
-  return run<MatrixEngine<kQuant, D, 2>, D, 2>(a, st);
+  if (a.G <= 4) return run<MatrixEngine<kQuant, D, 1, true>, D, 3>(a, st);
+  if (a.G <= 8) return run<MatrixEngine<kQuant, D, 1, false>, D, 3>(a, st);
+  return run<MatrixEngine<kQuant, D, 2, false>, D, 2>(a, st);
 }
 template <typename TQ, typename TC, int D>
 int run_simt(const DecodeArgs& a, cudaStream_t st) {

@@ -1,0 +1,105 @@
+"""Single-token attention where its weights, its values and its joins are
+extreme, against the fp64 definition.
+
+Bound of an e4m3 cache with bf16 queries, tighter than test_gpu_decode's.  A
+weight (softmax weight times V's scale, at most 2^15 in f16 and at least 2^7
+for the largest of a piece) goes in as an f16 value and the f16 rest: 2^-22 of
+it, and half of f16's smallest step, 2^-25, which is 2^-32 of the largest:
+  sum_j 2^-32 max_i(p_i scale_i) |code_jd|.
+Queries have their largest element at 2^14 to 2^15 in f16, where bf16's eight
+bits are exact down to 2^-31 of it and the smallest step's half is 2^-39 of it:
+a score is off by scale 2^-39 max|q| sum |k_d|.
+The rest is test_gpu_decode's: ds = (D + 4) e scale sum |q k|, e = 2^-24,
+|do| <= (2 max ds + (n + 16) e + 2^-22) sum p |v| + the above + half a step of
+the output."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from long_context_sequence_seq_gb300 import ulysses as U
+from oracle import serving_oracle as so
+from tests.test_gpu_decode import CASES, DT, E, build, check, f64, widen
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(args):
+    """q, k, v of each sequence in fp64, and V's scales and codes, from the call's own tensors."""
+    tab = args["page_table"].cpu().numpy()
+    q = f64(args["q"])
+    q = q if args["layout"] == "seq" else q.transpose(1, 0, 2)
+    out = []
+    for b, n in enumerate(args["seq_lens"].tolist()):
+        got = []
+        for c, s in ((args["k_cache"], args["k_scale"]), (args["v_cache"], args["v_scale"])):
+            r = so.cache_rows(f64(c), tab, b, n)
+            w = so.cache_rows(f64(s)[..., None], tab, b, n)
+            got.append((r * w, w[..., 0], r))
+        out.append((q[b], got[0][0], got[1][0], got[1][1], got[1][2]))
+    return out
+
+
+def check_e4m3(o, lse, args):
+    o = f64(o)
+    o = o if args["layout"] == "seq" else o.transpose(1, 0, 2)
+    lse = f64(lse)
+    for b, (q, k, v, sv, cv) in enumerate(rows_of(args)):
+        Hq, D = q.shape
+        n, sc = len(k), 1.0 / math.sqrt(D)
+        ro, rl = so.decode(q, k, v)
+        if n == 0:
+            assert np.all(o[b] == 0) and np.all(np.isneginf(lse[b]))
+            continue
+        G = Hq // k.shape[1]
+        for h in range(Hq):
+            K, V = k[:, h // G], v[:, h // G]
+            ds = sc * ((D + 4) * E * (np.abs(K) @ np.abs(q[h])).max()
+                       + 2.0 ** -39 * np.abs(q[h]).max() * np.abs(K).sum(-1).max())
+            p = np.exp(sc * (K @ q[h]) - rl[h])
+            lim = (2 * ds + (n + 16) * E + 2.0 ** -22) * (p @ np.abs(V))
+            lim = lim + 2.0 ** -32 * (p * sv[:, h // G]).max() * np.abs(cv[:, h // G]).sum(0)
+            lim = lim + np.abs(ro[h]) * 2.0 ** -8 * 1.01 + 1e-37
+            err = np.abs(o[b, h] - ro[h])
+            assert np.all(err <= lim), (b, h, n, float((err / lim).max()))
+            assert abs(lse[b, h] - rl[h]) <= ds + (n + 16) * E + 2 * E * abs(rl[h]), (b, h, lse[b, h], rl[h])
+
+
+# ------------------------------------------------------------------ e4m3 weights
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,dtype,cache,layout",
+                         [c for c in CASES if c[5:7] == ("bf16", "e4m3")])
+def test_e4m3_weights_keep_more_than_f16(lens, Hq, Hkv, D, page, dtype, cache, layout):
+    args, _ = build(lens, Hq, Hkv, D, page, dtype, cache, layout, seed=20)
+    for x in (args, widen(args)):
+        o, lse = U.attn_decode(**x)
+        U.check()
+        check_e4m3(o, lse, x)
+
+
+@pytest.mark.parametrize("above", [10.0, 15.0, 18.0])
+@pytest.mark.parametrize("D,Hq", [(128, 8), (128, 16), (64, 24)])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_one_key_far_above_the_others(above, D, Hq, how):
+    """One key's score `above` nats over the others', its V row zero: the output
+    is the others' alone, weights of e^-above beside it."""
+    n = 700
+    args, _ = build([n], Hq, 2, D, 16, "bf16", "e4m3", "seq", seed=21)
+    tab = args["page_table"].cpu().numpy()
+    args["q"][..., 0] = 4.0
+    args["q"][..., 1:] *= 0.05
+    pg, sl = so.place(tab, 16, 0, 37)
+    kc, vc = args["k_cache"].float(), args["v_cache"].float()
+    kc[..., 0] = 0.0
+    kc[pg, :, sl] = 0.0
+    kc[pg, :, sl, 0] = 1.0
+    vc[pg, :, sl] = 0.0
+    args["k_cache"], args["v_cache"] = kc.to(DT["e4m3"]), vc.to(DT["e4m3"])
+    args["k_scale"][pg, :, sl] = above * math.sqrt(D) / 4.0
+    args["v_scale"][pg, :, sl] = 3.0 / 448.0                 # as of a row of usual size
+    if how == "split":
+        args = widen(args)
+    o, lse = U.attn_decode(**args)
+    U.check()
+    check_e4m3(o, lse, args)
