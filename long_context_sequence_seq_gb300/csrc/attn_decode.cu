@@ -41,9 +41,9 @@
 //                 S's layout to the operand's by movmatrix
 //   bf16 weights go in as a value and its rounding error (2^-16 instead of 2^-8:
 //   the output is then off by its own rounding alone, and the pipe has room).
-//   E4m3 codes become f16 exactly.  q is scaled by a power of two into f16's
-//   range (exact, but for elements 2^-24 below its largest); the rows' scales
-//   enter in fp32: K's times the score, V's in the weight, as
+//   E4m3 codes become f16 exactly.  q is scaled by a power of two to the top of
+//   f16's range (exact but for elements 2^-31 below its largest, which are off by
+//   2^-39 of that); the rows' scales enter in fp32: K's times the score, V's in the weight, as
 //   2^(s + log2 vs - M + 7) with a running maximum M of its own, so that the
 //   largest weights of a piece, whatever the rows' scales are, lie at 2^7 to 2^15
 //   of f16's range (below 2^16), and those 2^-32 below them are still held.
@@ -247,9 +247,9 @@ struct MatrixEngine {
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // the power of two below the head's largest element
+      // the power of two below the head's largest element comes to 2^14 (2^127 to 2^15: bf16 ends at 65280 then)
       int e = (int)(__float_as_uint(big) >> 23) - 127;
-      e = e < -100 ? -100 : (e > 126 ? 126 : e);
+      e = (e < -100 ? -100 : (e > 126 ? 126 : e)) - 14;
       const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
 #pragma unroll
       for (int i = 0; i < kN; ++i) {

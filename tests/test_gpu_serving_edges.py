@@ -103,3 +103,21 @@ def test_one_key_far_above_the_others(above, D, Hq, how):
     o, lse = U.attn_decode(**args)
     U.check()
     check_e4m3(o, lse, args)
+
+
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_queries_with_one_huge_element(how):
+    """An element 2^28 times the others, where K is zero: the scores are the
+    others' products."""
+    args, _ = build([400, 0, 33], 8, 2, 128, 16, "bf16", "e4m3", "seq", seed=22)
+    args["q"] *= 2.0 ** -9
+    args["q"][..., 5] = 2.0 ** 20
+    kc = args["k_cache"].float()
+    kc[..., 5] = 0.0
+    args["k_cache"] = kc.to(DT["e4m3"])
+    args["k_scale"] *= 2.0 ** 8
+    if how == "split":
+        args = widen(args)
+    o, lse = U.attn_decode(**args)
+    U.check()
+    check_e4m3(o, lse, args)
