@@ -415,7 +415,9 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * the table, and a page id outside [0, num_pages), are reported by
  * ulysses_check as ULYSSES_ERR_BAD_PAGES (the keys concerned are left out).
  * Results do not depend on the order in which the GPU runs the call's blocks.
- * Scales of an E4M3 cache are positive (or NaN).  With FP32 queries products
+ * Scales of an E4M3 cache are positive (or NaN).  An infinite element of V makes
+ * its output element infinite (NaN with both signs, or where its key's weight
+ * vanishes in fp32).  With FP32 queries products
  * are formed of two 11-bit parts of each operand: rounded as in fp32, but an
  * infinite element gives NaN (a K element in its key's score, a V element in
  * its output element).

@@ -39,8 +39,11 @@
 //     O^T += V^T P^T   it holds rows 2j, 2j+1, 2j+8, 2j+9, words g, g+8, ..; pairs
 //                 of rows are interleaved by byte permutes, and P turns from
 //                 S's layout to the operand's by movmatrix
-//   bf16 weights go in as a value and its rounding error (2^-16 instead of 2^-8:
-//   the output is then off by its own rounding alone, and the pipe has room).
+//   bf16 weights go in as a value and the rest (2^-16 instead of 2^-8: the output
+//   is then off by its own rounding alone, and the pipe has room).  The value is
+//   cut, not rounded, and the rest at least 2^-126 for a weight that is not zero:
+//   both are positive then, so an infinite V element gives infinity, as a rest of
+//   zero or below would not (0 x inf, inf - inf).
 //   E4m3 codes become f16 exactly.  q is scaled by a power of two to the top of
 //   f16's range (exact but for elements 2^-31 below its largest, which are off by
 //   2^-39 of that); the rows' scales enter in fp32: K's times the score, V's in the weight, as
@@ -76,6 +79,7 @@ constexpr int kUnit = 16;                       // keys of a unit
 constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr float kLazy = 8.f;                    // a maximum moves when exceeded by 2^8
 constexpr float kLift = 7.f;                    // f16 weights are 2^7 at the maximum, so at most 2^15
+constexpr float kTiny = 1.17549435082228751e-38f;   // 2^-126
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                       // of a CTA
 constexpr int kMinUnits = 2;                    // of a warp, where there are enough for all
@@ -442,10 +446,10 @@ struct MatrixEngine {
             const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
             lo = f32_to_f16x2(p0 - h.x, p1 - h.y);
           } else {
-            hi = f32_to_bf16x2(p0, p1);
+            hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
             float h[2];
             bf16x2_to_f32(hi, h);
-            lo = f32_to_bf16x2(p0 - h[0], p1 - h[1]);
+            lo = f32_to_bf16x2(fmaxf(p0 - h[0], fminf(p0, kTiny)), fmaxf(p1 - h[1], fminf(p1, kTiny)));
           }
           if (kTwice) {
             pb[t][x] = transpose8x8(j < 2 ? hi : lo);

@@ -121,3 +121,40 @@ def test_queries_with_one_huge_element(how):
     o, lse = U.attn_decode(**args)
     U.check()
     check_e4m3(o, lse, args)
+
+
+# ------------------------------------------------------------------ infinite V
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (8, 2, 64), (24, 2, 128), (2, 2, 128)])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+@pytest.mark.parametrize("simt", [False, True])
+def test_infinite_values_of_a_bf16_cache(Hq, Hkv, D, how, simt):
+    """Infinite V elements make their element of the output infinite, both signs
+    in one element NaN, and leave the others as they are."""
+    n = 300
+    args, _ = build([n, 40], Hq, Hkv, D, 16, "bf16", "bf16", "seq", seed=23)
+    tab = args["page_table"].cpu().numpy()
+    inf = float("inf")
+    clean = args["v_cache"].clone()
+    for d, keys in ((3, [(7, inf)]), (20, [(150, -inf)]), (41, [(9, inf), (280, -inf)]), (50, [(i, inf) for i in range(n)])):
+        for key, x in keys:
+            pg, sl = so.place(tab, 16, 0, key)
+            args["v_cache"][pg, 0, sl, d] = x
+            clean[pg, 0, sl, d] = 0.0
+    if how == "split":
+        args = widen(args)
+    U.set_kernel(U.KERNEL_SIMT if simt else U.KERNEL_AUTO)
+    try:
+        o, _ = U.attn_decode(**args)
+        want, _ = U.attn_decode(**{**args, "v_cache": clean})
+        U.check()
+    finally:
+        U.set_kernel(U.KERNEL_AUTO)
+    g = Hq // Hkv
+    mine = o[0, :g].float()
+    assert bool((mine[:, 3] == inf).all()) and bool((mine[:, 20] == -inf).all()), (mine[:, 3], mine[:, 20])
+    assert bool(torch.isnan(mine[:, 41]).all()) and bool((mine[:, 50] == inf).all())
+    left = torch.ones(D, dtype=torch.bool, device="cuda")
+    left[[3, 20, 41, 50]] = False
+    assert torch.equal(o[0, :g][:, left], want[0, :g][:, left])
+    assert torch.equal(o[0, g:], want[0, g:]) and torch.equal(o[1], want[1])
