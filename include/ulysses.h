@@ -405,7 +405,8 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  *   q    element (b, h, d) at q[b*q_b + h*q_h + d], H_q heads; head h reads kv
  *        head h / G, G = H_q / H_kv
  *   seq_lens [B] int32, device: the keys of sequence b are positions
- *        [0, seq_lens[b]); length 0 gives O = 0 and LSE = -inf
+ *        [0, seq_lens[b]); where none of them counts (length 0, every page out
+ *        of range, every score -inf), O = 0 and LSE = -inf
  *   o    written at o[b*o_b + h*o_h + d] in dtype;  lse [B][H_q] fp32 (or NULL)
  *   dtype BF16 with a BF16 or E4M3 cache, FP32 with an FP32 or E4M3 cache
  *   workspace  >= ulysses_attn_decode_workspace() bytes (0: may be NULL),

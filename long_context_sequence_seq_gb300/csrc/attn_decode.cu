@@ -159,6 +159,11 @@ struct Walk {
   }
 };
 
+// A sum over keys by the weights' sum.  Where no key counts (none on a good page,
+// or every score -inf) l is 0 and the output 0, as of a sequence without keys;
+// the sum itself may hold 0 x inf then.
+__device__ __forceinline__ float quotient(float s, float l) { return l == 0.f ? 0.f : s / l; }
+
 // ------------------------------------------------------------------ matrix engine
 
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -585,7 +590,7 @@ struct MatrixEngine {
           float f[kVE];
           values(t, c, w, f);
 #pragma unroll
-          for (int e = 0; e < kVE; ++e) f[e] *= inv;
+          for (int e = 0; e < kVE; ++e) f[e] = l[t][c] == 0.f ? 0.f : f[e] * inv;
 #pragma unroll
           for (int e = 0; e < kVE; e += 8) {
             Row8<TQ> y;
@@ -830,7 +835,10 @@ struct SplitEngine {
     const int hq = p.h * a.G + p.g0 + g;
     if (j == 0 && a.lse) a.lse[(int64_t)p.b * a.H_q + hq] = (m + log2f(l)) * kLn2;
     float* out = reinterpret_cast<float*>(a.o) + (int64_t)p.b * a.o_b + (int64_t)hq * a.o_h;
-    each_word(1.f / l, [&](int d, float4 v) { *reinterpret_cast<float4*>(out + d) = v; });
+    const bool none = l == 0.f;
+    each_word(1.f / l, [&](int d, float4 v) {
+      *reinterpret_cast<float4*>(out + d) = none ? make_float4(0.f, 0.f, 0.f, 0.f) : v;
+    });
   }
 };
 
@@ -1022,7 +1030,7 @@ struct SimtEngine {
       if (i == 0 && a.lse) a.lse[(int64_t)p.b * a.H_q + hq] = (m[g] + log2f(l[g])) * kLn2;
       TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)p.b * a.o_b + (int64_t)hq * a.o_h;
 #pragma unroll
-      for (int e = 0; e < E; ++e) d[LaneRow<TC, D>::element(e, i)] = from_f32<TQ>(acc[g][e] / l[g]);
+      for (int e = 0; e < E; ++e) d[LaneRow<TC, D>::element(e, i)] = from_f32<TQ>(quotient(acc[g][e], l[g]));
     }
   }
 };
@@ -1170,12 +1178,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
     using TQ = typename Engine::TQ;
     const int hq = pc.h * a.G + pc.g0 + hl;
     TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)pc.b * a.o_b + (int64_t)hq * a.o_h + c * 4;
-    const bool none = pc.len == 0;
-    d[0] = from_f32<TQ>(none ? 0.f : s.x / l);
-    d[1] = from_f32<TQ>(none ? 0.f : s.y / l);
-    d[2] = from_f32<TQ>(none ? 0.f : s.z / l);
-    d[3] = from_f32<TQ>(none ? 0.f : s.w / l);
-    if (c == 0 && a.lse) a.lse[(int64_t)pc.b * a.H_q + hq] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    d[0] = from_f32<TQ>(quotient(s.x, l));
+    d[1] = from_f32<TQ>(quotient(s.y, l));
+    d[2] = from_f32<TQ>(quotient(s.z, l));
+    d[3] = from_f32<TQ>(quotient(s.w, l));
+    if (c == 0 && a.lse) a.lse[(int64_t)pc.b * a.H_q + hq] = (m + log2f(l)) * kLn2;   // l = 0: -inf
   }
   __syncwarp();
   tc::cluster_sync();                                      // no CTA leaves while another reads its sums
@@ -1289,12 +1296,11 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
   } else if (lane >= kLanes) {
     return;
   }
-  const bool none = units == 0;
-  d[0] = from_f32<TQ>(none ? 0.f : x.s.x / x.l);
-  d[1] = from_f32<TQ>(none ? 0.f : x.s.y / x.l);
-  d[2] = from_f32<TQ>(none ? 0.f : x.s.z / x.l);
-  d[3] = from_f32<TQ>(none ? 0.f : x.s.w / x.l);
-  if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = none ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
+  d[0] = from_f32<TQ>(quotient(x.s.x, x.l));
+  d[1] = from_f32<TQ>(quotient(x.s.y, x.l));
+  d[2] = from_f32<TQ>(quotient(x.s.z, x.l));
+  d[3] = from_f32<TQ>(quotient(x.s.w, x.l));
+  if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = (x.m + log2f(x.l)) * kLn2;   // l = 0: -inf
 }
 
 // ------------------------------------------------------------------ host

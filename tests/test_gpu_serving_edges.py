@@ -158,3 +158,51 @@ def test_infinite_values_of_a_bf16_cache(Hq, Hkv, D, how, simt):
     left[[3, 20, 41, 50]] = False
     assert torch.equal(o[0, :g][:, left], want[0, :g][:, left])
     assert torch.equal(o[0, g:], want[0, g:]) and torch.equal(o[1], want[1])
+
+
+# ------------------------------------------------------------------ no key that counts
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32"), ("fp32", "e4m3")])
+@pytest.mark.parametrize("Hq", [2, 8])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+@pytest.mark.parametrize("simt", [False, True])
+def test_a_sequence_whose_pages_are_all_bad_is_empty(dtype, cache, Hq, how, simt):
+    """Its keys are left out, every one: O = 0 and LSE = -inf, as of length 0."""
+    n = 900
+    args, rows = build([40, n, 70], Hq, 2, 128, 16, dtype, cache, "seq", seed=24)
+    if how == "split":
+        args = widen(args)
+    args["page_table"][1] = -1
+    U.set_kernel(U.KERNEL_SIMT if simt else U.KERNEL_AUTO)
+    try:
+        o, lse = U.attn_decode(**args)
+    finally:
+        U.set_kernel(U.KERNEL_AUTO)
+    with pytest.raises(U.UlyssesError) as e:
+        U.check()
+    assert e.value.code == U.ERR_BAD_PAGES
+    assert bool((o[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
+    check(o[::2], lse[::2], rows[::2], dtype, cache, "seq", simt=simt)
+
+
+@pytest.mark.parametrize("dtype,Hq,simt", [("bf16", 8, False), ("bf16", 8, True), ("fp32", 2, False), ("fp32", 8, True)])
+@pytest.mark.parametrize("n", [1, 900])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_scores_of_minus_infinity_alone_are_empty(dtype, Hq, simt, n, how):
+    args, rows = build([40, n], Hq, 2, 128, 16, dtype, dtype, "seq", seed=25)
+    args["q"][1, :, 0] = 1.0
+    tab = args["page_table"].cpu().numpy()
+    for i in range(n):
+        pg, sl = so.place(tab, 16, 1, i)
+        args["k_cache"][pg, :, sl] = 0.0
+        args["k_cache"][pg, :, sl, 0] = float("-inf")
+    if how == "split":
+        args = widen(args)
+    U.set_kernel(U.KERNEL_SIMT if simt else U.KERNEL_AUTO)
+    try:
+        o, lse = U.attn_decode(**args)
+        U.check()
+    finally:
+        U.set_kernel(U.KERNEL_AUTO)
+    assert bool((o[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
+    check(o[:1], lse[:1], rows[:1], dtype, dtype, "seq", simt=simt)
