@@ -206,3 +206,22 @@ def test_scores_of_minus_infinity_alone_are_empty(dtype, Hq, simt, n, how):
         U.set_kernel(U.KERNEL_AUTO)
     assert bool((o[1] == 0).all()) and bool(torch.isneginf(lse[1]).all())
     check(o[:1], lse[:1], rows[:1], dtype, dtype, "seq", simt=simt)
+
+
+# ------------------------------------------------------------------ joins
+
+@pytest.mark.parametrize("dtype,cache,D", [("bf16", "bf16", 128), ("fp32", "fp32", 128), ("bf16", "e4m3", 64),
+                                           ("fp32", "fp32", 64)])
+@pytest.mark.parametrize("B,longest", [(6, 2100), (16, 900), (24, 700), (64, 330), (80, 300)])
+def test_every_way_to_join(dtype, cache, D, B, longest):
+    """192, 512, 768, 2048 and 2560 output rows of 32 heads each, from items
+    whose keys several warps walk, and an empty place."""
+    lens = [longest] + [1 + (i * 389) % longest for i in range(1, B)]
+    lens[B // 2] = 0
+    args, rows = build(lens, 32, 8, D, 16, dtype, cache, "head", seed=26)
+    args = widen(args)
+    o, lse = U.attn_decode(**args)
+    U.check()
+    check(o, lse, rows, dtype, cache, "head")
+    o2, lse2 = U.attn_decode(**args)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
