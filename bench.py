@@ -538,6 +538,12 @@ def cpu_baseline(w, cu_np, min_sample_s=7.5):
             "sample_seconds": dt}
 
 
+def select_kernels(U, world):
+    """Replicas on several GPUs run the attention forward without TMA multicast."""
+    if world > 1:
+        U.set_kernel(U.KERNEL_NO_MULTICAST)
+
+
 def gpu_arm(args):
     world = int(os.environ.get("WORLD_SIZE", "1"))
     rank = int(os.environ.get("RANK", "0"))
@@ -549,6 +555,7 @@ def gpu_arm(args):
     torch.cuda.set_device(dev)
     from long_context_sequence_seq_gb300 import ulysses as U
     U.lib()
+    select_kernels(U, world)
     w = workload_from_args(args)
     cu_np = inputs.workload_cu_seqlens(w)
     step = LayerStep(w, dev, cu_np)

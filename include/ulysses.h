@@ -74,9 +74,13 @@ enum {
 /* E4M3 is a type of cached rows only (ulysses_cache_write and its readers). */
 enum { ULYSSES_BF16 = 0, ULYSSES_FP32 = 1, ULYSSES_E4M3 = 2 };
 
-/* Kernel selection for diagnostics: AUTO picks the tcgen05 kernels for BF16
- * with D = 128 and the fp32 SIMT kernels otherwise; SIMT forces the latter. */
-enum { ULYSSES_KERNEL_AUTO = 0, ULYSSES_KERNEL_SIMT = 1 };
+/* Kernel selection: AUTO picks the tcgen05 kernels for BF16 with D = 128 and
+ * the fp32 SIMT kernels otherwise; SIMT forces the latter (for diagnostics).
+ * NO_MULTICAST is AUTO with each CTA of the attention forward loading its own
+ * K and V tiles instead of sharing them with a neighbour by TMA multicast: for
+ * programs that run on several GPUs at once, which AUTO is not for.  Results are
+ * the same. */
+enum { ULYSSES_KERNEL_AUTO = 0, ULYSSES_KERNEL_SIMT = 1, ULYSSES_KERNEL_NO_MULTICAST = 2 };
 
 /* ---------------------------------------------------------------------------
  * The layer with the all-to-alls folded into the attention kernels: on one
@@ -467,7 +471,7 @@ int ulysses_layer_bwd(const void* q_seq, const void* k_seq, const void* v_seq, c
  *   (ULYSSES_ERR_BAD_PAGES).  Returns ULYSSES_ERR_CUDA if the stream
  *   reports a CUDA error.
  * ulysses_last_error: message of the last failure on this thread ("" if none).
- * ulysses_set_kernel: ULYSSES_KERNEL_AUTO or ULYSSES_KERNEL_SIMT (process wide).
+ * ulysses_set_kernel: one of ULYSSES_KERNEL_* (process wide; AUTO at the start).
  * ulysses_launch_count: number of kernels this library has launched so far in
  *   this process (host-side counter).
  * ulysses_checked_build: 1 for the bounds-checked build of the library

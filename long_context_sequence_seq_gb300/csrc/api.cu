@@ -102,6 +102,7 @@ bool tc_fwd_supported(const AttnArgs& a);
 bool tc_bwd_supported(const AttnArgs& a);
 
 bool simt_chosen() { return g_kernel_choice.load() == ULYSSES_KERNEL_SIMT; }
+bool multicast_allowed() { return g_kernel_choice.load() != ULYSSES_KERNEL_NO_MULTICAST; }
 
 }  // namespace ulysses
 
@@ -234,10 +235,10 @@ int attn_shape(AttnArgs& a, int64_t S, int B, int H_q, int H_kv, int D, int P, i
 }
 
 bool use_tc_fwd(const AttnArgs& a) {
-  return g_kernel_choice.load() == ULYSSES_KERNEL_AUTO && tc_fwd_supported(a);
+  return !simt_chosen() && tc_fwd_supported(a);
 }
 bool use_tc_bwd(const AttnArgs& a) {
-  return g_kernel_choice.load() == ULYSSES_KERNEL_AUTO && tc_bwd_supported(a);
+  return !simt_chosen() && tc_bwd_supported(a);
 }
 
 int run_fwd(AttnArgs& a, cudaStream_t st) {
@@ -848,7 +849,7 @@ int ulysses_check(void* stream) {
 const char* ulysses_last_error(void) { return g_msg; }
 
 int ulysses_set_kernel(int which) {
-  if (which != ULYSSES_KERNEL_AUTO && which != ULYSSES_KERNEL_SIMT)
+  if (which != ULYSSES_KERNEL_AUTO && which != ULYSSES_KERNEL_SIMT && which != ULYSSES_KERNEL_NO_MULTICAST)
     return set_error(ULYSSES_ERR_INVALID, "unknown kernel choice %d", which);
   g_kernel_choice.store(which);
   return ULYSSES_OK;

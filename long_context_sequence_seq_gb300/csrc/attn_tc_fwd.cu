@@ -389,8 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Cluster size: two CTAs of q heads that share a kv head (same query tile)
 // share each K/V tile, each loading half of its rows and multicasting them to
-// the other; one CTA without GQA.
-inline int fwd_cluster(int G) { return G % 2 == 0 ? 2 : 1; }
+// the other; one CTA without GQA, and where the process runs on several GPUs
+// (ULYSSES_KERNEL_NO_MULTICAST).
+inline int fwd_cluster(int G) { return G % 2 == 0 && multicast_allowed() ? 2 : 1; }
 
 template <int D, int CL>
 int launch_fwd_dc(const AttnArgs& a, cudaStream_t st) {

@@ -131,5 +131,6 @@ struct DecodeArgs {
 size_t decode_workspace(const DecodeArgs& a);
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st);
 bool simt_chosen();                                                       // api.cu
+bool multicast_allowed();                                                 // api.cu
 
 }  // namespace ulysses

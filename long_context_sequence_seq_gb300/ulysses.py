@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(_PKG, "libulysses_checked.so" if os.environ.get("ULYSSES
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS, ERR_BOUNDS, ERR_BAD_PAGES = range(8)
 BF16, FP32, E4M3 = 0, 1, 2
 PAIRS_HALF, PAIRS_ADJACENT = 0, 1
-KERNEL_AUTO, KERNEL_SIMT = 0, 1
+KERNEL_AUTO, KERNEL_SIMT, KERNEL_NO_MULTICAST = 0, 1, 2
 
 _lib = None
 # C++ marshalling of the strided calls (_fastcall.so), bound to the loaded
