@@ -1,5 +1,5 @@
 """Build libulysses.so in-tree with nvcc for sm_103a (no cmake, no torch), and
-the C++ marshalling of the binding's small calls (_fastcall.so, g++).
+the C++ marshalling of the binding's small calls (_fastcall-*.so, g++).
 
 Each .cu file compiles to an object in parallel; one nvcc link makes the
 shared library.  The CUDA runtime is linked statically, and the driver's
@@ -27,10 +27,8 @@ LIB = os.path.join(PKG, "libulysses.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libulysses_checked.so")
 
-# Marshalling of the strided calls against this interpreter's torch; the binding
-# works without it, slower (see ulysses.py).
+# Marshalling of the strided calls; the binding works without it, slower.
 FAST_SRC = os.path.join(PKG, "csrc_py", "fastcall.cpp")
-FAST = os.path.join(PKG, "_fastcall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -89,32 +87,55 @@ def build(force: bool = False, verbose: bool = False, extra=None, checked: bool 
     return lib_path
 
 
+def fastcall_path() -> str:
+    """Where the marshalling for this interpreter and this torch is: it uses the
+    layouts of both, so another's, left in the tree, must not be taken for it."""
+    import torch
+    return os.path.join(PKG, f"_fastcall-{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+
+
 def build_fastcall(force: bool = False) -> str:
-    """Compile _fastcall.so with the host compiler, against the headers and
+    """Compile the marshalling with the host compiler, against the headers and
     libraries of the installed torch; raises with the compiler's words if that
-    fails."""
-    if not force and not _stale(FAST, [FAST_SRC, os.path.join(INCLUDE, "ulysses.h"), os.path.abspath(__file__)]):
-        return FAST
+    fails, and leaves none behind then."""
+    path = fastcall_path()
+    if not force and not _stale(path, [FAST_SRC, os.path.join(INCLUDE, "ulysses.h"), os.path.abspath(__file__)]):
+        return path
+    if os.path.exists(path):
+        os.remove(path)
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    tmp = FAST + ".tmp"
+    tmp = path + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
            FAST_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"compiling {FAST_SRC} failed: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"compiling {FAST_SRC} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, FAST)
-    return FAST
+    os.replace(tmp, path)
+    return path
+
+
+def try_build_fastcall(force: bool = False) -> str | None:
+    """build_fastcall; where it fails, its words on stderr and None: the calls
+    are then marshalled in Python."""
+    try:
+        return build_fastcall(force)
+    except RuntimeError as e:
+        print(f"warning: no C++ marshalling of the strided calls (Python's serves): {e}", file=sys.stderr)
+        return None
 
 
 if __name__ == "__main__":
-    build_fastcall(force="--force" in sys.argv)
+    try_build_fastcall(force="--force" in sys.argv)
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
                 extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else None, checked="--checked" in sys.argv))

@@ -12,10 +12,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import struct
 
 import torch
+
+from .build import fastcall_path
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # ULYSSES_CHECKED=1 loads the bounds-checked build of the same library
@@ -28,7 +31,7 @@ PAIRS_HALF, PAIRS_ADJACENT = 0, 1
 KERNEL_AUTO, KERNEL_SIMT, KERNEL_NO_MULTICAST = 0, 1, 2
 
 _lib = None
-# C++ marshalling of the strided calls (_fastcall.so), bound to the loaded
+# C++ marshalling of the strided calls (_fastcall-*.so), bound to the loaded
 # library; None where it has not been built: the Python marshalling serves then.
 _fast = None
 
@@ -122,13 +125,16 @@ def lib():
 
 
 def _bind_fast(L):
-    """Load the C++ marshalling, if it is there, and give it the library's
-    functions.  One built against another torch does not load: it is left out."""
+    """Load the C++ marshalling built for this interpreter and torch, if it is
+    there, and give it the library's functions."""
     global _fast
-    if not os.path.exists(os.path.join(_PKG, "_fastcall.so")):
+    path = fastcall_path()
+    if not os.path.exists(path):
         return
+    spec = importlib.util.spec_from_file_location(f"{__package__}._fastcall", path)
     try:
-        from . import _fastcall
+        _fastcall = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fastcall)
     except ImportError:
         return
     _fastcall.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
@@ -531,7 +537,7 @@ def layer_bwd_fused(q_seq, k_seq, v_seq, o_seq, do_seq, lse, P, head_chunk, cu_s
 # tensors, whichever is current, on `stream` or that device's current stream;
 # outputs and workspaces made here belong to that stream.
 # A call's kernels take a few microseconds at decode sizes.  Plain calls (no
-# stream given, everything as it should be) are marshalled by _fastcall.so; the
+# stream given, everything as it should be) are marshalled by _fastcall-*.so; the
 # Python below serves the others and says what is wrong with a call.  It reads
 # each tensor property once and makes no objects besides the results.
 
