@@ -335,14 +335,16 @@ int ulysses_attn_bwd_noalloc(const void* q_h, const void* k_h, const void* v_h, 
  *              must be distinct.  In place (dst == src, equal strides, equal
  *              types) is allowed; any other overlap is not.
  *   positions  [n_axes][B][S] int32, device; any values.  1 <= n_axes <= 4.
- *   inv_freq   [rot_dim / 2] double, HOST pointer, finite, read during the call.
+ *   inv_freq   [rot_dim / 2] double, HOST pointer, finite and at most 2^40 in
+ *              magnitude, read during the call.
  *   axes       [rot_dim / 2] int32, HOST pointer: the axis each pair turns by
  *              (NULL: axis 0).
  *   dtype, out_dtype  of src and dst: equal, or FP32 -> BF16 (rounded once).
  *   D in {64, 128}; rot_dim a multiple of 16, <= D; base pointers 16-byte
  *   aligned and strides multiples of 16 bytes.
  * Angles are formed as turns in 64-bit fixed point (pos * (inv_freq / (2 pi) *
- * 2^64) mod 2^64), so far positions lose nothing. */
+ * 2^64) mod 2^64, the factor right to its last unit), so far positions lose
+ * nothing. */
 enum { ULYSSES_PAIRS_HALF = 0, ULYSSES_PAIRS_ADJACENT = 1 };
 typedef struct {
   const void* src;

@@ -97,6 +97,24 @@ bool same_place(const Span& x, const Span& y) {
   return same;
 }
 
+constexpr double kMaxFreq = 1099511627776.0;   // 2^40
+
+// freq / 2 pi in units of 2^-64 of a turn, whole turns dropped: off by one unit
+// at most for |freq| <= 2^40.  A quotient in doubles is off by 2^-53 of itself,
+// which at position 2^31 is 2^-22 radians for freq = 1 and 1/4 for 2^20; so
+// 1 / 2 pi is held in two doubles and the product's rounding error kept.
+uint64_t turn_units(double freq) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi to 2^-111
+  constexpr double kUnits = 18446744073709551616.0;                            // 2^64
+  const double f = std::fabs(freq);
+  const volatile double whole = f * kHi;                       // rounded here, whatever the compiler contracts
+  const double p = whole, rest = std::fma(f, kHi, -p) + f * kLo;
+  const double units = (p - std::floor(p)) * kUnits;           // exact, below 2^64
+  const uint64_t n = (uint64_t)units;
+  const uint64_t u = n + (uint64_t)std::llround(rest * kUnits + (units - (double)n));
+  return freq < 0.0 ? 0 - u : u;
+}
+
 int rope(const ulysses_rope_item* items, int n_items, const int32_t* positions, int n_axes, const double* inv_freq,
          const int32_t* axes, int rot_dim, int pairs, int64_t S, int B, int D, int dtype, int out_dtype, int inverse,
          void* stream) {
@@ -119,10 +137,9 @@ int rope(const ulysses_rope_item* items, int n_items, const int32_t* positions, 
   a.half = rot_dim / 2;
   for (int i = 0; i < a.half; ++i) {
     if (!std::isfinite(inv_freq[i])) return set_error(ULYSSES_ERR_INVALID, "inv_freq[%d] is not finite", i);
-    const double turns = inv_freq[i] / 6.283185307179586476925286766559;
-    // a fraction of a turn in [0, 1), exact in 53 bits; 2^64 of them wrap to 0
-    const double frac = turns - std::floor(turns);
-    a.freq[i] = frac >= 1.0 ? 0 : (uint64_t)(frac * 18446744073709551616.0);
+    if (std::fabs(inv_freq[i]) > kMaxFreq)
+      return set_error(ULYSSES_ERR_UNSUPPORTED, "inv_freq[%d]=%g above 2^40", i, inv_freq[i]);
+    a.freq[i] = turn_units(inv_freq[i]);
     const int ax = axes ? axes[i] : 0;
     if (ax < 0 || ax >= n_axes) return set_error(ULYSSES_ERR_INVALID, "axes[%d]=%d outside [0, %d)", i, ax, n_axes);
     a.axis[i] = (uint8_t)ax;

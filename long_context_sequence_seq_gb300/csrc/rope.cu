@@ -5,7 +5,7 @@
 //
 // The angle of a far position needs more than fp32: at position 2^20 an fp32
 // product is off by 0.06 rad.  Here it is a turn in 64-bit fixed point: freq is
-// held as f / 2 pi * 2^64 (cut to an integer), the product with the integer
+// held as f / 2 pi * 2^64 (an integer, right to a unit), the product with the integer
 // position is taken mod 2^64, which drops whole turns exactly, and the top 32
 // bits are the turn in [-1/2, 1/2): two integer multiplies, no fp64 (which this
 // GPU runs at 1/60 of its fp32 rate).  sincospif of that turn is off by at most
