@@ -394,7 +394,8 @@ int ulysses_rope_bwd(const ulysses_rope_item* items, int n_items, const int32_t*
  *
  * A position outside the table, or a page id outside [0, num_pages), makes
  * ulysses_check return ULYSSES_ERR_BAD_PAGES, and a cu that does not rise from
- * 0 to at most T ULYSSES_ERR_BAD_SEQLENS; such tokens are skipped. */
+ * 0 to at most T ULYSSES_ERR_BAD_SEQLENS; such tokens, and those of a sequence
+ * whose range does not lie in [0, T], are skipped. */
 int ulysses_cache_write(const void* k, const void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h,
                         int64_t T, int B, const int32_t* cu_new, const int32_t* page_table, int table_cols,
                         const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,

@@ -42,7 +42,7 @@ __device__ __forceinline__ int64_t place_of(const CacheArgs& a, int64_t t, bool 
   if (a.cu) {
     b = doc_of(a.cu, a.B, t);
     const int64_t lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
-    if (t < lo || t >= hi) return -1;
+    if (t < lo || t >= hi || lo < 0 || hi > a.T) return -1;   // the last two reported by check_cu
     pos = write ? (int64_t)__ldg(a.lens + b) - (hi - t) : (a.lens ? (int64_t)__ldg(a.lens + b) : 0) + t - lo;
   } else {
     const int len = __ldg(a.lens + b);
@@ -62,7 +62,8 @@ __device__ __forceinline__ int64_t place_of(const CacheArgs& a, int64_t t, bool 
   return (int64_t)pg * a.H * a.page + (pos - (int64_t)col * a.page);
 }
 
-// cu[0] == 0, non-decreasing, cu[B] <= T; checked by the first CTA.
+// cu[0] == 0, non-decreasing, cu[B] <= T; checked by the first CTA.  A range that
+// does not lie in [0, T] shows in one of these.
 __device__ __forceinline__ void check_cu(const CacheArgs& a) {
   if (blockIdx.x != 0 || !a.cu) return;
   for (int i = threadIdx.x; i <= a.B; i += kThreads) {

@@ -1,4 +1,5 @@
-"""Rotary positions with large frequencies."""
+"""Rotary positions with large frequencies, and offsets that do not fit the
+tokens of a cache call."""
 import math
 from fractions import Fraction
 
@@ -34,3 +35,30 @@ def test_angles_of_large_frequencies(top):
     lim = np.tile(np.abs(u) + np.abs(v), 2) * c + 1e-38
     err = np.abs(G - want)
     assert np.all(err <= lim), float((err / lim).max())
+
+
+@pytest.mark.parametrize("cu,lens", [([0, 2, 7], [2, 5]), ([-3, 2, 4], [5, 2])])
+def test_sequences_whose_offsets_do_not_fit_are_skipped(cu, lens):
+    """A sequence that begins before the first token or ends behind the last is
+    reported and none of its tokens is stored or read; the other one's are."""
+    T, good = 4, 0 if cu[0] == 0 else 1
+    tab = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    kc, vc, _, _ = U.kv_cache(2, 16, 1, 64)
+    x = torch.randn((T, 1, 64), generator=torch.Generator().manual_seed(31)).add(100.0).bfloat16().cuda()
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    U.cache_write(x, x, kc, vc, tab, torch.tensor(lens, dtype=torch.int32, device="cuda"), cu_new=c)
+    with pytest.raises(U.UlyssesError) as e:
+        U.check()
+    assert e.value.code == U.ERR_BAD_SEQLENS
+    mine = slice(0, 2) if good == 0 else slice(2, 4)
+    for cache in (kc, vc):
+        assert torch.equal(cache[good, 0, :2], x[mine, 0]) and bool((cache[1 - good] == 0).all())
+    kc.fill_(5.0)
+    vc.fill_(5.0)
+    out = [torch.full((T, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    U.cache_read(kc, vc, tab, c, T, out=out)
+    with pytest.raises(U.UlyssesError) as e:
+        U.check()
+    assert e.value.code == U.ERR_BAD_SEQLENS
+    for y in out:
+        assert bool((y[mine] == 5.0).all()) and int((y == 7.0).sum()) == 2 * 64
