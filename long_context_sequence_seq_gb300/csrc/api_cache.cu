@@ -165,6 +165,7 @@ int rope(const ulysses_rope_item* items, int n_items, const int32_t* positions, 
   }
   if (S == 0 || n_items == 0) return ULYSSES_OK;
   if (!positions) return set_error(ULYSSES_ERR_INVALID, "NULL positions");
+  if (!aligned4(positions)) return set_error(ULYSSES_ERR_INVALID, "positions must be 4-byte aligned");
   if (a.heads > (1 << 20)) return set_error(ULYSSES_ERR_UNSUPPORTED, "rope: %d heads in one call", a.heads);
   for (int i = 0; i < n_items; ++i)
     for (int k = 0; k < n_items; ++k) {
@@ -204,8 +205,8 @@ int check_cache(int64_t num_pages, int page, int H_kv, int D, int B, int cols, i
   if ((cache_dtype == ULYSSES_E4M3) != (ks != nullptr) || (cache_dtype == ULYSSES_E4M3) != (vs != nullptr))
     return set_error(ULYSSES_ERR_INVALID, "scales go with an E4M3 cache, and only with one");
   if (num_pages && (!kc || !vc)) return set_error(ULYSSES_ERR_INVALID, "NULL cache");
-  if (!aligned16(kc) || !aligned16(vc) || ((uintptr_t)ks & 3u) || ((uintptr_t)vs & 3u))
-    return set_error(ULYSSES_ERR_INVALID, "caches must be 16-byte aligned");
+  if (!aligned16(kc) || !aligned16(vc) || !aligned4(ks) || !aligned4(vs))
+    return set_error(ULYSSES_ERR_INVALID, "caches must be 16-byte aligned, scales 4-byte");
   return ULYSSES_OK;
 }
 
@@ -218,6 +219,8 @@ int cache_args(CacheArgs& a, const void* k, const void* v, int64_t k_s, int64_t 
   if (T < 0 || T > kMaxTokens) return set_error(ULYSSES_ERR_INVALID, "bad token count %lld", (long long)T);
   if (T == 0 || B == 0) return ULYSSES_OK;
   if (!k || !v || !table) return set_error(ULYSSES_ERR_INVALID, "NULL buffer");
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(cu))
+    return set_error(ULYSSES_ERR_INVALID, "tables, lengths and offsets must be 4-byte aligned");
   if (!aligned16(k) || !aligned16(v)) return set_error(ULYSSES_ERR_INVALID, "buffers must be 16-byte aligned");
   Dim dk[2] = {{T, k_s}, {H, k_h}}, dv[2] = {{T, v_s}, {H, v_h}};
   const int e = elt_size(dtype);
@@ -315,6 +318,8 @@ int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_c
   if (B == 0) return ULYSSES_OK;
   if (!q || !o || !seq_lens || (table_cols && !page_table)) return set_error(ULYSSES_ERR_INVALID, "NULL buffer");
   if (!aligned16(q) || !aligned16(o)) return set_error(ULYSSES_ERR_INVALID, "buffers must be 16-byte aligned");
+  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(lse))
+    return set_error(ULYSSES_ERR_INVALID, "table, lengths and LSE must be 4-byte aligned");
   Dim dq[2] = {{B, q_b}, {H_q, q_h}}, dout[2] = {{B, o_b}, {H_q, o_h}};
   const int e = elt_size(dtype);
   if ((rc = check_strides(dq, 2, e, "q")) || (rc = check_strides(dout, 2, e, "o"))) return rc;

@@ -13,6 +13,7 @@ namespace ulysses {
 // Argument helpers of the C entry points.
 inline int elt_size(int dtype) { return dtype == ULYSSES_BF16 ? 2 : (dtype == ULYSSES_FP32 ? 4 : 0); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool overlap(const char* a, size_t la, const char* b, size_t lb) { return a < b + lb && b < a + la; }
 

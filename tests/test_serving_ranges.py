@@ -24,3 +24,22 @@ def test_frequencies_above_2_40(L, fn, f):
     assert getattr(L, f"ulysses_rope_{fn}")(items, 1, P(3 << 32), 1, freq, None, 64, 0, 4, 1, 64, U.BF16, U.BF16,
                                             None) == U.ERR_UNSUPPORTED
     assert b"inv_freq[31]" in L.ulysses_last_error() and L.ulysses_launch_count() == launches
+
+
+def test_pointers_of_32_bit_elements_are_aligned(L):
+    launches = L.ulysses_launch_count()
+    x, y, z, w, i = (P(n << 40) for n in range(1, 6))
+    for odd in (P((5 << 40) + 1), P((5 << 40) + 2)):
+        items = (U.RopeItem * 1)(U.RopeItem(1 << 32, 2 << 32, 2, 0, 128, 64, 0, 128, 64))
+        freq = (ctypes.c_double * 32)(*[1.0] * 32)
+        assert L.ulysses_rope_fwd(items, 1, odd, 1, freq, None, 64, 0, 4, 1, 64, U.BF16, U.BF16, None) == U.ERR_INVALID
+        for cu, table, lens in ((odd, i, i), (i, odd, i), (i, i, odd)):
+            assert L.ulysses_cache_write(x, y, 256, 128, 256, 128, 4, 4, cu, table, 8, lens, z, w, None, None, 64, 16, 2, 128,
+                                         U.BF16, U.BF16, None) == U.ERR_INVALID
+            assert L.ulysses_cache_read(z, w, None, None, table, 8, cu, lens, x, y, 256, 128, 256, 128, 4, 4, 64, 16, 2, 128,
+                                        U.BF16, U.BF16, None) == U.ERR_INVALID
+        for table, lens, lse in ((odd, i, i), (i, odd, i), (i, i, odd)):
+            assert L.ulysses_attn_decode(x, 512, 128, z, w, None, None, table, 8, lens, y, 512, 128, lse, 4, 4, 2, 128, 64, 16,
+                                         0.0, U.BF16, U.BF16, None, 0, None) == U.ERR_INVALID
+            assert b"4-byte" in L.ulysses_last_error()
+    assert L.ulysses_launch_count() == launches
