@@ -425,13 +425,15 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * Results do not depend on the order in which the GPU runs the call's blocks.
  * Scales of an E4M3 cache are positive (or NaN).  An infinite element of V makes
  * its output element infinite (NaN with both signs, or where its key's weight
- * vanishes in fp32).  With FP32 queries products
- * are formed of two 11-bit parts of each operand: rounded as in fp32, but an
- * infinite element gives NaN (a K element in its key's score, a V element in
- * its output element).
- * B * H_q <= 2^24; table_cols * page_size * H_kv (times H_q / H_kv / 16 where
- * that is more than one) <= 2^35; strides and alignment as for
- * ulysses_cache_write. */
+ * vanishes in fp32).  With FP32 queries of three heads a kv head or more (two
+ * with D = 64) products are formed of two 11-bit parts of each operand: within
+ * 2^-21 of the product, and the sums rounded as in fp32; an infinite element
+ * gives NaN there (a K element in its key's score, a V element in its output
+ * element).
+ * B * H_q <= 2^24; table_cols * page_size * H_kv * groups < 2^35, where groups =
+ * ceil(H_q / H_kv / n) with n = 16 for BF16 queries, 8 for FP32 ones, and under
+ * ULYSSES_KERNEL_SIMT 4 (2 for three heads); strides and alignment as for
+ * ulysses_cache_write, tables, lengths and LSE 4-byte aligned. */
 size_t ulysses_attn_decode_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
                                      int cache_dtype);
 int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,

@@ -1388,7 +1388,7 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   int batch = kMaxBatch;
   if (full > 0 && 2147483647 / full < batch) batch = (int)(2147483647 / full);
   if (batch == 0)
-    return set_error(ULYSSES_ERR_UNSUPPORTED, "attn_decode: table_cols * page_size * H_kv of one sequence above 2^35");
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "attn_decode: table_cols * page_size * H_kv * groups of one sequence at or above 2^35");
   for (int b0 = 0; b0 < a.B; b0 += batch) {
     DecodeArgs x = a;
     x.B = a.B - b0 < batch ? a.B - b0 : batch;

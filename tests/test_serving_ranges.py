@@ -43,3 +43,25 @@ def test_pointers_of_32_bit_elements_are_aligned(L):
                                          0.0, U.BF16, U.BF16, None, 0, None) == U.ERR_INVALID
             assert b"4-byte" in L.ulysses_last_error()
     assert L.ulysses_launch_count() == launches
+
+
+@pytest.mark.parametrize("dt,Hkv,G,kernel", [(U.BF16, 32, 16, "AUTO"), (U.BF16, 16, 17, "AUTO"), (U.FP32, 32, 8, "AUTO"),
+                                             (U.FP32, 16, 9, "AUTO"), (U.FP32, 16, 16, "AUTO"), (U.BF16, 16, 5, "SIMT"),
+                                             (U.FP32, 16, 3, "SIMT"), (U.FP32, 32, 1, "AUTO")])
+def test_units_of_one_sequence(L, dt, Hkv, G, kernel):
+    """2^30 positions, as many heads as make 2^35 with the groups the header names."""
+    n = 16 if dt == U.BF16 else 8
+    if kernel == "SIMT":
+        n = 2 if G == 3 else 4
+    assert (1 << 30) * Hkv * -(-G // n) == 1 << 35
+    launches = L.ulysses_launch_count()
+    x, y, z, w, i, ws = (P(m << 44) for m in range(1, 7))
+    Hq = Hkv * G
+    assert L.ulysses_set_kernel(getattr(U, f"KERNEL_{kernel}")) == U.OK
+    try:
+        rc = L.ulysses_attn_decode(x, Hq * 128, 128, z, w, None, None, i, 1 << 26, i, y, Hq * 128, 128, None, 1, Hq, Hkv, 128,
+                                   64, 16, 0.0, dt, dt, ws, 1 << 40, None)
+    finally:
+        L.ulysses_set_kernel(U.KERNEL_AUTO)
+    assert rc == U.ERR_UNSUPPORTED and b"2^35" in L.ulysses_last_error()
+    assert L.ulysses_launch_count() == launches
