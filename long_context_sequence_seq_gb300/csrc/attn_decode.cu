@@ -1296,11 +1296,16 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
   } else if (lane >= kLanes) {
     return;
   }
-  d[0] = from_f32<TQ>(quotient(x.s.x, x.l));
-  d[1] = from_f32<TQ>(quotient(x.s.y, x.l));
-  d[2] = from_f32<TQ>(quotient(x.s.z, x.l));
-  d[3] = from_f32<TQ>(quotient(x.s.w, x.l));
-  if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = (x.m + log2f(x.l)) * kLn2;   // l = 0: -inf
+  if (x.l == 0.f) {   // no key that counts; a branch: selects at each quotient made 25.9 us of 24 ragged x 4096 27.0
+    d[0] = d[1] = d[2] = d[3] = from_f32<TQ>(0.f);
+    if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = -INFINITY;
+    return;
+  }
+  d[0] = from_f32<TQ>(x.s.x / x.l);
+  d[1] = from_f32<TQ>(x.s.y / x.l);
+  d[2] = from_f32<TQ>(x.s.z / x.l);
+  d[3] = from_f32<TQ>(x.s.w / x.l);
+  if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = (x.m + log2f(x.l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
