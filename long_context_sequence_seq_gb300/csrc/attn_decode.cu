@@ -1356,6 +1356,12 @@ WsLayout ws_layout(const DecodeArgs& a, int heads) {
   return w;
 }
 
+// Reported here, and not left for the next call's check to find.
+int launch_failed(const char* what, cudaError_t err) {
+  (void)cudaGetLastError();
+  return set_error(ULYSSES_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
+}
+
 template <class Engine, int D, int kCtas>
 int run(const DecodeArgs& a, cudaStream_t st) {
   int dev = 0, sms = 148;
@@ -1379,7 +1385,7 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<Engine, D, kCtas>, a, p.groups, p.heads, c);
-    if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode: launch failed: %s", cudaGetErrorString(err));
+    if (err != cudaSuccess) return launch_failed("attn_decode", err);
     count_launch();
     return ULYSSES_OK;
   }
@@ -1430,7 +1436,7 @@ int run(const DecodeArgs& a, cudaStream_t st) {
                       : threads == 256                 ? decode_join_kernel<TQ, D, kRow, 256>
                                                        : decode_join_kernel<TQ, D, kRow, 128>;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, join, x, p);
-    if (err != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "attn_decode join: launch failed: %s", cudaGetErrorString(err));
+    if (err != cudaSuccess) return launch_failed("attn_decode join", err);
     count_launch();
   }
   return ULYSSES_OK;
