@@ -22,15 +22,15 @@
 // programmatic dependency so that its launch overlaps, adds each item's pieces
 // in the order of the warps.  No atomics, nothing to initialise.  (Measured:
 // one CTA an item instead, 64 ragged sequences of 512 to 32768 keys, bf16: 1846
-// us; this way 309 us for 2.10 GB, 102% of the measured copy rate.  A million
-// keys of one sequence in e4m3: 57.3 ms and 328 us for 2.21 GB, 101%.)
+// us; this way 305 to 313 us for 2.10 GB, 100 to 103% of the measured copy rate.
+// A million keys of one sequence in e4m3: 57.3 ms and 336 us for 2.21 GB, 98%.)
 // Where the page table has room for a few units a warp only, a cluster of CTAs
 // takes each item and joins through distributed shared memory: one launch.
 //
 // Three engines walk a piece.
 //   Matrix engine (bf16 queries): keys are the M = 16 side of mma m16n8k16 and
 //   the query heads of the group (up to 8 or 16) the N side.  The warp-level
-//   instruction leaves the pipe 85% idle, which is all that is asked of it, and
+//   instruction leaves the pipe 83 to 91% idle, which is all that is asked of it, and
 //   its register operands take rows straight from global memory, since the
 //   contraction may run over d in any order that Q shares: no shared memory,
 //   no barrier, no copy (tcgen05 reads its operands from shared memory).  Rows
@@ -50,19 +50,20 @@
 //   2^(s + log2 vs - M + 7) with a running maximum M of its own, so that the
 //   largest weights of a piece, whatever the rows' scales are, lie at 2^7 to 2^15
 //   of f16's range (below 2^16), and those 2^-32 below them are still held.
-//   They go in as a value and its rounding error too, 2^-22; as a value alone
-//   (2^-12) the output of a million keys differed from fp32 arithmetic's by
-//   8.8e-4 in norm.
+//   They go in as a value and its rounding error too, 2^-22: the output of a
+//   million keys differs from fp32 arithmetic's by 1.6e-4 in norm, roundings of
+//   the output itself; as a value alone (2^-12) by 8.8e-4.
 //   Split engine (fp32 queries, from two or three heads on): fp32 operands as two
 //   11-bit parts on the tf32 pipe; heads are the M side, the high parts of up
 //   to 8 in its rows 0-7 and their low parts in rows 8-15, so one instruction
 //   multiplies both by a part of K or V, and two make the product to 2^-21.  A
 //   step's products are summed from zero and added in fp32: left to accumulate
-//   in the pipe, which cuts instead of rounding, 8 x 30000 keys were 7.5e-6 off
-//   (2-norm) in 338 us; this way 7.8e-7, less than plain fp32, in 392 us (75% of
-//   the copy rate).
+//   in the pipe, which cuts instead of rounding, 8 x 30000 keys (8 kv heads of
+//   128, 4 query heads each: 1.97 GB) were 7.5e-6 off (2-norm) in 338 us; this way
+//   7.8e-7, less than plain fp32, in 394 us (75% of the copy rate).
 //   SIMT engine (fp32 queries of one head or two, and by choice): FMA
-//   throughout, 8 lanes a key.  (8 x 8000 keys, 1 head of 128: 83 us, 95%.)
+//   throughout, 8 lanes a key.  (8 x 8000 keys, 8 kv heads of 128 with a query
+//   head each, 0.52 GB: 81 us, 97%.)
 #include "internal.h"
 #include "rows.cuh"
 #include "tc_ptx.cuh"
@@ -555,8 +556,7 @@ struct MatrixEngine {
       f[2 * e + 1] = acc[t][w * (kVE / 2) + e][c + 2];
     }
   }
-  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
-    (void)heads;
+  __device__ __forceinline__ void partial(float2* ml, float* o, int gn) const {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -824,8 +824,7 @@ struct SplitEngine {
                              (acc[e + 2][x] + acc[e + 2][x + 2]) * by, (acc[e + 3][x] + acc[e + 3][x + 2]) * by));
       }
   }
-  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
-    (void)heads;
+  __device__ __forceinline__ void partial(float2* ml, float* o, int gn) const {
     if (g >= gn) return;
     if (j == 0) ml[g] = make_float2(m, l);
     each_word(1.f, [&](int d, float4 v) { *reinterpret_cast<float4*>(o + g * D + d) = v; });
@@ -1010,8 +1009,7 @@ struct SimtEngine {
       }
     }
   }
-  __device__ __forceinline__ void partial(float2* ml, float* o, int heads, int gn) const {
-    (void)heads;
+  __device__ __forceinline__ void partial(float2* ml, float* o, int gn) const {
     if (grp != 0) return;
 #pragma unroll
     for (int g = 0; g < HG; ++g) {
@@ -1122,7 +1120,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
       e.result(a, pc);
     } else {
       const int64_t slot = 2 * w + (at == begin ? 0 : 1);
-      e.partial(p.ml + slot * p.heads, p.o + slot * p.heads * D, p.heads, pc.gn);
+      e.partial(p.ml + slot * p.heads, p.o + slot * p.heads * D, pc.gn);
     }
     at += pc.units;
   }
@@ -1152,7 +1150,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   Engine e(lane);
   e.begin(a, pc);
   if (pc.units > 0) e.run(a, pc);
-  e.partial(sml[warp], &so[warp][0][0], kH, pc.gn);
+  e.partial(sml[warp], &so[warp][0][0], pc.gn);
   __syncwarp();
   tc::cluster_sync();
   const int total = pc.gn * D / 4, each = (total + ctas - 1) / ctas;
@@ -1313,9 +1311,11 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
 constexpr int kMaxWarps = 152 * 16;              // of a launch: slots of the workspace
 
 // fp32 queries of few heads a key are SIMT work: at 1-2 flops a byte the FMA
-// pipe keeps up.  1 head of 128 (8 x 30000 keys): 283 us, 96% of the copy rate;
-// 2 of 128 (8 x 8000): 87 us, 98 by the fp32 matrix engine; but 2 of 64 (8 x
-// 30000) 203 and 186 us, 3 of 128 578 and 392, 8 of 128 734 and 393.
+// pipe keeps up.  8 kv heads, 8 x 30000 keys, 1.97 GB of D = 128: 1 query head a
+// kv head 279 us (105% of the copy rate), 2 291 (101%; 8 x 8000 keys 85, and 98 by
+// the fp32 matrix engine); 3 heads 569 by SIMT and 394 by the matrix engine, 4 374
+// and 394, 8 734 and 394.  0.98 GB of D = 64: 1 head 166, 2 205 and 186, 4 304 and
+// 186.
 bool use_simt(const DecodeArgs& a, bool chosen) {
   return chosen || (a.dtype == ULYSSES_FP32 && a.G <= (a.D == 128 ? 2 : 1));
 }
@@ -1328,12 +1328,14 @@ int heads_of(const DecodeArgs& a, bool simt) {
 }
 
 // CTAs of a cluster for each item, or 0: split the keys over the whole launch.
-// A cluster saves the join and its launch, but waits for the longest item: it
-// pays while its warps have at most kClusterUnits units when the table is full
-// and all clusters are resident at once (8 kv heads of 4: 1 x 777 keys 7.2 us
-// by clusters, 8.5 split; 1 x 6000 13.1 and 12.5, but a launch and a workspace
-// less; 16 x 4000 ragged 32.7 and 19.5, 4 x 16000 ragged 37.0 and 22.2, which
-// twice as many units would take).
+// A cluster saves the join, its launch and a workspace, but waits for the longest
+// item: it is taken while its warps have at most kClusterUnits units when the
+// table is full and all clusters are resident at once.  (8 kv heads of 4, one
+// sequence, clusters and split: 777 keys 7.2 and 9.2 us, 3000 9.5 and 10.8, 4500
+// 11.3 and 11.8, 6000 13.6 and 13.1, 8000 17.0 and 13.6: on time alone they part at
+// 5000 keys.  16 x 4000 ragged 32.7 and 19.5, 4 x 16000 ragged 37.0 and 22.2, which
+// twice as many units would take.)  152 SMs and not the device's: the workspace is
+// asked for without one, and both have to choose alike.
 constexpr int kClusterUnits = 16;
 int cluster_of(const DecodeArgs& a, int heads) {
   const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);

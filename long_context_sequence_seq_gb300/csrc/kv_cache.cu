@@ -17,7 +17,8 @@
 // with a division for each row took 186 us where this takes 130 (131072 tokens
 // of 8 heads of 128, bf16 to e4m3, K and V: 814 MB, 94% of the measured copy
 // rate), so bf16 maxima are taken two at a time and one pair of divisions
-// serves four rows.  Reading 65536 such tokens back: 65 us (407 MB, 93%).
+// serves four rows.  Reading 65536 such tokens back: 65 us (407 MB, 93%).  (GPU
+// times; a call among others takes 132 and 67 us.)
 #include "internal.h"
 #include "rows.cuh"
 
