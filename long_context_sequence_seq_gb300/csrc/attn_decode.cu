@@ -39,17 +39,17 @@
 //     O^T += V^T P^T   it holds rows 2j, 2j+1, 2j+8, 2j+9, words g, g+8, ..; pairs
 //                 of rows are interleaved by byte permutes, and P turns from
 //                 S's layout to the operand's by movmatrix
-//   bf16 weights go in as a value and the rest (2^-16 instead of 2^-8: the output
-//   is then off by its own rounding alone, and the pipe has room).  The value is
-//   cut, not rounded, and the rest at least 2^-126 for a weight that is not zero:
-//   both are positive then, so an infinite V element gives infinity, as a rest of
+//   bf16 weights go in as three parts, which hold all 24 bits: the output is then
+//   off by fp32 arithmetic and its own rounding alone, and the pipe has room.  The
+//   parts are cut, not rounded, and at least 2^-126 for a weight that is not zero:
+//   all are positive then, so an infinite V element gives infinity, as a part of
 //   zero or below would not (0 x inf, inf - inf).
 //   E4m3 codes become f16 exactly.  q is scaled by a power of two to the top of
 //   f16's range (exact but for elements 2^-31 below its largest, which are off by
-//   2^-39 of that); the rows' scales enter in fp32: K's times the score, V's in the weight, as
-//   2^(s + log2 vs - M + 7) with a running maximum M of its own, so that the
-//   largest weights of a piece, whatever the rows' scales are, lie at 2^7 to 2^15
-//   of f16's range (below 2^16), and those 2^-32 below them are still held.
+//   2^-39 of that); the rows' scales enter in fp32: K's times the score, V's in
+//   the weight, as 2^(s + log2 vs - M + 7) with a running maximum M of its own, so
+//   that the largest weights of a piece, whatever the rows' scales are, lie at 2^7
+//   to 2^15 of f16's range (below 2^16), and those 2^-32 below are still held.
 //   They go in as a value and its rounding error too, 2^-22: the output of a
 //   million keys differs from fp32 arithmetic's by 1.6e-4 in norm, roundings of
 //   the output itself; as a value alone (2^-12) by 8.8e-4.
@@ -203,6 +203,7 @@ template <bool kQuant, int D, int NT, bool kTwice>
 struct MatrixEngine {
   using TQ = __nv_bfloat16;
   static constexpr int kHeads = kTwice ? 4 : 8 * NT;
+  static constexpr int kProducts = (kQuant ? 2 : 3) - (kTwice ? 1 : 0);   // with V for a step's weights
   static constexpr int kRowB = kQuant ? D : 2 * D;        // bytes of a row
   static constexpr int kSub = kRowB == 256 ? 1 : 2;       // units of a step: 32 registers of K and of V, or 16
   static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
@@ -340,6 +341,27 @@ struct MatrixEngine {
     return e4m3x2_to_f16x2((uint16_t)(w[e2 >> 1] >> (16 * (e2 & 1))));
   }
 
+  // The 16-bit parts of two weights, largest first: they add up to the weight.
+  // The third goes into both columns of a head with kTwice, so half of it.
+  __device__ __forceinline__ static void parts(float p0, float p1, uint32_t (&part)[3]) {
+    if (kQuant) {
+      part[0] = f32_to_f16x2(p0, p1);
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&part[0]));
+      part[1] = f32_to_f16x2(p0 - h.x, p1 - h.y);
+      return;
+    }
+    const float t0 = fminf(p0, kTiny), t1 = fminf(p1, kTiny);
+    float h[2];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (k == 2 && kTwice) { p0 = fmaxf(0.5f * p0, t0); p1 = fmaxf(0.5f * p1, t1); }
+      part[k] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);   // cut to bf16
+      bf16x2_to_f32(part[k], h);
+      p0 = fmaxf(p0 - h[0], t0);
+      p1 = fmaxf(p1 - h[1], t1);
+    }
+  }
+
   // two sums of half the row each: half the chain of dependent products
   __device__ __forceinline__ void scores(const Rows& r, int u, float (&s)[NT][4]) {
     float h[2][NT][4];
@@ -440,28 +462,20 @@ struct MatrixEngine {
       }
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
-      uint32_t pb[NT][2], pl[NT][2];                       // weights, and what their rounding left
+      uint32_t pw[kProducts][NT][2];                       // the weights' parts
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float p0 = s[u][t][2 * x], p1 = s[u][t][2 * x + 1];
-          uint32_t hi, lo;
-          if (kQuant) {
-            hi = f32_to_f16x2(p0, p1);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            lo = f32_to_f16x2(p0 - h.x, p1 - h.y);
-          } else {
-            hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
-            float h[2];
-            bf16x2_to_f32(hi, h);
-            lo = f32_to_bf16x2(fmaxf(p0 - h[0], fminf(p0, kTiny)), fmaxf(p1 - h[1], fminf(p1, kTiny)));
-          }
+          uint32_t part[3];
+          parts(p0, p1, part);
           if (kTwice) {
-            pb[t][x] = transpose8x8(j < 2 ? hi : lo);
+            pw[0][t][x] = transpose8x8(j < 2 ? part[0] : part[1]);
+            if (!kQuant) pw[kProducts - 1][t][x] = transpose8x8(part[2]);
           } else {
-            pb[t][x] = transpose8x8(hi);
-            pl[t][x] = transpose8x8(lo);
+#pragma unroll
+            for (int k = 0; k < kProducts; ++k) pw[k][t][x] = transpose8x8(part[k]);
           }
         }
 #pragma unroll
@@ -475,13 +489,10 @@ struct MatrixEngine {
                                  __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float* sum = acc[t][w * (kVE / 2) + e];
-            if (kQuant) {
-              mma_f16(sum, f, pb[t][0], pb[t][1]);
-              if (!kTwice) mma_f16(sum, f, pl[t][0], pl[t][1]);
-            } else {
-              mma_bf16(sum, f, pb[t][0], pb[t][1]);
-              if (!kTwice) mma_bf16(sum, f, pl[t][0], pl[t][1]);
+#pragma unroll
+            for (int k = 0; k < kProducts; ++k) {
+              if (kQuant) mma_f16(acc[t][w * (kVE / 2) + e], f, pw[k][t][0], pw[k][t][1]);
+              else mma_bf16(acc[t][w * (kVE / 2) + e], f, pw[k][t][0], pw[k][t][1]);
             }
           }
         }

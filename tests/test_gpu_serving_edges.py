@@ -225,3 +225,35 @@ def test_every_way_to_join(dtype, cache, D, B, longest):
     check(o, lse, rows, dtype, cache, "head")
     o2, lse2 = U.attn_decode(**args)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------------ roundings of bf16 outputs
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [2, 5])
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (16, 8, 64), (64, 8, 128), (32, 2, 64)])
+@pytest.mark.parametrize("how", ["cluster", "split"])
+def test_outputs_are_rounded_from_fp32_sums(cache, n, Hq, Hkv, D, how):
+    """Few keys and small scores, so that fp32 arithmetic is within
+    lim = (2 max ds + (n + 16) e + 2^-22) sum p |v| of the output (the last term an
+    e4m3 cache's), about 2^-19 of it: every element is one that bf16 rounds a value
+    within lim of the definition's to, and not the next."""
+    B = 48
+    args, rows = build([n] * B, Hq, Hkv, D, 16, "bf16", cache, "seq", seed=27)
+    args["q"] = (args["q"].float() * 0.02).bfloat16()
+    if how == "split":
+        args = widen(args)
+    o, _ = U.attn_decode(**args)
+    U.check()
+    got, sc = f64(o), 1.0 / math.sqrt(D)
+    low, high = np.empty_like(got), np.empty_like(got)
+    for b, (_, k, v) in enumerate(rows):
+        q = f64(args["q"][b])
+        ro, rl = so.decode(q, k, v)
+        for h in range(Hq):
+            K, V = k[:, h * Hkv // Hq], v[:, h * Hkv // Hq]
+            ds = sc * (D + 4) * E * (np.abs(K) @ np.abs(q[h])).max()
+            lim = (2 * ds + (n + 16) * E + (2.0 ** -22 if cache == "e4m3" else 0.0)) * (np.exp(sc * (K @ q[h]) - rl[h]) @ np.abs(V))
+            low[b, h], high[b, h] = ro[h] - lim, ro[h] + lim
+    low, high = (f64(torch.from_numpy(x).to(torch.bfloat16)) for x in (low, high))
+    assert np.all((low <= got) & (got <= high)), int(np.sum((got < low) | (got > high)))
