@@ -22,17 +22,18 @@
 // programmatic dependency so that its launch overlaps, adds each item's pieces
 // in the order of the warps.  No atomics, nothing to initialise.  (Measured:
 // one CTA an item instead, 64 ragged sequences of 512 to 32768 keys, bf16: 1846
-// us; this way 305 to 313 us for 2.10 GB, 100 to 103% of the measured copy rate.
-// A million keys of one sequence in e4m3: 57.3 ms and 336 us for 2.21 GB, 98%.)
+// us; this way 305 to 314 us for 2.10 GB, 100 to 103% of the measured copy rate.
+// A million keys of one sequence in e4m3: 57.3 ms and 337 us for 2.21 GB, 98%, or
+// 344 as a call among others.)
 // Where the page table has room for a few units a warp only, a cluster of CTAs
 // takes each item and joins through distributed shared memory: one launch.
 //
 // Three engines walk a piece.
 //   Matrix engine (bf16 queries): keys are the M = 16 side of mma m16n8k16 and
 //   the query heads of the group (up to 8 or 16) the N side.  The warp-level
-//   instruction leaves the pipe 83 to 91% idle, which is all that is asked of it, and
-//   its register operands take rows straight from global memory, since the
-//   contraction may run over d in any order that Q shares: no shared memory,
+//   instruction leaves the pipe 83% idle or more, which is all that is asked of
+//   it, and its register operands take rows straight from global memory, since
+//   the contraction may run over d in any order that Q shares: no shared memory,
 //   no barrier, no copy (tcgen05 reads its operands from shared memory).  Rows
 //   stay in the lanes that loaded them:
 //     S = K Q^T   lane (g, j) holds rows g and g + 8, the 16-byte words j, j+4, ..
@@ -53,6 +54,12 @@
 //   They go in as a value and its rounding error too, 2^-22: the output of a
 //   million keys differs from fp32 arithmetic's by 1.6e-4 in norm, roundings of
 //   the output itself; as a value alone (2^-12) by 8.8e-4.
+//   Sums stay in the pipe's fp32 accumulators over a piece, which it cuts where an
+//   fp32 addition rounds: after thousands of keys that shows in the last rounding
+//   of some outputs (64 x 16384 keys: 1.9e-4 in norm off the definition rounded to
+//   bf16, plain fp32 1.0e-4, beside the rounding's own 1.7e-3).  A step's sums added
+//   in fp32 instead, 4.4e-5, cost registers: a million e4m3 keys 396 us, not 343,
+//   16 bf16 heads a kv head 70, not 66.
 //   Split engine (fp32 queries, from two or three heads on): fp32 operands as two
 //   11-bit parts on the tf32 pipe; heads are the M side, the high parts of up
 //   to 8 in its rows 0-7 and their low parts in rows 8-15, so one instruction
@@ -194,11 +201,12 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, as exp2f, with
 }
 
 // kTwice: up to 4 heads a group, each in two columns of the N side, h and h + 4;
-// the scores of both are the same, and the first takes the weights and the
-// second what their rounding left, so one product has both.  (A million e4m3
-// keys, 4 heads a kv head: 343 us; with two products 390, and with weights as a
-// value alone 339.  Groups of more heads have no columns left: 8 ragged
-// sequences of up to 30000 e4m3 keys, 8 heads a kv head, 46 us, a value alone 42.)
+// the scores of both are the same, and the first takes the weights' first part
+// and the second their second, so one product has both (in bf16 a further one the
+// third).  (A million e4m3 keys, 4 heads a kv head: 343 us; with two products 390,
+// and with weights as a value alone 339.  Groups of more heads have no columns
+// left: 8 ragged sequences of up to 30000 e4m3 keys, 8 heads a kv head, 45 us, a
+// value alone 42; 16 heads 54 and 50.  In bf16 parts cost no time.)
 template <bool kQuant, int D, int NT, bool kTwice>
 struct MatrixEngine {
   using TQ = __nv_bfloat16;
