@@ -71,8 +71,8 @@ enum {
   ULYSSES_ERR_BAD_PAGES = 7
 };
 
-/* E4M3 is a type of cached rows only (ulysses_cache_write and its readers). */
-enum { ULYSSES_BF16 = 0, ULYSSES_FP32 = 1, ULYSSES_E4M3 = 2 };
+/* E4M3 and E2M1 are types of cached rows only (ulysses_cache_write and its readers). */
+enum { ULYSSES_BF16 = 0, ULYSSES_FP32 = 1, ULYSSES_E4M3 = 2, ULYSSES_E2M1 = 3 };
 
 /* Kernel selection: AUTO picks the tcgen05 kernels for BF16 with D = 128 and
  * the fp32 SIMT kernels otherwise; SIMT forces the latter (for diagnostics).
@@ -364,7 +364,13 @@ int ulysses_rope_bwd(const ulysses_rope_item* items, int n_items, const int32_t*
  * Paged key-value cache: rows of D values in pages of page_size tokens,
  *   k_cache, v_cache  [num_pages][H_kv][page_size][D] in cache_dtype
  *   k_scale, v_scale  [num_pages][H_kv][page_size] fp32 for ULYSSES_E4M3 (the
- *                     row's value is code * scale), NULL otherwise
+ *                     row's value is code * scale) and ULYSSES_E2M1, NULL
+ *                     otherwise
+ * ULYSSES_E2M1 holds 9 D / 16 bytes a row: a page of a head is its rows' codes
+ * ([page_size][D / 2] bytes; element 2i in the low half of byte i, 2i + 1 in the
+ * high half; bit 3 the sign, bits 0-2 one of 0, 1/2, 1, 3/2, 2, 3, 4, 6) and
+ * behind them their block scales ([page_size][D / 16] bytes of e4m3, one for 16
+ * elements); a value is code * block scale * row scale.
  *   page_table        [B][table_cols] int32, device: token p of sequence b is
  *                     row p % page_size of page page_table[b][p / page_size];
  *                     entries past a sequence's last page are never read
@@ -383,14 +389,19 @@ int ulysses_rope_bwd(const ulysses_rope_item* items, int n_items, const int32_t*
  *   cache_dtype == dtype stores the rows as they are; ULYSSES_E4M3 stores
  *   scale = max(max|x|, 2^-100) / 448 and code = e4m3(x * (448 / max(...))),
  *   round to nearest even; a row with an infinity or NaN gets scale NaN, so it
- *   reads back as NaN.
+ *   reads back as NaN.  ULYSSES_E2M1 stores scale = the least power of two with
+ *   max(max|x|, 2^-100) <= 2688 * scale, b = e4m3(max of the block's |x / scale|
+ *   / 6) and code = e2m1(x / scale / b) (0 where b is 0), all to nearest even;
+ *   infinities and NaN as with ULYSSES_E4M3.
  *   The tokens of one call must have distinct places (a page owned by two
  *   sequences must not be written through both in one call).
  *
  * ulysses_cache_read gathers rows back: token t of the packed outputs, in
  *   sequence b (cu[b] <= t < cu[b+1]), is position first[b] + t - cu[b]
  *   (first NULL: 0).  Rows from cu[B] on are left as they were.  dtype is the
- *   cache's type, or BF16/FP32 for ULYSSES_E4M3 (code * scale, rounded once).
+ *   cache's type, or BF16/FP32 for ULYSSES_E4M3 (code * scale, rounded once)
+ *   and ULYSSES_E2M1 (exact but for values below the type's smallest normal one;
+ *   magnitudes above 2^127 may come back as infinities).
  *
  * A position outside the table, or a page id outside [0, num_pages), makes
  * ulysses_check return ULYSSES_ERR_BAD_PAGES, and a cu that does not rise from
@@ -401,6 +412,13 @@ int ulysses_cache_write(const void* k, const void* v, int64_t k_s, int64_t k_h, 
                         const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                         int64_t num_pages, int page_size, int H_kv, int D, int dtype, int cache_dtype,
                         void* stream);
+/* ulysses_cache_write, which also sets the weights (ulysses_attn_decode_weights)
+ * of the tokens that it stores to 0, whatever a slot's last token left there. */
+int ulysses_cache_write_weights(const void* k, const void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h,
+                                int64_t T, int B, const int32_t* cu_new, const int32_t* page_table, int table_cols,
+                                const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                float* weights, int64_t num_pages, int page_size, int H_kv, int D, int dtype,
+                                int cache_dtype, void* stream);
 int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                        const int32_t* page_table, int table_cols, const int32_t* cu, const int32_t* first,
                        void* k, void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h, int64_t T, int B,
@@ -415,7 +433,8 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  *        [0, seq_lens[b]); where none of them counts (length 0, every page out
  *        of range, every score -inf), O = 0 and LSE = -inf
  *   o    written at o[b*o_b + h*o_h + d] in dtype;  lse [B][H_q] fp32 (or NULL)
- *   dtype BF16 with a BF16 or E4M3 cache, FP32 with an FP32 or E4M3 cache
+ *   dtype BF16 with a BF16, E4M3 or E2M1 cache, FP32 with an FP32, E4M3 or E2M1
+ *        cache
  *   workspace  >= ulysses_attn_decode_workspace() bytes (0: may be NULL),
  *        256-byte aligned, contents need no init; calls that share one must
  *        not overlap on the GPU
@@ -423,7 +442,7 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * the table, and a page id outside [0, num_pages), are reported by
  * ulysses_check as ULYSSES_ERR_BAD_PAGES (the keys concerned are left out).
  * Results do not depend on the order in which the GPU runs the call's blocks.
- * Scales of an E4M3 cache are positive (or NaN).  An infinite element of V makes
+ * Row scales of an E4M3 or E2M1 cache are positive (or NaN).  An infinite element of V makes
  * its output element infinite (NaN with both signs, or where its key's weight
  * vanishes in fp32).  With FP32 queries of three heads a kv head or more (two
  * with D = 64) products are formed of two 11-bit parts of each operand: within
@@ -441,6 +460,46 @@ int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_c
                         const int32_t* seq_lens, void* o, int64_t o_b, int64_t o_h, float* lse, int B, int H_q,
                         int H_kv, int D, int64_t num_pages, int page_size, float scale, int dtype,
                         int cache_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ulysses_attn_decode, which also adds to what each cached token has gathered:
+ *   weights[page][h][slot of key j] += sum over the query heads of kv head h of
+ *   exp(s_j - LSE), s_j = scale * q . k_j
+ *   weights  [num_pages][H_kv][page_size] fp32, 16-byte aligned
+ * A slot gets one addition a call; where sequences share a page it gets one of
+ * each, in no fixed order.  Keys that the call leaves out, and heads none of whose
+ * keys counts, add nothing.  The workspace holds the scores of every position of
+ * the tables (4 * B * H_q * table_cols * page_size bytes, at most 2048 sequences'). */
+size_t ulysses_attn_decode_weights_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
+                                             int cache_dtype);
+int ulysses_attn_decode_weights(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int32_t* page_table, int table_cols,
+                                const int32_t* seq_lens, void* o, int64_t o_b, int64_t o_h, float* lse, float* weights,
+                                int B, int H_q, int H_kv, int D, int64_t num_pages, int page_size, float scale, int dtype,
+                                int cache_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction from the paged cache: of the n = seq_lens[b] tokens of a sequence
+ * m = min(n, keep[b]) stay (all where keep[b] < 0), for each kv head its own: the
+ * last r = min(m, recent), and of the n - r before them the m - r of greatest
+ * weight (the lower position first among equals; NaN above everything, -0 equal
+ * to 0).  They close up in their order: position i < m then holds the i-th token
+ * that stays, with its K and V rows, scales and weight.  Positions from m on are
+ * left as they were, and pages that hold none below m are the caller's again.
+ *   weights   [num_pages][H_kv][page_size] fp32, 16-byte aligned
+ *   keep      [B] int32, device;  recent >= 0
+ *   new_lens  [B] int32, device, written: m (may be seq_lens)
+ *   workspace >= ulysses_cache_evict_workspace() bytes, 256-byte aligned,
+ *        contents need no init; calls that share one must not overlap on the GPU
+ * The sequences of a call must not share pages, and a sequence's pages must be
+ * distinct.  A sequence whose length does not fit the table, or that has a page
+ * id outside [0, num_pages) below its length, is left as it is (new_lens its
+ * length) and makes ulysses_check return ULYSSES_ERR_BAD_PAGES.
+ * B' * H_kv * table_cols * page_size <= 2^36 with B' = min(B, 2048). */
+size_t ulysses_cache_evict_workspace(int B, int H_kv, int table_cols, int page_size);
+int ulysses_cache_evict(void* k_cache, void* v_cache, float* k_scale, float* v_scale, float* weights,
+                        const int32_t* page_table, int table_cols, const int32_t* seq_lens, const int32_t* keep, int recent,
+                        int32_t* new_lens, int B, int64_t num_pages, int page_size, int H_kv, int D, int cache_dtype,
+                        void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Whole layer (steps 3-5, forward or backward) with the UPipe stage loop run

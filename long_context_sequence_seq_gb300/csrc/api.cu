@@ -79,6 +79,9 @@ unsigned read_error_proj_gemm(cudaStream_t st);
 unsigned read_error_rope(cudaStream_t st);
 unsigned read_error_kv_cache(cudaStream_t st);
 unsigned read_error_attn_decode(cudaStream_t st);
+unsigned read_error_attn_decode_4bit(cudaStream_t st);
+unsigned read_error_attn_decode_seen(cudaStream_t st);
+unsigned read_error_cache_evict(cudaStream_t st);
 ULYSSES_ERROR_READER(read_error_api)
 
 // cu_seqlens check: cu[0] == 0, cu[nd] == S, non-decreasing.
@@ -835,7 +838,8 @@ int ulysses_check(void* stream) {
   if (e != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "stream error: %s", cudaGetErrorString(e));
   unsigned w = read_error_api(st) | read_error_attn_tc_fwd(st) | read_error_attn_tc_bwd(st) |
                read_error_proj_gemm(st) | read_error_rope(st) | read_error_kv_cache(st) |
-               read_error_attn_decode(st);
+               read_error_attn_decode(st) | read_error_attn_decode_4bit(st) | read_error_attn_decode_seen(st) |
+               read_error_cache_evict(st);
   e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(ULYSSES_ERR_CUDA, "error-word read failed: %s", cudaGetErrorString(e));
   if (w & kErrTimeout) return set_error(ULYSSES_ERR_TIMEOUT, "a kernel gave up a bounded wait");

@@ -1,4 +1,4 @@
-// C ABI of the rotary positions, the paged cache and single-token attention:
+// C ABI of the rotary positions, the paged cache, eviction from it and single-token attention:
 // argument validation and dispatch (the kernels are in rope.cu, kv_cache.cu
 // and attn_decode.cu).
 #include <cmath>
@@ -13,7 +13,11 @@ namespace {
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxPositions = (int64_t)1 << 30;   // of one sequence: positions and tile counts fit int32
 
-int type_size(int dtype) { return dtype == ULYSSES_E4M3 ? 1 : elt_size(dtype); }
+bool scaled(int cache_dtype) { return cache_dtype == ULYSSES_E4M3 || cache_dtype == ULYSSES_E2M1; }
+// Bytes of a cached row (0: no type of cached rows); in 4 bits the block scales are among them.
+int row_bytes(int cache_dtype, int D) {
+  return cache_dtype == ULYSSES_E2M1 ? D / 2 + D / 16 : (cache_dtype == ULYSSES_E4M3 ? D : elt_size(cache_dtype) * D);
+}
 
 // One dimension of a strided tensor.
 struct Dim { int64_t n, stride; };
@@ -189,10 +193,10 @@ int rope(const ulysses_rope_item* items, int n_items, const int32_t* positions, 
 // Shape of the paged cache, shared by every call that touches it.
 int check_cache(int64_t num_pages, int page, int H_kv, int D, int B, int cols, int dtype, int cache_dtype,
                 const void* kc, const void* vc, const float* ks, const float* vs) {
-  if (!elt_size(dtype) || !type_size(cache_dtype))
+  if (!elt_size(dtype) || !row_bytes(cache_dtype, 128))
     return set_error(ULYSSES_ERR_INVALID, "unknown dtype %d (cache %d)", dtype, cache_dtype);
-  if (cache_dtype != dtype && cache_dtype != ULYSSES_E4M3)
-    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache type %d must be the rows' type %d or E4M3", cache_dtype, dtype);
+  if (cache_dtype != dtype && !scaled(cache_dtype))
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache type %d must be the rows' type %d, E4M3 or E2M1", cache_dtype, dtype);
   if (D != 64 && D != 128) return set_error(ULYSSES_ERR_UNSUPPORTED, "head dim %d not in {64,128}", D);
   if (page <= 0 || page % 16 || page > (1 << 20))
     return set_error(ULYSSES_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 16 up to 2^20", page);
@@ -202,11 +206,23 @@ int check_cache(int64_t num_pages, int page, int H_kv, int D, int B, int cols, i
     return set_error(ULYSSES_ERR_UNSUPPORTED, "table_cols * page_size = %lld above 2^30 positions", (long long)cols * page);
   if ((double)num_pages * H_kv * (page / 16) > 2147483647.0)
     return set_error(ULYSSES_ERR_UNSUPPORTED, "cache of more than 2^31 blocks of 16 rows");
-  if ((cache_dtype == ULYSSES_E4M3) != (ks != nullptr) || (cache_dtype == ULYSSES_E4M3) != (vs != nullptr))
-    return set_error(ULYSSES_ERR_INVALID, "scales go with an E4M3 cache, and only with one");
+  if (scaled(cache_dtype) != (ks != nullptr) || scaled(cache_dtype) != (vs != nullptr))
+    return set_error(ULYSSES_ERR_INVALID, "scales go with an E4M3 or E2M1 cache, and only with one");
   if (num_pages && (!kc || !vc)) return set_error(ULYSSES_ERR_INVALID, "NULL cache");
   if (!aligned16(kc) || !aligned16(vc) || !aligned4(ks) || !aligned4(vs))
     return set_error(ULYSSES_ERR_INVALID, "caches must be 16-byte aligned, scales 4-byte");
+  return ULYSSES_OK;
+}
+
+// The tokens' weights, [num_pages][H_kv][page]: apart from the caches and their scales.
+int check_weights(const float* w, int64_t num_pages, int page, int H_kv, int D, int cache_dtype, const void* kc,
+                  const void* vc, const float* ks, const float* vs) {
+  if (!aligned16(w)) return set_error(ULYSSES_ERR_INVALID, "weights must be 16-byte aligned");
+  const size_t rows = (size_t)num_pages * H_kv * page, cb = rows * row_bytes(cache_dtype, D);
+  const char* p = (const char*)w;
+  if (overlap(p, rows * 4, (const char*)kc, cb) || overlap(p, rows * 4, (const char*)vc, cb) ||
+      (ks && (overlap(p, rows * 4, (const char*)ks, rows * 4) || overlap(p, rows * 4, (const char*)vs, rows * 4))))
+    return set_error(ULYSSES_ERR_INVALID, "weights must not overlap the caches or scales");
   return ULYSSES_OK;
 }
 
@@ -230,14 +246,14 @@ int cache_args(CacheArgs& a, const void* k, const void* v, int64_t k_s, int64_t 
     if ((rc = check_distinct(dk, 2, D, "k")) || (rc = check_distinct(dv, 2, D, "v"))) return rc;
     if (may_overlap(sk, sv, D)) return set_error(ULYSSES_ERR_INVALID, "k overlaps v");
   }
-  const size_t rows = (size_t)num_pages * H * page, cb = rows * D * type_size(cache_dtype);
+  const size_t rows = (size_t)num_pages * H * page, cb = rows * row_bytes(cache_dtype, D);
   const Span* both[2] = {&sk, &sv};
   for (const Span* s : both)
     if (overlap(s->p, (size_t)s->bytes, (const char*)kc, cb) || overlap(s->p, (size_t)s->bytes, (const char*)vc, cb))
       return set_error(ULYSSES_ERR_INVALID, "k and v must not overlap the caches");
   if (!written && overlap((const char*)kc, cb, (const char*)vc, cb))
     return set_error(ULYSSES_ERR_INVALID, "k_cache overlaps v_cache");
-  a = CacheArgs{kc, vc, ks, vs, const_cast<void*>(k), const_cast<void*>(v), k_s, k_h, v_s, v_h, cu, lens, table,
+  a = CacheArgs{kc, vc, ks, vs, nullptr, const_cast<void*>(k), const_cast<void*>(v), k_s, k_h, v_s, v_h, cu, lens, table,
                 T, num_pages, B, cols, page, H, D, dtype, cache_dtype};
   return ULYSSES_OK;
 }
@@ -249,6 +265,82 @@ int decode_args(DecodeArgs& a, int B, int H_q, int H_kv, int D, int cols, int pa
   a = DecodeArgs{};
   a.B = B; a.H_q = H_q; a.H_kv = H_kv; a.G = H_q / H_kv; a.D = D;
   a.cols = cols; a.page = page; a.dtype = dtype; a.cache_dtype = cache_dtype;
+  return ULYSSES_OK;
+}
+
+int cache_write(const void* k, const void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h, int64_t T, int B,
+                const int32_t* cu_new, const int32_t* page_table, int table_cols, const int32_t* seq_lens, void* k_cache,
+                void* v_cache, float* k_scale, float* v_scale, float* weights, int64_t num_pages, int page_size, int H_kv,
+                int D, int dtype, int cache_dtype, void* stream) {
+  CacheArgs a{};
+  int rc = cache_args(a, k, v, k_s, k_h, v_s, v_h, T, B, cu_new, page_table, table_cols, seq_lens, k_cache, v_cache,
+                      k_scale, v_scale, num_pages, page_size, H_kv, D, dtype, cache_dtype, false);
+  if (!rc && weights) rc = check_weights(weights, num_pages, page_size, H_kv, D, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+  if (rc) return rc;
+  if (!cu_new && T != B)
+    return set_error(ULYSSES_ERR_INVALID, "without cu_new there is one token per sequence: T=%lld, B=%d", (long long)T, B);
+  if (T == 0 || B == 0) return ULYSSES_OK;
+  if (!seq_lens) return set_error(ULYSSES_ERR_INVALID, "NULL seq_lens");
+  const size_t wb = (size_t)num_pages * H_kv * page_size * 4;
+  const Dim dk[2] = {{T, k_s}, {H_kv, k_h}}, dv[2] = {{T, v_s}, {H_kv, v_h}};
+  if (weights && (overlap((const char*)weights, wb, (const char*)k, (size_t)extent(dk, 2, D) * elt_size(dtype)) ||
+                  overlap((const char*)weights, wb, (const char*)v, (size_t)extent(dv, 2, D) * elt_size(dtype))))
+    return set_error(ULYSSES_ERR_INVALID, "weights must not overlap k and v");
+  a.w = weights;
+  return launch_cache_write(a, (cudaStream_t)stream);
+}
+
+int attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache, const float* k_scale,
+                const float* v_scale, const int32_t* page_table, int table_cols, const int32_t* seq_lens, void* o,
+                int64_t o_b, int64_t o_h, float* lse, float* weights, int B, int H_q, int H_kv, int D, int64_t num_pages,
+                int page_size, float scale, int dtype, int cache_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  int rc = check_cache(num_pages, page_size, H_kv, D, B, table_cols, dtype, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+  if (!rc && weights) rc = check_weights(weights, num_pages, page_size, H_kv, D, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+  if (rc) return rc;
+  DecodeArgs a;
+  if ((rc = decode_args(a, B, H_q, H_kv, D, table_cols, page_size, dtype, cache_dtype))) return rc;
+  if (B == 0) return ULYSSES_OK;
+  if (!q || !o || !seq_lens || (table_cols && !page_table)) return set_error(ULYSSES_ERR_INVALID, "NULL buffer");
+  if (!aligned16(q) || !aligned16(o)) return set_error(ULYSSES_ERR_INVALID, "buffers must be 16-byte aligned");
+  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(lse))
+    return set_error(ULYSSES_ERR_INVALID, "table, lengths and LSE must be 4-byte aligned");
+  Dim dq[2] = {{B, q_b}, {H_q, q_h}}, dout[2] = {{B, o_b}, {H_q, o_h}};
+  const int e = elt_size(dtype);
+  if ((rc = check_strides(dq, 2, e, "q")) || (rc = check_strides(dout, 2, e, "o"))) return rc;
+  const int64_t qn = extent(dq, 2, D) * e, on = extent(dout, 2, D) * e;
+  if ((rc = check_distinct(dout, 2, D, "o"))) return rc;
+  if (overlap((const char*)o, (size_t)on, (const char*)q, (size_t)qn))
+    return set_error(ULYSSES_ERR_INVALID, "o overlaps q");
+  const size_t wb = (size_t)num_pages * H_kv * page_size * 4;
+  if (weights && (overlap((const char*)weights, wb, (const char*)q, (size_t)qn) || overlap((const char*)weights, wb, (const char*)o, (size_t)on)))
+    return set_error(ULYSSES_ERR_INVALID, "weights must not overlap q and o");
+  a.seen = weights;
+  const size_t need = decode_workspace(a);
+  if (ws_bytes < need || (need && !workspace))
+    return set_error(ULYSSES_ERR_INVALID, "workspace too small: %zu < %zu", ws_bytes, need);
+  if (((uintptr_t)workspace & 255u) != 0) return set_error(ULYSSES_ERR_INVALID, "workspace must be 256-byte aligned");
+  a.q = q; a.q_b = q_b; a.q_h = q_h;
+  a.o = o; a.o_b = o_b; a.o_h = o_h; a.lse = lse;
+  a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale;
+  a.table = page_table; a.lens = seq_lens; a.num_pages = num_pages;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+  a.ws = workspace;
+  return launch_decode(a, simt_chosen(), (cudaStream_t)stream);
+}
+
+int evict_args(EvictArgs& a, int B, int H_kv, int cols, int page) {
+  if (page <= 0 || page % 16 || page > (1 << 20))
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 16 up to 2^20", page);
+  if (H_kv <= 0 || H_kv > 4096 || B < 0 || cols < 0)
+    return set_error(ULYSSES_ERR_INVALID, "bad sizes B=%d H_kv=%d table_cols=%d", B, H_kv, cols);
+  if ((int64_t)cols * page > kMaxPositions)
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "table_cols * page_size = %lld above 2^30 positions", (long long)cols * page);
+  // chunks of 64 positions of a launch's sequences (at most 2048) are counted in 31 bits
+  const int64_t b = B < 2048 ? B : 2048;
+  if (((int64_t)cols * page / 64 + 1) * b * H_kv > (1 << 30))
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache_evict: B * H_kv * table_cols * page_size above 2^36");
+  a = EvictArgs{};
+  a.B = B; a.H = H_kv; a.cols = cols; a.page = page;
   return ULYSSES_OK;
 }
 
@@ -273,15 +365,18 @@ int ulysses_cache_write(const void* k, const void* v, int64_t k_s, int64_t k_h, 
                         const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                         int64_t num_pages, int page_size, int H_kv, int D, int dtype, int cache_dtype,
                         void* stream) {
-  CacheArgs a{};
-  int rc = cache_args(a, k, v, k_s, k_h, v_s, v_h, T, B, cu_new, page_table, table_cols, seq_lens, k_cache, v_cache,
-                      k_scale, v_scale, num_pages, page_size, H_kv, D, dtype, cache_dtype, false);
-  if (rc) return rc;
-  if (!cu_new && T != B)
-    return set_error(ULYSSES_ERR_INVALID, "without cu_new there is one token per sequence: T=%lld, B=%d", (long long)T, B);
-  if (T == 0 || B == 0) return ULYSSES_OK;
-  if (!seq_lens) return set_error(ULYSSES_ERR_INVALID, "NULL seq_lens");
-  return launch_cache_write(a, (cudaStream_t)stream);
+  return cache_write(k, v, k_s, k_h, v_s, v_h, T, B, cu_new, page_table, table_cols, seq_lens, k_cache, v_cache, k_scale,
+                     v_scale, nullptr, num_pages, page_size, H_kv, D, dtype, cache_dtype, stream);
+}
+
+int ulysses_cache_write_weights(const void* k, const void* v, int64_t k_s, int64_t k_h, int64_t v_s, int64_t v_h,
+                                int64_t T, int B, const int32_t* cu_new, const int32_t* page_table, int table_cols,
+                                const int32_t* seq_lens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                float* weights, int64_t num_pages, int page_size, int H_kv, int D, int dtype,
+                                int cache_dtype, void* stream) {
+  if (num_pages && !weights) return set_error(ULYSSES_ERR_INVALID, "NULL weights");
+  return cache_write(k, v, k_s, k_h, v_s, v_h, T, B, cu_new, page_table, table_cols, seq_lens, k_cache, v_cache, k_scale,
+                     v_scale, weights, num_pages, page_size, H_kv, D, dtype, cache_dtype, stream);
 }
 
 int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
@@ -311,33 +406,61 @@ int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_c
                         const int32_t* seq_lens, void* o, int64_t o_b, int64_t o_h, float* lse, int B, int H_q,
                         int H_kv, int D, int64_t num_pages, int page_size, float scale, int dtype,
                         int cache_dtype, void* workspace, size_t ws_bytes, void* stream) {
-  int rc = check_cache(num_pages, page_size, H_kv, D, B, table_cols, dtype, cache_dtype, k_cache, v_cache, k_scale, v_scale);
-  if (rc) return rc;
+  return attn_decode(q, q_b, q_h, k_cache, v_cache, k_scale, v_scale, page_table, table_cols, seq_lens, o, o_b, o_h, lse,
+                     nullptr, B, H_q, H_kv, D, num_pages, page_size, scale, dtype, cache_dtype, workspace, ws_bytes, stream);
+}
+
+size_t ulysses_attn_decode_weights_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
+                                             int cache_dtype) {
   DecodeArgs a;
-  if ((rc = decode_args(a, B, H_q, H_kv, D, table_cols, page_size, dtype, cache_dtype))) return rc;
+  if (B < 0 || decode_args(a, B, H_q, H_kv, D, table_cols, page_size, dtype, cache_dtype)) return 0;
+  static float any;
+  a.seen = &any;                                           // asked for, not read
+  return decode_workspace(a);
+}
+
+int ulysses_attn_decode_weights(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int32_t* page_table, int table_cols,
+                                const int32_t* seq_lens, void* o, int64_t o_b, int64_t o_h, float* lse, float* weights,
+                                int B, int H_q, int H_kv, int D, int64_t num_pages, int page_size, float scale, int dtype,
+                                int cache_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (num_pages && !weights) return set_error(ULYSSES_ERR_INVALID, "NULL weights");
+  return attn_decode(q, q_b, q_h, k_cache, v_cache, k_scale, v_scale, page_table, table_cols, seq_lens, o, o_b, o_h, lse,
+                     weights, B, H_q, H_kv, D, num_pages, page_size, scale, dtype, cache_dtype, workspace, ws_bytes, stream);
+}
+
+size_t ulysses_cache_evict_workspace(int B, int H_kv, int table_cols, int page_size) {
+  EvictArgs a;
+  if (evict_args(a, B, H_kv, table_cols, page_size)) return 0;
+  return evict_workspace(a);
+}
+
+int ulysses_cache_evict(void* k_cache, void* v_cache, float* k_scale, float* v_scale, float* weights,
+                        const int32_t* page_table, int table_cols, const int32_t* seq_lens, const int32_t* keep, int recent,
+                        int32_t* new_lens, int B, int64_t num_pages, int page_size, int H_kv, int D, int cache_dtype,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  const int dtype = cache_dtype == ULYSSES_FP32 ? ULYSSES_FP32 : ULYSSES_BF16;
+  int rc = check_cache(num_pages, page_size, H_kv, D, B, table_cols, dtype, cache_dtype, k_cache, v_cache, k_scale, v_scale);
+  EvictArgs a;
+  if (rc || (rc = evict_args(a, B, H_kv, table_cols, page_size))) return rc;
+  if (recent < 0) return set_error(ULYSSES_ERR_INVALID, "recent=%d below 0", recent);
+  if (num_pages && !weights) return set_error(ULYSSES_ERR_INVALID, "NULL weights");
+  if ((rc = check_weights(weights, num_pages, page_size, H_kv, D, cache_dtype, k_cache, v_cache, k_scale, v_scale))) return rc;
+  const size_t rows = (size_t)num_pages * H_kv * page_size, cb = rows * row_bytes(cache_dtype, D);
+  if (overlap((const char*)k_cache, cb, (const char*)v_cache, cb) ||
+      (k_scale && overlap((const char*)k_scale, rows * 4, (const char*)v_scale, rows * 4)))
+    return set_error(ULYSSES_ERR_INVALID, "K's and V's buffers must not overlap");
   if (B == 0) return ULYSSES_OK;
-  if (!q || !o || !seq_lens || (table_cols && !page_table)) return set_error(ULYSSES_ERR_INVALID, "NULL buffer");
-  if (!aligned16(q) || !aligned16(o)) return set_error(ULYSSES_ERR_INVALID, "buffers must be 16-byte aligned");
-  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(lse))
-    return set_error(ULYSSES_ERR_INVALID, "table, lengths and LSE must be 4-byte aligned");
-  Dim dq[2] = {{B, q_b}, {H_q, q_h}}, dout[2] = {{B, o_b}, {H_q, o_h}};
-  const int e = elt_size(dtype);
-  if ((rc = check_strides(dq, 2, e, "q")) || (rc = check_strides(dout, 2, e, "o"))) return rc;
-  const int64_t qn = extent(dq, 2, D) * e, on = extent(dout, 2, D) * e;
-  if ((rc = check_distinct(dout, 2, D, "o"))) return rc;
-  if (overlap((const char*)o, (size_t)on, (const char*)q, (size_t)qn))
-    return set_error(ULYSSES_ERR_INVALID, "o overlaps q");
-  const size_t need = decode_workspace(a);
-  if (ws_bytes < need || (need && !workspace))
-    return set_error(ULYSSES_ERR_INVALID, "workspace too small: %zu < %zu", ws_bytes, need);
+  if (!seq_lens || !keep || !new_lens || (table_cols && !page_table)) return set_error(ULYSSES_ERR_INVALID, "NULL buffer");
+  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(keep) || !aligned4(new_lens))
+    return set_error(ULYSSES_ERR_INVALID, "table, lengths and budgets must be 4-byte aligned");
+  const size_t need = evict_workspace(a);
+  if (ws_bytes < need || !workspace) return set_error(ULYSSES_ERR_INVALID, "workspace too small: %zu < %zu", ws_bytes, need);
   if (((uintptr_t)workspace & 255u) != 0) return set_error(ULYSSES_ERR_INVALID, "workspace must be 256-byte aligned");
-  a.q = q; a.q_b = q_b; a.q_h = q_h;
-  a.o = o; a.o_b = o_b; a.o_h = o_h; a.lse = lse;
-  a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale;
-  a.table = page_table; a.lens = seq_lens; a.num_pages = num_pages;
-  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  a.ws = workspace;
-  return launch_decode(a, simt_chosen(), (cudaStream_t)stream);
+  a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale; a.w = weights;
+  a.table = page_table; a.lens = seq_lens; a.keep = keep; a.out = new_lens;
+  a.num_pages = num_pages; a.D = D; a.cache_dtype = cache_dtype; a.recent = recent; a.ws = workspace;
+  return launch_evict(a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -107,6 +107,7 @@ int launch_rope(const RopeArgs& a, cudaStream_t st);
 // The paged cache and the tokens of one write or read (kv_cache.cu).
 struct CacheArgs {
   void* kc; void* vc; float* ks; float* vs;       // caches and scales
+  float* w;                                       // attention weights of the tokens, or NULL (write: set to 0)
   void* k; void* v;                               // tokens' rows
   int64_t k_s, k_h, v_s, v_h;
   const int32_t* cu; const int32_t* lens;         // write: lens; read: first (in lens)
@@ -128,9 +129,24 @@ struct DecodeArgs {
   int B, H_q, H_kv, G, D, cols, page, dtype, cache_dtype;
   float scale_log2;            // score scale * log2(e)
   void* ws;
+  float* seen;                 // [num_pages][H_kv][page] weights to add to, or NULL
+  float* scores; float2* fin;  // inside: scores kept for that, the heads' (maximum, 1 / sum)
 };
 size_t decode_workspace(const DecodeArgs& a);
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st);
+int launch_decode_4bit(const DecodeArgs& a, bool simt, cudaStream_t st);   // attn_decode_4bit.cu
+int launch_decode_seen(const DecodeArgs& a, bool simt, cudaStream_t st);   // attn_decode_seen.cu
+// Eviction from the paged cache by accumulated attention weight (cache_evict.cu).
+struct EvictArgs {
+  void* kc; void* vc; float* ks; float* vs; float* w;
+  const int32_t* table; const int32_t* lens; const int32_t* keep;
+  int32_t* out;
+  int64_t num_pages;
+  int B, cols, page, H, D, cache_dtype, recent;
+  void* ws;
+};
+size_t evict_workspace(const EvictArgs& a);
+int launch_evict(const EvictArgs& a, cudaStream_t st);
 bool simt_chosen();                                                       // api.cu
 bool multicast_allowed();                                                 // api.cu
 

@@ -11,6 +11,9 @@
 namespace ulysses {
 namespace rows {
 
+// How a cache holds its rows: as they are, in 8 bits or in 4.
+enum Held { kAsIs, kE4m3, kE2m1 };
+
 // Streaming accesses: each word is used once, so L1 keeps none of them.
 __device__ __forceinline__ uint4 ld16(const void* p) {
   uint4 v;
@@ -21,6 +24,11 @@ __device__ __forceinline__ uint4 ld16(const void* p) {
 __device__ __forceinline__ uint2 ld8(const void* p) {
   uint2 v;
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ void st16(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
@@ -54,6 +62,43 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
     f[2 * i] = v.x;
     f[2 * i + 1] = v.y;
   }
+}
+// Eight e2m1 codes (the lowest four bits first) as f16 pairs: exact.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{ .reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+// Eight fp32 values as e2m1 codes: nearest, half way to the even code, at most 6.
+__device__ __forceinline__ uint32_t f32_to_e2m1x8(const float* f) {
+  uint32_t r;
+  asm("{ .reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3}; }"
+      : "=r"(r) : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Where the parts of a row of a 4-bit cache are: a page of a head holds its rows'
+// codes ([page][D / 2] bytes) and behind them their block scales ([page][D / 16]).
+// `row` counts rows ([num_pages][H_kv][page]), `slot` is the row's in its page.
+__device__ __forceinline__ int64_t e2m1_codes(int64_t row, int slot, int D) {
+  return (row - slot) * (D / 16 * 9) + slot * (D / 2);
+}
+__device__ __forceinline__ int64_t e2m1_blocks(int64_t row, int slot, int page, int D) {
+  return (row - slot) * (D / 16 * 9) + (int64_t)page * (D / 2) + slot * (D / 16);
 }
 
 __device__ __forceinline__ float max_nan(float x, float y) {   // NaN if either is

@@ -1,5 +1,5 @@
-// Marshalling of the strided calls (rotary positions, paged cache, single-token
-// attention) in C++: what ulysses.py does for them in Python, without the
+// Marshalling of the strided calls (rotary positions, paged cache, eviction from
+// it, single-token attention) in C++: what ulysses.py does for them in Python, without the
 // interpreter.  A kernel of these takes 3 to 8 us at decode sizes and the
 // Python marshalling around it 18 to 24, so the calls that a decode loop makes
 // go through here.
@@ -31,6 +31,11 @@ decltype(&ulysses_cache_write) g_cache_write = nullptr;
 decltype(&ulysses_cache_read) g_cache_read = nullptr;
 decltype(&ulysses_attn_decode) g_attn_decode = nullptr;
 decltype(&ulysses_attn_decode_workspace) g_attn_decode_workspace = nullptr;
+decltype(&ulysses_cache_write_weights) g_cache_write_weights = nullptr;
+decltype(&ulysses_attn_decode_weights) g_attn_decode_weights = nullptr;
+decltype(&ulysses_attn_decode_weights_workspace) g_attn_decode_weights_workspace = nullptr;
+decltype(&ulysses_cache_evict) g_cache_evict = nullptr;
+decltype(&ulysses_cache_evict_workspace) g_cache_evict_workspace = nullptr;
 
 struct NotPlain {};   // thrown where the Python function has to look at the call
 
@@ -104,9 +109,19 @@ struct Cache {
     page = (int)tk.size(2);
     D = (int)tk.size(3);
     plain(tk.size(1) <= INT32_MAX && tk.size(2) <= INT32_MAX && tk.size(3) <= INT32_MAX);
-    type = code(tk.scalar_type());
+    if (tk.scalar_type() == at::kByte) {                 // 4 bits: 9 D / 16 bytes a row
+      plain(D % 9 == 0 && D <= INT32_MAX / 16);
+      D = D / 9 * 16;
+      type = ULYSSES_E2M1;
+    } else {
+      type = code(tk.scalar_type());
+    }
     if (pks != Py_None) ks = scale(c, tensor(pks), tk);
     if (pvs != Py_None) vs = scale(c, tensor(pvs), tk);
+  }
+  // the tokens' weights, or NULL
+  static float* weights(const Call& c, PyObject* w, PyObject* of) {
+    return w == Py_None ? nullptr : scale(c, tensor(w), tensor(of));
   }
   static float* scale(const Call& c, const Tensor& s, const Tensor& of) {
     plain(s.sizes() == of.sizes().slice(0, 3));
@@ -219,7 +234,7 @@ PyObject* rope(PyObject* const* a) {
   return THPVariable_Wrap(result[0]);
 }
 
-// k, v, k_cache, v_cache, page_table, seq_lens, cu_new, k_scale, v_scale, layout
+// k, v, k_cache, v_cache, page_table, seq_lens, cu_new, k_scale, v_scale, layout, weights
 PyObject* cache_write(PyObject* const* a) {
   const Tensor &k = tensor(a[0]), &v = tensor(a[1]), &lens = tensor(a[5]);
   const Call c(k);
@@ -240,7 +255,12 @@ PyObject* cache_write(PyObject* const* a) {
   }
   const int32_t* ln = c.flat<int32_t>(lens, at::kInt);
   const int type = code(k.scalar_type());
+  float* const weights = Cache::weights(c, a[10], a[2]);
   const int rc = unlocked([&] {
+    if (weights)
+      return g_cache_write_weights(k.data_ptr(), v.data_ptr(), rk.ts, rk.hs, rv.ts, rv.hs, rk.T, (int)B, cu, table.p, table.cols,
+                                   ln, cache.k, cache.v, cache.ks, cache.vs, weights, cache.pages, cache.page, cache.H, cache.D,
+                                   type, cache.type, c.stream());
     return g_cache_write(k.data_ptr(), v.data_ptr(), rk.ts, rk.hs, rv.ts, rv.hs, rk.T, (int)B, cu, table.p, table.cols, ln,
                          cache.k, cache.v, cache.ks, cache.vs, cache.pages, cache.page, cache.H, cache.D, type, cache.type,
                          c.stream());
@@ -264,7 +284,7 @@ PyObject* cache_read(PyObject* const* a) {
     plain(t.numel() == B);
     first = c.flat<int32_t>(t, at::kInt);
   }
-  at::ScalarType type = kc.scalar_type() == at::kFloat8_e4m3fn ? at::kBFloat16 : kc.scalar_type();
+  at::ScalarType type = cache.ks ? at::kBFloat16 : kc.scalar_type();
   Tensor k, v;
   const int64_t size[3] = {head ? cache.H : T, head ? T : cache.H, cache.D};
   if (a[10] != Py_None) {
@@ -293,7 +313,7 @@ PyObject* cache_read(PyObject* const* a) {
   return rc ? status(rc) : pair(k, v);
 }
 
-// q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, scale, layout, workspace, out, lse
+// q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, scale, layout, workspace, out, lse, weights
 PyObject* attn_decode(PyObject* const* a) {
   const Tensor &q = tensor(a[0]), &lens = tensor(a[4]);
   const Call c(q);
@@ -326,10 +346,11 @@ PyObject* attn_decode(PyObject* const* a) {
     lse = c.empty(ls, at::kFloat);
   }
   float* pl = c.flat<float>(lse, at::kFloat);
+  float* const weights = Cache::weights(c, a[12], a[1]);
   if (a[9] != Py_None) {
     ws = tensor(a[9]);
   } else {
-    const int64_t n = (int64_t)g_attn_decode_workspace((int)B, (int)rq.H, cache.H, cache.D, table.cols, cache.page, dq, cache.type);
+    const int64_t n = (int64_t)(weights ? g_attn_decode_weights_workspace : g_attn_decode_workspace)((int)B, (int)rq.H, cache.H, cache.D, table.cols, cache.page, dq, cache.type);
     if (n) ws = c.empty(n, at::kByte);
   }
   void* pw = nullptr;
@@ -339,6 +360,10 @@ PyObject* attn_decode(PyObject* const* a) {
     nw = (size_t)ws.numel();
   }
   const int rc = unlocked([&] {
+    if (weights)
+      return g_attn_decode_weights(q.data_ptr(), rq.ts, rq.hs, cache.k, cache.v, cache.ks, cache.vs, table.p, table.cols, ln,
+                                   o.data_ptr(), ro.ts, ro.hs, pl, weights, (int)B, (int)rq.H, cache.H, cache.D, cache.pages,
+                                   cache.page, (float)scale, dq, cache.type, pw, nw, c.stream());
     return g_attn_decode(q.data_ptr(), rq.ts, rq.hs, cache.k, cache.v, cache.ks, cache.vs, table.p, table.cols, ln, o.data_ptr(),
                          ro.ts, ro.hs, pl, (int)B, (int)rq.H, cache.H, cache.D, cache.pages, cache.page, (float)scale, dq,
                          cache.type, pw, nw, c.stream());
@@ -346,14 +371,58 @@ PyObject* attn_decode(PyObject* const* a) {
   return rc ? status(rc) : pair(o, lse);
 }
 
-template <PyObject* (*kFn)(PyObject* const*), int kArgs>
+// k_cache, v_cache, weights, page_table, seq_lens, keep, recent, k_scale, v_scale, out, workspace
+PyObject* cache_evict(PyObject* const* a) {
+  const Tensor &kc = tensor(a[0]), &lens = tensor(a[4]), &keep = tensor(a[5]);
+  const Call c(kc);
+  const Cache cache(c, a[0], a[1], a[7], a[8]);
+  plain(a[2] != Py_None);
+  float* const weights = Cache::weights(c, a[2], a[0]);
+  const int64_t B = lens.numel();
+  plain(B > 0 && B <= INT32_MAX && keep.numel() == B);
+  const Table table(c, a[3], B);
+  const int32_t *ln = c.flat<int32_t>(lens, at::kInt), *kp = c.flat<int32_t>(keep, at::kInt);
+  plain(PyLong_CheckExact(a[6]));
+  const long long recent = PyLong_AsLongLong(a[6]);
+  plain(recent >= 0 && recent <= INT32_MAX);
+  Tensor out, ws;
+  if (a[9] != Py_None) {
+    out = tensor(a[9]);
+    plain(out.numel() == B);
+  } else {
+    out = c.empty({B}, at::kInt);
+  }
+  int32_t* const po = c.flat<int32_t>(out, at::kInt);
+  if (a[10] != Py_None) {
+    ws = tensor(a[10]);
+  } else {
+    const int64_t n = (int64_t)g_cache_evict_workspace((int)B, cache.H, table.cols, cache.page);
+    if (n) ws = c.empty(n, at::kByte);
+  }
+  void* pw = nullptr;
+  size_t nw = 0;
+  if (ws.defined()) {
+    pw = c.flat<void>(ws, at::kByte);
+    nw = (size_t)ws.numel();
+  }
+  const int rc = unlocked([&] {
+    return g_cache_evict(cache.k, cache.v, cache.ks, cache.vs, weights, table.p, table.cols, ln, kp, (int)recent, po, (int)B,
+                         cache.pages, cache.page, cache.H, cache.D, cache.type, pw, nw, c.stream());
+  });
+  return rc ? status(rc) : THPVariable_Wrap(out);
+}
+
+// kMore: trailing arguments that may be left out (None).
+template <PyObject* (*kFn)(PyObject* const*), int kArgs, int kMore = 0>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != kArgs) {
+  if (n < kArgs || n > kArgs + kMore) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return nullptr;
   }
+  PyObject* all[kArgs + kMore];
+  for (int i = 0; i < kArgs + kMore; ++i) all[i] = i < n ? args[i] : Py_None;
   try {
-    return kFn(args);
+    return kFn(all);
   } catch (...) {
     // not a plain call, or torch refused something (memory): the Python function looks
     PyErr_Clear();
@@ -363,23 +432,29 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // Addresses of the library's functions, in this order.
 PyObject* bind(PyObject*, PyObject* args) {
-  unsigned long long p[6];
-  if (!PyArg_ParseTuple(args, "KKKKKK", p, p + 1, p + 2, p + 3, p + 4, p + 5)) return nullptr;
+  unsigned long long p[11];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, p + 7, p + 8, p + 9, p + 10)) return nullptr;
   g_rope_fwd = reinterpret_cast<decltype(g_rope_fwd)>(p[0]);
   g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(p[1]);
   g_cache_write = reinterpret_cast<decltype(g_cache_write)>(p[2]);
   g_cache_read = reinterpret_cast<decltype(g_cache_read)>(p[3]);
   g_attn_decode = reinterpret_cast<decltype(g_attn_decode)>(p[4]);
   g_attn_decode_workspace = reinterpret_cast<decltype(g_attn_decode_workspace)>(p[5]);
+  g_cache_write_weights = reinterpret_cast<decltype(g_cache_write_weights)>(p[6]);
+  g_attn_decode_weights = reinterpret_cast<decltype(g_attn_decode_weights)>(p[7]);
+  g_attn_decode_weights_workspace = reinterpret_cast<decltype(g_attn_decode_weights_workspace)>(p[8]);
+  g_cache_evict = reinterpret_cast<decltype(g_cache_evict)>(p[9]);
+  g_cache_evict_workspace = reinterpret_cast<decltype(g_cache_evict_workspace)>(p[10]);
   Py_RETURN_NONE;
 }
 
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
     {"rope", (PyCFunction)(void*)entry<rope, 10>, METH_FASTCALL, nullptr},
-    {"cache_write", (PyCFunction)(void*)entry<cache_write, 10>, METH_FASTCALL, nullptr},
+    {"cache_write", (PyCFunction)(void*)entry<cache_write, 10, 1>, METH_FASTCALL, nullptr},
     {"cache_read", (PyCFunction)(void*)entry<cache_read, 11>, METH_FASTCALL, nullptr},
-    {"attn_decode", (PyCFunction)(void*)entry<attn_decode, 12>, METH_FASTCALL, nullptr},
+    {"attn_decode", (PyCFunction)(void*)entry<attn_decode, 12, 1>, METH_FASTCALL, nullptr},
+    {"cache_evict", (PyCFunction)(void*)entry<cache_evict, 11>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(_PKG, "libulysses_checked.so" if os.environ.get("ULYSSES
                         else "libulysses.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_SEQLENS, ERR_BOUNDS, ERR_BAD_PAGES = range(8)
-BF16, FP32, E4M3 = 0, 1, 2
+BF16, FP32, E4M3, E2M1 = 0, 1, 2, 3
 PAIRS_HALF, PAIRS_ADJACENT = 0, 1
 KERNEL_AUTO, KERNEL_SIMT, KERNEL_NO_MULTICAST = 0, 1, 2
 
@@ -114,6 +114,15 @@ def lib():
     L.ulysses_attn_decode_workspace.restype = sz
     L.ulysses_attn_decode.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, i64, i64, vp, i32, i32, i32, i32,
                                       i64, i32, f32, i32, i32, vp, sz, vp]
+    L.ulysses_cache_write_weights.argtypes = [vp, vp, i64, i64, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, i64,
+                                              i32, i32, i32, i32, i32, vp]
+    L.ulysses_attn_decode_weights_workspace.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32]
+    L.ulysses_attn_decode_weights_workspace.restype = sz
+    L.ulysses_attn_decode_weights.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp, i64, i64, vp, vp, i32, i32, i32,
+                                              i32, i64, i32, f32, i32, i32, vp, sz, vp]
+    L.ulysses_cache_evict_workspace.argtypes = [i32, i32, i32, i32]
+    L.ulysses_cache_evict_workspace.restype = sz
+    L.ulysses_cache_evict.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, i32, i64, i32, i32, i32, i32, vp, sz, vp]
     L.ulysses_check.argtypes = [vp]
     L.ulysses_last_error.restype = ctypes.c_char_p
     L.ulysses_set_kernel.argtypes = [i32]
@@ -139,7 +148,8 @@ def _bind_fast(L):
         return
     _fastcall.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.ulysses_rope_fwd, L.ulysses_rope_bwd, L.ulysses_cache_write, L.ulysses_cache_read, L.ulysses_attn_decode,
-        L.ulysses_attn_decode_workspace)))
+        L.ulysses_attn_decode_workspace, L.ulysses_cache_write_weights, L.ulysses_attn_decode_weights,
+        L.ulysses_attn_decode_weights_workspace, L.ulysses_cache_evict, L.ulysses_cache_evict_workspace)))
     _fast = _fastcall
 
 
@@ -755,23 +765,42 @@ def rope_bwd(dq, dk, positions, inv_freq, axes=None, layout="seq", pairs="half",
 def kv_cache(num_pages, page_size, H_kv, D, dtype=torch.bfloat16, device="cuda"):
     """Buffers of a paged cache: (k_cache, v_cache [num_pages, H_kv, page_size,
     D], k_scale, v_scale [num_pages, H_kv, page_size] fp32, or None unless
-    dtype is torch.float8_e4m3fn).  Zero-filled."""
-    shape = (num_pages, H_kv, page_size, D)
+    dtype is torch.float8_e4m3fn or torch.uint8).  Zero-filled.  torch.uint8 is
+    the 4-bit cache, [num_pages, H_kv, page_size, 9 D / 16] bytes: a page of a
+    head holds its rows' e2m1 codes ([page_size, D / 2], two a byte, the first in
+    the low half) and behind them their e4m3 scales of 16 codes each
+    ([page_size, D / 16])."""
+    four = dtype == torch.uint8
+    shape = (num_pages, H_kv, page_size, D * 9 // 16 if four else D)
     k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
-    if dtype != torch.float8_e4m3fn:
+    if not four and dtype != torch.float8_e4m3fn:
         return k, v, None, None
     ks, vs = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
     return k, v, ks, vs
 
 
+def cache_weights(k_cache):
+    """Attention weights that the tokens of a cache have gathered: zeros
+    [num_pages, H_kv, page_size] fp32, for cache_write, attn_decode and
+    cache_evict."""
+    return torch.zeros(k_cache.shape[:3], dtype=torch.float32, device=k_cache.device)
+
+
 def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Pointers of the cache's buffers and its sizes, after the checks that
-    need the tensors."""
+    """Pointers of the cache's buffers, its sizes and its type's code, after the
+    checks that need the tensors."""
     sh, dt = k_cache.shape, k_cache.dtype
     if len(sh) != 4 or sh != v_cache.shape or dt is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must be [num_pages, H_kv, page_size, D] of one shape and dtype")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k_cache and v_cache must be contiguous")
+    if dt is _U8:
+        code = E2M1
+        if sh[3] % 9:
+            raise ValueError("a 4-bit cache (uint8) must have 9 D / 16 bytes a row")
+        sh = (*sh[:3], sh[3] // 9 * 16)
+    else:
+        code = _code(dt, "k_cache")
     ks = vs = None
     if k_scale is not None:
         if k_scale.shape != sh[:3]:
@@ -781,7 +810,13 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
         if v_scale.shape != sh[:3]:
             raise ValueError("scales must be [num_pages, H_kv, page_size]")
         vs = _flat(v_scale, _F32, "v_scale")
-    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, sh
+    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, sh, code
+
+
+def _weights(weights, sh):
+    if weights.shape != sh[:3]:
+        raise ValueError("weights must be [num_pages, H_kv, page_size]")
+    return _flat(weights, _F32, "weights")
 
 
 def _batch_table(page_table, n, what):
@@ -792,17 +827,19 @@ def _batch_table(page_table, n, what):
 
 
 def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_scale=None, v_scale=None, layout="seq",
-                stream=None):
+                stream=None, weights=None):
     """Store the K and V rows of new tokens in the paged cache.
 
     k, v: [T, H_kv, D] ("seq") or [H_kv, T, D] ("head"), any strides with D
     contiguous.  page_table int32 [B, columns], seq_lens int32 [B]: the lengths
     with the new tokens.  cu_new int32 [B + 1]: sequence b's new tokens are
     rows [cu_new[b], cu_new[b+1]); None: one token per sequence, and a length
-    of 0 marks an empty place of the batch.  An e4m3 cache (with its scales) is
-    quantised row by row on the way.  Bad positions or pages raise in check()."""
+    of 0 marks an empty place of the batch.  An e4m3 or 4-bit (uint8) cache, with
+    its scales, is quantised row by row on the way.  weights (cache_weights()):
+    those of the new tokens are set to 0.  Bad positions or pages raise in
+    check()."""
     if _fast is not None and stream is None:
-        r = _fast.cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, k_scale, v_scale, layout)
+        r = _fast.cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new, k_scale, v_scale, layout, weights)
         if r is not None:
             return _ck(r)
     ks, kh, T, H, D = _rows3(k, layout, "k")
@@ -810,8 +847,8 @@ def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_sca
     dt = k.dtype
     if T != Tv or H != Hv or D != Dv or dt is not v.dtype:
         raise ValueError("k and v must have one shape and dtype")
-    tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new)
-    pk, pv, pks, pvs, sh = _cache(k_cache, v_cache, k_scale, v_scale)
+    tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_new, weights)
+    pk, pv, pks, pvs, sh, held = _cache(k_cache, v_cache, k_scale, v_scale)
     if H != sh[1] or D != sh[3]:
         raise ValueError("rows and cache differ in heads or D")
     idx = _device_of(tensors)
@@ -822,9 +859,13 @@ def cache_write(k, v, k_cache, v_cache, page_table, seq_lens, cu_new=None, k_sca
         if cu_new.numel() != B + 1:
             raise ValueError("cu_new must have B + 1 entries")
         cu = _flat(cu_new, _I32, "cu_new")
-    _launch(lib().ulysses_cache_write, idx, stream, tensors,
-            (k.data_ptr(), v.data_ptr(), ks, kh, vs, vh, T, B, cu, tab, cols, _flat(seq_lens, _I32, "seq_lens"), pk, pv,
-             pks, pvs, sh[0], sh[2], H, D, _code(dt, "k"), _code(k_cache.dtype, "k_cache")))
+    args = (k.data_ptr(), v.data_ptr(), ks, kh, vs, vh, T, B, cu, tab, cols, _flat(seq_lens, _I32, "seq_lens"), pk, pv, pks,
+            pvs)
+    sizes = (sh[0], sh[2], H, D, _code(dt, "k"), held)
+    if weights is None:
+        _launch(lib().ulysses_cache_write, idx, stream, tensors, (*args, *sizes))
+    else:
+        _launch(lib().ulysses_cache_write_weights, idx, stream, tensors, (*args, _weights(weights, sh), *sizes))
 
 
 def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=None, v_scale=None, dtype=None,
@@ -833,15 +874,14 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=
     (cu_seqlens[b] <= t < cu_seqlens[b+1]), is position first[b] + t -
     cu_seqlens[b] (first None: 0).  Returns (k, v) with T tokens, [T, H_kv, D]
     or [H_kv, T, D]; rows from cu_seqlens[B] on are left as they were.  dtype:
-    the cache's, or bf16 (default) / fp32 from an e4m3 cache."""
+    the cache's, or bf16 (default) / fp32 from an e4m3 or 4-bit cache."""
     if _fast is not None and stream is None:
         r = _fast.cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first, k_scale, v_scale, dtype, layout, out)
         if r is not None:
             return r if type(r) is not int else _ck(r)
-    pk, pv, pks, pvs, (n_pages, H, page, D) = _cache(k_cache, v_cache, k_scale, v_scale)
-    held = k_cache.dtype
+    pk, pv, pks, pvs, (n_pages, H, page, D), held = _cache(k_cache, v_cache, k_scale, v_scale)
     if dtype is None:
-        dtype = out[0].dtype if out is not None else _BF16 if held is _F8 else held
+        dtype = out[0].dtype if out is not None else _BF16 if held in (E4M3, E2M1) else k_cache.dtype
     B = cu_seqlens.numel() - 1
     tab, cols = _batch_table(page_table, B, "cu_seqlens")
     at = None
@@ -865,49 +905,109 @@ def cache_read(k_cache, v_cache, page_table, cu_seqlens, T, first=None, k_scale=
     tensors = (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, first)
     _launch(lib().ulysses_cache_read, idx, stream, tensors,
             (pk, pv, pks, pvs, tab, cols, _flat(cu_seqlens, _I32, "cu_seqlens"), at, k.data_ptr(), v.data_ptr(), ks, kh,
-             vs, vh, T, B, n_pages, page, H, D, _code(dtype, "k"), _code(held, "k_cache")))
+             vs, vh, T, B, n_pages, page, H, D, _code(dtype, "k"), held))
     return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _evict_bytes(*sizes):
+    return lib().ulysses_cache_evict_workspace(*sizes)
+
+
+def cache_evict_workspace(k_cache, page_table):
+    """Workspace for cache_evict on tensors of these shapes (uint8, on their
+    device)."""
+    n = _evict_bytes(page_table.shape[0], k_cache.shape[1], page_table.shape[1], k_cache.shape[2])
+    return torch.empty(n, dtype=torch.uint8, device=k_cache.device)
+
+
+def cache_evict(k_cache, v_cache, weights, page_table, seq_lens, keep, recent=0, k_scale=None, v_scale=None, out=None,
+                workspace=None, stream=None):
+    """Take the tokens with the least attention weight out of the paged cache.
+
+    Of a sequence's n = seq_lens[b] tokens min(n, keep[b]) stay (keep int32 [B];
+    negative: all), for each kv head its own: the last `recent` of them for
+    their age, and of those before the ones of greatest weight (the lower
+    position first among equals, NaN above everything).  They close up in their
+    order to positions 0, 1, ..., in place, with their scales and weights; the
+    places behind are left as they were, and pages that hold none of them are
+    the caller's again.  The sequences of a call must not share pages.  Returns
+    the new lengths int32 [B] (out: into this tensor, which may be seq_lens).
+    workspace: cache_evict_workspace(), for calls that do not overlap on the
+    GPU; made per call if not given.  A sequence with a bad length or page is
+    left as it is, and raises in check()."""
+    if _fast is not None and stream is None:
+        r = _fast.cache_evict(k_cache, v_cache, weights, page_table, seq_lens, keep, recent, k_scale, v_scale, out, workspace)
+        if r is not None:
+            return r if type(r) is not int else _ck(r)
+    pk, pv, pks, pvs, sh, held = _cache(k_cache, v_cache, k_scale, v_scale)
+    n_pages, H, page, D = sh
+    B = seq_lens.numel()
+    idx = _device_of((k_cache, v_cache, weights, page_table, seq_lens, keep, k_scale, v_scale, out, workspace))
+    pw = _weights(weights, sh)
+    tab, cols = _batch_table(page_table, B, "seq_lens")
+    if keep.numel() != B:
+        raise ValueError("keep must have B entries")
+    if out is None:
+        out = _empty(seq_lens, (B,), _I32, stream)
+    elif out.numel() != B:
+        raise ValueError("out must have B entries")
+    if workspace is None:
+        n = _evict_bytes(B, H, cols, page)
+        if n:
+            workspace = _empty(k_cache, (n,), _U8, stream)
+    ws, n = (None, 0) if workspace is None else (_flat(workspace, _U8, "workspace"), workspace.numel())
+    _launch(lib().ulysses_cache_evict, idx, stream,
+            (k_cache, v_cache, weights, page_table, seq_lens, keep, k_scale, v_scale, out, workspace),
+            (pk, pv, pks, pvs, pw, tab, cols, _flat(seq_lens, _I32, "seq_lens"), _flat(keep, _I32, "keep"), recent,
+             _flat(out, _I32, "out"), B, n_pages, page, H, D, held, ws, n))
+    return out
 
 
 # --------------------------------------------------------------- single-token attention
 
 @functools.lru_cache(maxsize=256)
-def _decode_bytes(*sizes):
-    return lib().ulysses_attn_decode_workspace(*sizes)
+def _decode_bytes(weights, *sizes):
+    return (lib().ulysses_attn_decode_weights_workspace if weights else lib().ulysses_attn_decode_workspace)(*sizes)
 
 
-def attn_decode_workspace(q, k_cache, page_table, layout="seq"):
+def attn_decode_workspace(q, k_cache, page_table, layout="seq", weights=False):
     """Workspace for attn_decode on tensors of these shapes (uint8, on their
-    device; empty where the call needs none)."""
+    device; empty where the call needs none).  weights: for calls with
+    weights, which keep the scores of every position of the table there."""
     _, _, B, H_q, D = _rows3(q, layout, "q")
-    n = _decode_bytes(B, H_q, k_cache.shape[1], D, page_table.shape[1], k_cache.shape[2], _code(q.dtype, "q"),
-                      _code(k_cache.dtype, "k_cache"))
+    n = _decode_bytes(bool(weights), B, H_q, k_cache.shape[1], D, page_table.shape[1], k_cache.shape[2], _code(q.dtype, "q"),
+                      E2M1 if k_cache.dtype is _U8 else _code(k_cache.dtype, "k_cache"))
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale=None, scale=None, layout="seq",
-                workspace=None, out=None, lse=None, stream=None):
+                workspace=None, out=None, lse=None, stream=None, weights=None):
     """Attention of one new token per sequence over the paged cache.
 
     q: [B, H_q, D] ("seq") or [H_q, B, D] ("head", as qkv_proj gives it), any
-    strides with D contiguous; bf16 (bf16 or e4m3 cache) or fp32 (fp32 or e4m3
-    cache).  The keys of sequence b are its first seq_lens[b] (int32 [B])
-    cached positions; length 0 gives O = 0, LSE = -inf.  Returns (O shaped as
-    q, LSE [B, H_q] fp32).  workspace: attn_decode_workspace(), for calls that
-    do not overlap on the GPU; made per call if not given."""
+    strides with D contiguous; bf16 (bf16, e4m3 or 4-bit cache) or fp32 (fp32,
+    e4m3 or 4-bit cache).  The keys of sequence b are its first seq_lens[b]
+    (int32 [B]) cached positions; length 0 gives O = 0, LSE = -inf.  Returns (O
+    shaped as q, LSE [B, H_q] fp32).  weights (cache_weights()): each key's
+    attention weight, summed over the query heads of its kv head, is added to
+    its slot's.  workspace: attn_decode_workspace(), for calls that do not
+    overlap on the GPU; made per call if not given."""
     if _fast is not None and stream is None:
         r = _fast.attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale, v_scale, scale, layout, workspace, out,
-                              lse)
+                              lse, weights)
         if r is not None:
             return r if type(r) is not int else _ck(r)
     qb, qh, B, H_q, D = _rows3(q, layout, "q")
-    pk, pv, pks, pvs, (n_pages, H_kv, page, Dc) = _cache(k_cache, v_cache, k_scale, v_scale)
+    pk, pv, pks, pvs, sh, dc = _cache(k_cache, v_cache, k_scale, v_scale)
+    n_pages, H_kv, page, Dc = sh
     if D != Dc or seq_lens.numel() != B:
         raise ValueError("attn_decode: q, cache and seq_lens differ in D or B")
-    idx = _device_of((q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse))
+    tensors = (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse, weights)
+    idx = _device_of(tensors)
     tab, cols = _batch_table(page_table, B, "q")
     dt = q.dtype
-    dq, dc = _code(dt, "q"), _code(k_cache.dtype, "k_cache")
+    dq = _code(dt, "q")
     if out is None:
         out = _empty(q, q.shape, dt, stream)
         ob, oh = (H_q * D, D) if layout == "seq" else (D, B * D)
@@ -923,12 +1023,15 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     else:
         pl = _flat(lse, _F32, "lse")
     if workspace is None:
-        n = _decode_bytes(B, H_q, H_kv, D, cols, page, dq, dc)
+        n = _decode_bytes(weights is not None, B, H_q, H_kv, D, cols, page, dq, dc)
         if n:
             workspace = _empty(q, (n,), _U8, stream)
     ws, n = (None, 0) if workspace is None else (_flat(workspace, _U8, "workspace"), workspace.numel())
-    _launch(lib().ulysses_attn_decode, idx, stream,
-            (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse),
-            (q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, _I32, "seq_lens"), out.data_ptr(), ob, oh,
-             pl, B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n))
+    args = (q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, _I32, "seq_lens"), out.data_ptr(), ob, oh, pl)
+    sizes = (B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n)
+    tensors = (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse, weights)
+    if weights is None:
+        _launch(lib().ulysses_attn_decode, idx, stream, tensors, (*args, *sizes))
+    else:
+        _launch(lib().ulysses_attn_decode_weights, idx, stream, tensors, (*args, _weights(weights, sh), *sizes))
     return out, lse
