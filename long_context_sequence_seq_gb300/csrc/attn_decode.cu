@@ -23,7 +23,7 @@ size_t decode_workspace(const DecodeArgs& a) {
 int launch_decode(const DecodeArgs& a, bool simt, cudaStream_t st) {
   if (a.cache_dtype == ULYSSES_E2M1) return launch_decode_4bit(a, simt, st);
   if (a.seen) return launch_decode_seen(a, simt, st);
-  return a.cache_dtype == ULYSSES_E4M3 ? run_decode<kE4m3, false>(a, simt, st) : run_decode<kAsIs, false>(a, simt, st);
+  return a.cache_dtype == ULYSSES_E4M3 ? run_decode<true, false>(a, simt, st) : run_decode<false, false>(a, simt, st);
 }
 
 }  // namespace ulysses

@@ -233,24 +233,21 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp, as exp2f, with
 // and with weights as a value alone 339.  Groups of more heads have no columns
 // left: 8 ragged sequences of up to 30000 e4m3 keys, 8 heads a kv head, 45 us, a
 // value alone 42; 16 heads 54 and 50.  In bf16 parts cost no time.)
-template <Held kHeld, int D, int NT, bool kTwice, bool kSeen_>
+template <bool kQuant, int D, int NT, bool kTwice, bool kSeen_>
 struct MatrixEngine {
   using TQ = __nv_bfloat16;
   static constexpr bool kSeen = kSeen_;
-  static constexpr bool kQuant = kHeld != kAsIs, kFour = kHeld == kE2m1;
   static constexpr int kHeads = kTwice ? 4 : 8 * NT;
   static constexpr int kProducts = (kQuant ? 2 : 3) - (kTwice ? 1 : 0);   // with V for a step's weights
-  static constexpr int kRowB = kFour ? D / 2 : (kQuant ? D : 2 * D);   // bytes of a row's values or codes
-  static constexpr int kSub = kRowB == 256 ? 1 : 2;       // units of a step: 32 registers of K and of V, 16, or 8
-  static constexpr int kKW = kRowB < 64 ? 1 : kRowB / 64; // K: words of a row per lane, of 16 bytes
-  static constexpr int kKE = D / (4 * kKW);               //    elements of a word (4 bits, D = 64: 8 bytes)
-  static constexpr int kVB = kRowB / 8 < 16 ? kRowB / 8 : 16;   // V: bytes of a word
+  static constexpr int kRowB = kQuant ? D : 2 * D;        // bytes of a row
+  static constexpr int kSub = kRowB == 256 ? 1 : 2;       // units of a step: 32 registers of K and of V, or 16
+  static constexpr int kKW = kRowB / 64;                  // K: 16-byte words of a row per lane
+  static constexpr int kVB = kRowB / 8 < 16 ? 8 : 16;     // V: bytes of a word
   static constexpr int kVW = kRowB / (8 * kVB);           //    words of a row per lane
-  static constexpr int kVR = (kVB + 3) / 4;               //    registers of a word
-  static constexpr int kVE = kFour ? 2 * kVB : (kQuant ? kVB : kVB / 2);   // elements of a word
+  static constexpr int kVE = kQuant ? kVB : kVB / 2;      //    elements of a word
   static constexpr int kMT = D / 16;                      // M tiles of O^T
 
-  uint32_t q[NT][D / 8];
+  uint32_t q[NT][kKW * 4 * (kQuant ? 2 : 1)];
   float acc[NT][kMT][4];
   float m[NT][2], l[NT][2], mw[NT][2], sc[NT][2];
   int lane, g, j;
@@ -259,7 +256,7 @@ struct MatrixEngine {
 
   // q as it is; scale_q() makes it the operand, behind the first rows' loads
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Piece& p) {
-    constexpr int kE = kKE;
+    constexpr int kE = kQuant ? 16 : 8;                    // elements of a K word
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int hl = kTwice ? g & 3 : t * 8 + g;
@@ -314,48 +311,16 @@ struct MatrixEngine {
 
   // rows of the units of a step; `unit` is its number in the cache, `keys` how
   // many of its 16 the piece has (0: none)
-  // (4 bits: kb, vb the block scales, of the lane's blocks)
-  struct Rows {
-    uint4 k[kSub][2][kKW];
-    uint32_t v[kSub][4][kVW * kVR];
-    float ks[kSub][2], vs[kSub][2];
-    uint32_t kb[kSub][2], vb[kSub][4];
-  };
-
-  // 4 bits: codes of the unit, which is the `off`-th of its page, and its block scales
-  __device__ __forceinline__ static const char* codes_at(const DecodeArgs& a, const void* cache, int unit, int off) {
-    return static_cast<const char*>(cache) + (int64_t)(unit - off) * (9 * D) + off * (8 * D);
-  }
-  __device__ __forceinline__ static const uint8_t* blocks_at(const DecodeArgs& a, const void* cache, int unit, int off) {
-    return static_cast<const uint8_t*>(cache) + (int64_t)(unit - off) * (9 * D) + (int64_t)a.page * (D / 2) + off * D;
-  }
+  struct Rows { uint4 k[kSub][2][kKW]; uint32_t v[kSub][4][kVW * kVB / 4]; float ks[kSub][2], vs[kSub][2]; };
 
   template <bool kAll>
-  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int u, int unit, int off, int keys) {
-    if (kFour) {
-      constexpr int kB = kKE / 2;                          // bytes of a word
-      const char* p = codes_at(a, a.kc, unit, off) + g * kRowB + j * kB;
-      const uint8_t* s = blocks_at(a, a.kc, unit, off) + g * (D / 16) + j * (D / 64);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool ok = kAll || g + 8 * x < keys;
-        if (kB == 16) {
-          r.k[u][x][0] = ok ? ld16(p + x * 8 * kRowB) : make_uint4(0, 0, 0, 0);
-          r.kb[u][x] = ok ? __ldg(reinterpret_cast<const uint16_t*>(s + x * 8 * (D / 16))) : 0;
-        } else {
-          const uint2 t = ok ? ld8(p + x * 8 * kRowB) : make_uint2(0, 0);
-          r.k[u][x][0] = make_uint4(t.x, t.y, 0, 0);
-          r.kb[u][x] = ok ? __ldg(s + x * 8 * (D / 16)) * 0x101u : 0;
-        }
-      }
-    }
+  __device__ __forceinline__ void load_k(const DecodeArgs& a, Rows& r, int u, int unit, int keys) {
     const char* p = reinterpret_cast<const char*>(a.kc) + ((int64_t)unit * kUnit + g) * kRowB + j * 16;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const bool ok = kAll || g + 8 * x < keys;
 #pragma unroll
-      for (int w = 0; w < kKW; ++w)
-        if (!kFour) r.k[u][x][w] = ok ? ld16(p + x * 8 * kRowB + w * 64) : make_uint4(0, 0, 0, 0);
+      for (int w = 0; w < kKW; ++w) r.k[u][x][w] = ok ? ld16(p + x * 8 * kRowB + w * 64) : make_uint4(0, 0, 0, 0);
     }
     if (kQuant) {
       const int64_t s = (int64_t)unit * kUnit + g;
@@ -368,24 +333,7 @@ struct MatrixEngine {
     }
   }
   template <bool kAll>
-  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int u, int unit, int off, int keys) {
-    if (kFour) {
-      const char* p = codes_at(a, a.vc, unit, off) + 2 * j * kRowB + g * kVB;
-      const uint8_t* s = blocks_at(a, a.vc, unit, off) + 2 * j * (D / 16) + g * kVE / 16;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = (x & 1) + (x >> 1) * 8;            // from 2 j on
-        const bool ok = kAll || 2 * j + key < keys;
-        if (kVB == 8) {
-          const uint2 t = ok ? ld8(p + key * kRowB) : make_uint2(0, 0);
-          r.v[u][x][0] = t.x; r.v[u][x][kVR - 1] = t.y;
-        } else {
-          r.v[u][x][0] = ok ? ld4(p + key * kRowB) : 0;
-        }
-        r.vb[u][x] = ok ? __ldg(s + key * (D / 16)) : 0;
-      }
-      return;
-    }
+  __device__ __forceinline__ void load_v(const DecodeArgs& a, Rows& r, int u, int unit, int keys) {
     const char* p = reinterpret_cast<const char*>(a.vc) + ((int64_t)unit * kUnit + 2 * j) * kRowB + g * kVB;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -393,10 +341,10 @@ struct MatrixEngine {
       const bool ok = kAll || 2 * j + key < keys;
 #pragma unroll
       for (int w = 0; w < kVW; ++w) {
-        if constexpr (kVB == 16) {
+        if (kVB == 16) {
           const uint4 t = ok ? ld16(p + key * kRowB + w * 128) : make_uint4(0, 0, 0, 0);
           r.v[u][x][w * 4] = t.x; r.v[u][x][w * 4 + 1] = t.y; r.v[u][x][w * 4 + 2] = t.z; r.v[u][x][w * 4 + 3] = t.w;
-        } else if constexpr (!kFour) {
+        } else {
           const uint2 t = ok ? ld8(p + key * kRowB) : make_uint2(0, 0);
           r.v[u][x][0] = t.x; r.v[u][x][1] = t.y;
         }
@@ -405,19 +353,19 @@ struct MatrixEngine {
   }
   // whole units take the path without predicates (warp-uniform)
   struct Next {
-    MatrixEngine& e; const DecodeArgs& a; const int (&unit)[kSub]; const int (&off)[kSub]; const int (&keys)[kSub];
+    MatrixEngine& e; const DecodeArgs& a; const int (&unit)[kSub]; const int (&keys)[kSub];
     __device__ __forceinline__ void load_k(Rows& r) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        if (keys[u] == kUnit) e.template load_k<true>(a, r, u, unit[u], off[u], kUnit);
-        else e.template load_k<false>(a, r, u, unit[u], off[u], keys[u]);
+        if (keys[u] == kUnit) e.template load_k<true>(a, r, u, unit[u], kUnit);
+        else e.template load_k<false>(a, r, u, unit[u], keys[u]);
       }
     }
     __device__ __forceinline__ void load_v(Rows& r) {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        if (keys[u] == kUnit) e.template load_v<true>(a, r, u, unit[u], off[u], kUnit);
-        else e.template load_v<false>(a, r, u, unit[u], off[u], keys[u]);
+        if (keys[u] == kUnit) e.template load_v<true>(a, r, u, unit[u], kUnit);
+        else e.template load_v<false>(a, r, u, unit[u], keys[u]);
       }
     }
   };
@@ -458,27 +406,8 @@ struct MatrixEngine {
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int c = 0; c < 4; ++c) h[k][t][c] = 0.f;
-    if (kFour) {
-      // 2 + 4 significant bits, from 2^-10 to 2688 (or 0): f16 holds code * block scale exactly
-      const uint32_t lo[4] = {r.k[u][0][0].x, r.k[u][0][0].y, r.k[u][0][0].z, r.k[u][0][0].w};
-      const uint32_t hi[4] = {r.k[u][1][0].x, r.k[u][1][0].y, r.k[u][1][0].z, r.k[u][1][0].w};
-      const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)r.kb[u][0]), b1 = e4m3x2_to_f16x2((uint16_t)r.kb[u][1]);
 #pragma unroll
-      for (int i = 0; i < kKE / 8; ++i) {
-        const uint32_t s0 = __byte_perm(b0, b0, i < 2 ? 0x1010 : 0x3232), s1 = __byte_perm(b1, b1, i < 2 ? 0x1010 : 0x3232);
-        uint32_t f0[4], f1[4];
-        e2m1x8_to_f16x2(lo[i], f0);
-        e2m1x8_to_f16x2(hi[i], f1);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t f[4] = {hmul2(f0[2 * x], s0), hmul2(f1[2 * x], s1), hmul2(f0[2 * x + 1], s0), hmul2(f1[2 * x + 1], s1)};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(h[x][t], f, q[t][i * 4 + 2 * x], q[t][i * 4 + 2 * x + 1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < (kFour ? 0 : kKW); ++w) {
+    for (int w = 0; w < kKW; ++w) {
       const uint32_t lo[4] = {r.k[u][0][w].x, r.k[u][0][w].y, r.k[u][0][w].z, r.k[u][0][w].w};
       const uint32_t hi[4] = {r.k[u][1][w].x, r.k[u][1][w].y, r.k[u][1][w].z, r.k[u][1][w].w};
       if (!kQuant) {
@@ -586,36 +515,13 @@ struct MatrixEngine {
             for (int k = 0; k < kProducts; ++k) pw[k][t][x] = transpose8x8(part[k]);
           }
         }
-      if (kFour) {
-        // the codes of two rows are paired before they become f16, so a pair comes out as the operand wants it
-        const uint32_t s0 = e4m3x2_to_f16x2((uint16_t)(r.vb[u][0] | r.vb[u][1] << 8));
-        const uint32_t s1 = e4m3x2_to_f16x2((uint16_t)(r.vb[u][2] | r.vb[u][3] << 8));
 #pragma unroll
-        for (int i = 0; i < kVR; ++i) {
-          const uint32_t m = 0x0f0f0f0fu;
-          const uint32_t w0 = r.v[u][0][i], w1 = r.v[u][1][i], w2 = r.v[u][2][i], w3 = r.v[u][3][i];
-          uint32_t e0[4], o0[4], e1[4], o1[4];             // even and odd elements, of rows 2j, 2j + 1 and of 2j + 8, 2j + 9
-          e2m1x8_to_f16x2((w0 & m) | ((w1 << 4) & ~m), e0);
-          e2m1x8_to_f16x2(((w0 >> 4) & m) | (w1 & ~m), o0);
-          e2m1x8_to_f16x2((w2 & m) | ((w3 << 4) & ~m), e1);
-          e2m1x8_to_f16x2(((w2 >> 4) & m) | (w3 & ~m), o1);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t f[4] = {hmul2(e0[x], s0), hmul2(o0[x], s0), hmul2(e1[x], s1), hmul2(o1[x], s1)};
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int k = 0; k < kProducts; ++k) mma_f16(acc[t][i * 4 + x], f, pw[k][t][0], pw[k][t][1]);
-          }
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < (kFour ? 0 : kVW); ++w)
+      for (int w = 0; w < kVW; ++w)
 #pragma unroll
         for (int e = 0; e < kVE / 2; ++e) {
           uint32_t v[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = v_pair(&r.v[u][x][w * kVR], e);
+          for (int x = 0; x < 4; ++x) v[x] = v_pair(&r.v[u][x][w * 4], e);
           const uint32_t f[4] = {__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632),
                                  __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632)};
 #pragma unroll
@@ -635,7 +541,7 @@ struct MatrixEngine {
     const int64_t total = a.num_pages * a.H_kv * a.page;
     Walk walk(a, p);
     Rows r;
-    int unit[kSub], off[kSub], keys[kSub], nkeys[kSub], pg[kSub];
+    int unit[kSub], keys[kSub], nkeys[kSub], pg[kSub];
     float* to = p.scores;
     int left = min(p.len - p.unit0 * kUnit, p.units * kUnit);   // keys of the piece from the step on
     // page ids are read a step ahead of the rows, rows a step ahead of their use
@@ -644,7 +550,6 @@ struct MatrixEngine {
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
         unit[u] = w.unit(pg[u]);
-        off[u] = w.off;
         n[u] = unit[u] >= 0 && in_bounds((int64_t)unit[u] * kUnit + kUnit - 1, total)
                    ? min(max(keys_left - u * kUnit, 0), kUnit) : 0;
         w.next();
@@ -662,14 +567,14 @@ struct MatrixEngine {
       for (int u = 0; u < kSub; ++u) { pg[u] = w.fetch(); w.next(); }
     }
     places(left, keys);
-    Next now{*this, a, unit, off, keys};
+    Next now{*this, a, unit, keys};
     now.load_k(r);
     now.load_v(r);
     scale_q();
     while (left > 0) {
       left -= kSub * kUnit;
       places(left, nkeys);
-      Next next{*this, a, unit, off, nkeys};
+      Next next{*this, a, unit, nkeys};
       step(a, p, to, r, keys, next);
       if (kSeen) to += kSub * p.heads * kUnit;
 #pragma unroll
@@ -1283,11 +1188,23 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t at, int rank) {
   return v;
 }
 
+// Shared memory that a warp of the engine copies rows through (Engine::kRing bytes; most have none).
+template <class Engine, class = void> struct Ring { static constexpr int kBytes = 0; };
+template <class Engine> struct Ring<Engine, std::enable_if_t<(Engine::kRing > 0)>> { static constexpr int kBytes = Engine::kRing; };
+template <class Engine>
+__host__ __device__ constexpr int ring_bytes() { return Ring<Engine>::kBytes; }
+template <class Engine>
+__device__ __forceinline__ Engine make_engine(int lane, char* ring) {
+  if constexpr (ring_bytes<Engine>() > 0) return Engine(lane, ring);
+  else return Engine(lane);
+}
+
 template <class Engine, int D, int kCtas>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid_constant__ DecodeArgs a,
                                                                     const __grid_constant__ Plan p) {
-  // prefix[b]: units of the sequences before b (of one head)
-  extern __shared__ int prefix[];
+  // the engines' rings, and prefix[b]: units of the sequences before b (of one head)
+  extern __shared__ __align__(16) char shared[];
+  int* const prefix = reinterpret_cast<int*>(shared + kWarps * ring_bytes<Engine>());
   __shared__ int sums[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int carry = 0;
@@ -1331,7 +1248,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
     }
     b = lo;
   }
-  Engine e(lane);
+  Engine e = make_engine<Engine>(lane, shared + warp * ring_bytes<Engine>());
   int at = begin;
   while (at < end) {
     while (prefix[b + 1] * per <= at) ++b;
@@ -1438,7 +1355,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
     pc.heads = heads;
     pc.scores = scores_of(a, item, heads) + (int64_t)pc.unit0 * heads * kUnit;
   }
-  Engine e(lane);
+  extern __shared__ __align__(16) char shared[];
+  Engine e = make_engine<Engine>(lane, shared + warp * ring_bytes<Engine>());
   e.begin(a, pc);
   if (pc.units > 0) e.run(a, pc);
   e.partial(sml[warp], &so[warp][0][0], pc.gn);
@@ -1706,7 +1624,13 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
     cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = kWarps * ring_bytes<Engine>();
     cfg.stream = st;
+    if (ring_bytes<Engine>() > 0) {
+      static PerDeviceOnce<> once;
+      if (const int rc = opt_in_smem(once, (const void*)decode_cluster_kernel<Engine, D, kCtas>, (int)cfg.dynamicSmemBytes, "attn_decode"))
+        return rc;
+    }
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)c;
@@ -1740,7 +1664,13 @@ int run(const DecodeArgs& a, cudaStream_t st) {
       x.fin = (float2*)(ws + w.fin);
       x.scores = (float*)(ws + w.scores);
     }
-    decode_kernel<Engine, D, kCtas><<<ctas, kWarps * 32, (x.B + 1) * sizeof(int), st>>>(x, p);
+    if (ring_bytes<Engine>() > 0) {
+      static PerDeviceOnce<> once;
+      if (const int rc = opt_in_smem(once, (const void*)decode_kernel<Engine, D, kCtas>,
+                                     kWarps * ring_bytes<Engine>() + (kMaxBatch + 1) * (int)sizeof(int), "attn_decode"))
+        return rc;
+    }
+    decode_kernel<Engine, D, kCtas><<<ctas, kWarps * 32, kWarps * ring_bytes<Engine>() + (x.B + 1) * sizeof(int), st>>>(x, p);
     count_launch();
     int rc = check_launch("attn_decode");
     if (rc) return rc;
@@ -1782,11 +1712,11 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   return ULYSSES_OK;
 }
 
-template <Held kHeld, int D, bool kSeen>
+template <bool kQuant, int D, bool kSeen>
 int run_matrix(const DecodeArgs& a, cudaStream_t st) {
-  if (a.G <= 4) return run<MatrixEngine<kHeld, D, 1, true, kSeen>, D, 3>(a, st);
-  if (a.G <= 8) return run<MatrixEngine<kHeld, D, 1, false, kSeen>, D, 3>(a, st);
-  return run<MatrixEngine<kHeld, D, 2, false, kSeen>, D, 2>(a, st);
+  if (a.G <= 4) return run<MatrixEngine<kQuant, D, 1, true, kSeen>, D, 3>(a, st);
+  if (a.G <= 8) return run<MatrixEngine<kQuant, D, 1, false, kSeen>, D, 3>(a, st);
+  return run<MatrixEngine<kQuant, D, 2, false, kSeen>, D, 2>(a, st);
 }
 template <typename TQ, typename TC, int D, bool kSeen>
 int run_simt(const DecodeArgs& a, cudaStream_t st) {
@@ -1795,23 +1725,20 @@ int run_simt(const DecodeArgs& a, cudaStream_t st) {
   return run<SimtEngine<TQ, TC, D, 4, kSeen>, D, 2>(a, st);
 }
 
-// The element type of a cache, held so, of queries of type TQ.
-template <Held kHeld, typename TQ> struct RowType { using T = TQ; };
-template <typename TQ> struct RowType<kE4m3, TQ> { using T = uint8_t; };
-template <typename TQ> struct RowType<kE2m1, TQ> { using T = Codes4; };
-
-template <Held kHeld, int D, bool kSeen>
-int run_held(const DecodeArgs& a, bool simt, cudaStream_t st) {
+template <bool kQuant, int D, bool kSeen>
+int run_engine(const DecodeArgs& a, bool simt, cudaStream_t st) {
   if (use_simt(a, simt)) {
-    if (a.dtype == ULYSSES_BF16) return run_simt<__nv_bfloat16, typename RowType<kHeld, __nv_bfloat16>::T, D, kSeen>(a, st);
-    return run_simt<float, typename RowType<kHeld, float>::T, D, kSeen>(a, st);
+    if (a.dtype == ULYSSES_BF16)
+      return run_simt<__nv_bfloat16, std::conditional_t<kQuant, uint8_t, __nv_bfloat16>, D, kSeen>(a, st);
+    return run_simt<float, std::conditional_t<kQuant, uint8_t, float>, D, kSeen>(a, st);
   }
-  if (a.dtype == ULYSSES_BF16) return run_matrix<kHeld, D, kSeen>(a, st);
-  return run<SplitEngine<kHeld, D, kSeen>, D, D == 128 ? 2 : 3>(a, st);
+  if (a.dtype == ULYSSES_BF16) return run_matrix<kQuant, D, kSeen>(a, st);
+  return run<SplitEngine<kQuant ? kE4m3 : kAsIs, D, kSeen>, D, D == 128 ? 2 : 3>(a, st);
 }
-template <Held kHeld, bool kSeen>
+// Caches as they are (kQuant: in e4m3).
+template <bool kQuant, bool kSeen>
 int run_decode(const DecodeArgs& a, bool simt, cudaStream_t st) {
-  return a.D == 128 ? run_held<kHeld, 128, kSeen>(a, simt, st) : run_held<kHeld, 64, kSeen>(a, simt, st);
+  return a.D == 128 ? run_engine<kQuant, 128, kSeen>(a, simt, st) : run_engine<kQuant, 64, kSeen>(a, simt, st);
 }
 
 }  // namespace

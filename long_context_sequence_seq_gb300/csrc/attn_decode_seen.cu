@@ -8,7 +8,7 @@ namespace ulysses {
 ULYSSES_ERROR_READER(read_error_attn_decode_seen)
 
 int launch_decode_seen(const DecodeArgs& a, bool simt, cudaStream_t st) {
-  return a.cache_dtype == ULYSSES_E4M3 ? run_decode<kE4m3, true>(a, simt, st) : run_decode<kAsIs, true>(a, simt, st);
+  return a.cache_dtype == ULYSSES_E4M3 ? run_decode<true, true>(a, simt, st) : run_decode<false, true>(a, simt, st);
 }
 
 }  // namespace ulysses
