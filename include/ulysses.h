@@ -391,8 +391,9 @@ int ulysses_rope_bwd(const ulysses_rope_item* items, int n_items, const int32_t*
  *   round to nearest even; a row with an infinity or NaN gets scale NaN, so it
  *   reads back as NaN.  ULYSSES_E2M1 stores scale = the least power of two with
  *   max(max|x|, 2^-100) <= 2688 * scale, b = e4m3(max of the block's |x / scale|
- *   / 6) and code = e2m1(x / scale / b) (0 where b is 0), all to nearest even;
- *   infinities and NaN as with ULYSSES_E4M3.
+ *   / 6) and code = e2m1(x / scale / b) (0 where b is 0), all to nearest even
+ *   (a code of magnitude 0 may have either sign); infinities and NaN as with
+ *   ULYSSES_E4M3.
  *   The tokens of one call must have distinct places (a page owned by two
  *   sequences must not be written through both in one call).
  *
@@ -494,7 +495,7 @@ int ulysses_attn_decode_weights(const void* q, int64_t q_b, int64_t q_h, const v
  * distinct.  A sequence whose length does not fit the table, or that has a page
  * id outside [0, num_pages) below its length, is left as it is (new_lens its
  * length) and makes ulysses_check return ULYSSES_ERR_BAD_PAGES.
- * B' * H_kv * table_cols * page_size <= 2^36 with B' = min(B, 2048). */
+ * B' * H_kv * (table_cols * page_size + 32) <= 2^35 with B' = min(B, 2048). */
 size_t ulysses_cache_evict_workspace(int B, int H_kv, int table_cols, int page_size);
 int ulysses_cache_evict(void* k_cache, void* v_cache, float* k_scale, float* v_scale, float* weights,
                         const int32_t* page_table, int table_cols, const int32_t* seq_lens, const int32_t* keep, int recent,

@@ -335,10 +335,10 @@ int evict_args(EvictArgs& a, int B, int H_kv, int cols, int page) {
     return set_error(ULYSSES_ERR_INVALID, "bad sizes B=%d H_kv=%d table_cols=%d", B, H_kv, cols);
   if ((int64_t)cols * page > kMaxPositions)
     return set_error(ULYSSES_ERR_UNSUPPORTED, "table_cols * page_size = %lld above 2^30 positions", (long long)cols * page);
-  // chunks of 64 positions of a launch's sequences (at most 2048) are counted in 31 bits
+  // chunks of 32 positions of a launch's sequences (at most 2048) are counted in 31 bits
   const int64_t b = B < 2048 ? B : 2048;
-  if (((int64_t)cols * page / 64 + 1) * b * H_kv > (1 << 30))
-    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache_evict: B * H_kv * table_cols * page_size above 2^36");
+  if (((int64_t)cols * page / 32 + 1) * b * H_kv > (1 << 30))
+    return set_error(ULYSSES_ERR_UNSUPPORTED, "cache_evict: B * H_kv * table_cols * page_size above 2^35");
   a = EvictArgs{};
   a.B = B; a.H = H_kv; a.cols = cols; a.page = page;
   return ULYSSES_OK;

@@ -13,8 +13,7 @@ size_t decode_workspace(const DecodeArgs& a) {
   size_t most = 0;
   for (const bool simt : {false, true}) {
     const int heads = heads_of(a, simt);
-    const bool cluster = cluster_of(a, heads) != 0;
-    const size_t n = cluster && !a.seen ? 0 : ws_layout(a, heads, cluster).total;
+    const size_t n = cluster_of(a, heads) ? 0 : ws_layout(a, heads).total;
     if (n > most) most = n;
   }
   return most;

@@ -95,6 +95,7 @@ constexpr float kTiny = 1.17549435082228751e-38f;   // 2^-126
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                       // of a CTA
 constexpr int kMinUnits = 2;                    // of a warp, where there are enough for all
+constexpr int kClusterUnits = 16;               // of a warp of a cluster, at most
 constexpr int kMaxBatch = 2048;                 // sequences of one launch (their prefix sums sit in shared memory)
 
 // How a launch is split (host), the same for both of its kernels.
@@ -179,13 +180,17 @@ __device__ __forceinline__ float* scores_of(const DecodeArgs& a, int64_t item, i
   const int64_t units = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit;
   return a.scores + item * units * heads * kUnit;
 }
-// Adds to the weight of key `key` of a unit of an item.  One addition a slot and
-// call, unless sequences share a page: then it gathers from all of them.
-__device__ __forceinline__ void add_weight(const DecodeArgs& a, int b, int h, int unit, int key, float x) {
+// Row number in the cache ([num_pages][H_kv][page]) of the first key of a unit of an
+// item; -1: its page is out of range (reported where its scores were to be formed).
+__device__ __forceinline__ int64_t row_of_unit(const DecodeArgs& a, int b, int h, int unit) {
   const int per = a.page / kUnit, col = unit / per;
   const int pg = __ldg(a.table + (int64_t)b * a.cols + col);
-  if ((unsigned)pg >= (unsigned)a.num_pages) return;       // reported where its scores were to be formed
-  const int64_t row = ((int64_t)(pg * (int64_t)a.H_kv + h) * per + (unit - col * per)) * kUnit + key;
+  if ((unsigned)pg >= (unsigned)a.num_pages) return -1;
+  return ((pg * (int64_t)a.H_kv + h) * per + (unit - col * per)) * kUnit;
+}
+// Adds to a slot's weight.  One addition a slot and call, unless sequences share a
+// page: then it gathers from all of them.
+__device__ __forceinline__ void add_weight(const DecodeArgs& a, int64_t row, float x) {
   if (in_bounds(row, a.num_pages * a.H_kv * a.page)) atomicAdd(a.seen + row, x);
 }
 // The head's maximum and the inverse of its sum, for the same pass.
@@ -1311,20 +1316,35 @@ __global__ void __launch_bounds__(kSeenThreads) decode_weights_kernel(const __gr
     const int item0 = prefix[b] * a.H_kv + h * units, unit0 = at - item0;
     const int n = min(end, item0 + units) - at, len = length_of(a, b);
     const float2* fin = a.fin + (int64_t)b * a.H_q + h * a.G;
-    for (int u = 0; u < n; u += 2) {
-      const int unit = unit0 + u + (lane >> 4), key = lane & 15;
-      if (u + (lane >> 4) >= n || unit * kUnit + key >= len) continue;
-      float x = 0.f;
+    // a lane a key of four pairs of units at a time: their loads do not wait for each other
+    constexpr int kPairs = 4;
+    for (int u = 0; u < n; u += 2 * kPairs) {
+      const int key = lane & 15;
+      int unit[kPairs];
+      int64_t row[kPairs];
+      float x[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const int v = u + 2 * i + (lane >> 4);
+        unit[i] = unit0 + v;
+        const bool live = v < n && unit[i] * kUnit + key < len;
+        row[i] = live ? row_of_unit(a, b, h, unit[i]) : -1;
+        if (!live) unit[i] = unit0;
+        x[i] = 0.f;
+      }
       for (int g = 0; g < p.groups; ++g) {
         const int g0 = g * p.heads, gn = min(a.G - g0, p.heads);
-        const float* s = scores_of(a, ((int64_t)b * a.H_kv + h) * p.groups + g, p.heads) + (int64_t)unit * p.heads * kUnit + key;
+        const float* s = scores_of(a, ((int64_t)b * a.H_kv + h) * p.groups + g, p.heads) + key;
 #pragma unroll 4
-        for (int i = 0; i < gn; ++i) {
-          const float2 f = fin[g0 + i];
-          x += exp2f(s[i * kUnit] - f.x) * f.y;
+        for (int k = 0; k < gn; ++k) {
+          const float2 f = fin[g0 + k];
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) x[i] += exp2f(s[((int64_t)unit[i] * p.heads + k) * kUnit] - f.x) * f.y;
         }
       }
-      add_weight(a, b, h, unit, key, x);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        if (row[i] >= 0) add_weight(a, row[i] + key, x[i]);
     }
     at += n;
   }
@@ -1351,11 +1371,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   const int units = (pc.len + kUnit - 1) / kUnit, warps = ctas * kWarps, w = rank * kWarps + warp;
   pc.unit0 = first_unit(w, warps, units);
   pc.units = first_unit(w + 1, warps, units) - pc.unit0;
-  if (Engine::kSeen) {
-    pc.heads = heads;
-    pc.scores = scores_of(a, item, heads) + (int64_t)pc.unit0 * heads * kUnit;
-  }
   extern __shared__ __align__(16) char shared[];
+  if (Engine::kSeen) {                                     // behind the rings
+    pc.heads = heads;
+    pc.scores = reinterpret_cast<float*>(shared + kWarps * ring_bytes<Engine>()) + warp * (kClusterUnits * heads * kUnit);
+  }
   Engine e = make_engine<Engine>(lane, shared + warp * ring_bytes<Engine>());
   e.begin(a, pc);
   if (pc.units > 0) e.run(a, pc);
@@ -1365,29 +1385,40 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   const int total = pc.gn * D / 4, each = (total + ctas - 1) / ctas;
   const uint32_t o_at = tc::smem_u32(&so[0][0][0]), ml_at = tc::smem_u32(&sml[0][0]);
   if (Engine::kSeen && pc.units > 0) {                     // (one group: the item has all of the kv head's query heads)
-    float m = kNoMax, l = 0.f;                             // of head `lane`
-    if (lane < pc.gn) {
-      for (int r = 0; r < ctas; ++r)
+    float mine = kNoMax, inv = 0.f;                        // of head `lane`: the maximum, and 1 / the sum
+    const int piece = min(lane, ctas * kWarps - 1);        // a lane a piece: at most 8 CTAs' four
+    for (int h = 0; h < pc.gn; ++h) {
+      float2 ml = cluster_ld2(ml_at + ((piece % kWarps) * kH + h) * 8, piece / kWarps);
+      float top = ml.x, l = lane < ctas * kWarps ? ml.y : 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) m = fmaxf(m, cluster_ld2(ml_at + (k * kH + lane) * 8, r).x);
-      for (int r = 0; r < ctas; ++r)
+      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      l *= exp2f(ml.x - top);
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float2 ml = cluster_ld2(ml_at + (k * kH + lane) * 8, r);
-          l += ml.y * exp2f(ml.x - m);
-        }
+      for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == h) { mine = top; inv = l == 0.f ? 0.f : 1.f / l; }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int u = 0; u < pc.units; u += 2) {                // the warp's own scores, two units at a time
-      const int mine = u + (lane >> 4), key = lane & 15;
-      const bool live = mine < pc.units && (pc.unit0 + mine) * kUnit + key < pc.len;
-      const float* s = pc.scores + (int64_t)(live ? mine : 0) * heads * kUnit + key;
-      float x = 0.f;
-      for (int h = 0; h < pc.gn; ++h) {
-        const float mh = __shfl_sync(0xffffffffu, m, h), ih = __shfl_sync(0xffffffffu, inv, h);
-        if (live) x += exp2f(s[h * kUnit] - mh) * ih;
+    constexpr int kPairs = 4;                              // of units, a lane a key: the warp's own scores
+    for (int u = 0; u < pc.units; u += 2 * kPairs) {
+      const int key = lane & 15;
+      int64_t row[kPairs];
+      float x[kPairs];
+      int unit[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        unit[i] = u + 2 * i + (lane >> 4);
+        const bool live = unit[i] < pc.units && (pc.unit0 + unit[i]) * kUnit + key < pc.len;
+        row[i] = live ? row_of_unit(a, pc.b, pc.h, pc.unit0 + unit[i]) : -1;
+        if (!live) unit[i] = 0;
+        x[i] = 0.f;
       }
-      if (live) add_weight(a, pc.b, pc.h, pc.unit0 + mine, key, x);
+      for (int h = 0; h < pc.gn; ++h) {
+        const float mh = __shfl_sync(0xffffffffu, mine, h), ih = __shfl_sync(0xffffffffu, inv, h);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) x[i] += exp2f(pc.scores[(unit[i] * heads + h) * kUnit + key] - mh) * ih;
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        if (row[i] >= 0) add_weight(a, row[i] + key, x[i]);
     }
   }
   for (int i = rank * each + threadIdx.x; i < min(total, (rank + 1) * each); i += kWarps * 32) {
@@ -1572,7 +1603,6 @@ inline int heads_of(const DecodeArgs& a, bool simt) {
 // 5000 keys.  16 x 4000 ragged 32.7 and 19.5, 4 x 16000 ragged 37.0 and 22.2, which
 // twice as many units would take.)  152 SMs and not the device's: the workspace is
 // asked for without one, and both have to choose alike.
-constexpr int kClusterUnits = 16;
 inline int cluster_of(const DecodeArgs& a, int heads) {
   if (a.seen && a.G > heads) return 0;              // groups of one kv head add to the same weights
   const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
@@ -1584,17 +1614,14 @@ inline int cluster_of(const DecodeArgs& a, int heads) {
   return c;
 }
 
-// cluster: without what the pieces of a split launch need
 struct WsLayout { size_t prefix, ml, o, fin, scores, total; };
-inline WsLayout ws_layout(const DecodeArgs& a, int heads, bool cluster) {
+inline WsLayout ws_layout(const DecodeArgs& a, int heads) {
   WsLayout w{};
   const int b = a.B < kMaxBatch ? a.B : kMaxBatch;
-  if (!cluster) {
-    w.ml = align256((size_t)(b + 1) * sizeof(int));
-    w.o = w.ml + align256((size_t)2 * kMaxWarps * heads * 8);
-    w.fin = w.o + align256((size_t)2 * kMaxWarps * heads * a.D * 4);
-    w.scores = w.fin + (a.seen ? align256((size_t)b * a.H_q * 8) : 0);
-  }
+  w.ml = align256((size_t)(b + 1) * sizeof(int));
+  w.o = w.ml + align256((size_t)2 * kMaxWarps * heads * 8);
+  w.fin = w.o + align256((size_t)2 * kMaxWarps * heads * a.D * 4);
+  w.scores = w.fin + (a.seen ? align256((size_t)b * a.H_q * 8) : 0);
   const size_t units = ((size_t)a.cols * a.page + kUnit - 1) / kUnit, groups = (a.G + heads - 1) / heads;
   w.total = w.scores + (a.seen ? align256((size_t)b * a.H_kv * groups * units * heads * kUnit * 4) : 0);
   return w;
@@ -1617,19 +1644,16 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   p.heads = a.G < Engine::kHeads ? a.G : Engine::kHeads;
   p.groups = (a.G + p.heads - 1) / p.heads;
   p.warps = ctas * kWarps;
-  char* ws = (char*)a.ws;
   if (const int c = cluster_of(a, p.heads)) {
-    DecodeArgs x = a;
-    if (Engine::kSeen) x.scores = (float*)(ws + ws_layout(a, p.heads, true).scores);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
     cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = kWarps * ring_bytes<Engine>();
+    constexpr int kScores = Engine::kSeen ? kClusterUnits * kUnit * 4 : 0;   // bytes of a head, in a warp
+    cfg.dynamicSmemBytes = kWarps * (ring_bytes<Engine>() + kScores * p.heads);
     cfg.stream = st;
-    if (ring_bytes<Engine>() > 0) {
+    if (constexpr int kMost = kWarps * (ring_bytes<Engine>() + kScores * Engine::kHeads)) {
       static PerDeviceOnce<> once;
-      if (const int rc = opt_in_smem(once, (const void*)decode_cluster_kernel<Engine, D, kCtas>, (int)cfg.dynamicSmemBytes, "attn_decode"))
-        return rc;
+      if (const int rc = opt_in_smem(once, (const void*)decode_cluster_kernel<Engine, D, kCtas>, kMost, "attn_decode")) return rc;
     }
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1637,12 +1661,13 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<Engine, D, kCtas>, x, p.groups, p.heads, c);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<Engine, D, kCtas>, a, p.groups, p.heads, c);
     if (err != cudaSuccess) return launch_failed("attn_decode", err);
     count_launch();
     return ULYSSES_OK;
   }
-  const WsLayout w = ws_layout(a, p.heads, false);
+  const WsLayout w = ws_layout(a, p.heads);
+  char* ws = (char*)a.ws;
   p.prefix = (int*)(ws + w.prefix);
   p.ml = (float2*)(ws + w.ml);
   p.o = (float*)(ws + w.o);

@@ -13,12 +13,13 @@
 // positions that stay.  Weights are ordered as unsigned numbers (sign and
 // magnitude made monotone; -0 as +0, NaN above everything).
 //
-// The second moves rows, in place: chunks of kChunk rows, K, V, scales and
-// weights, are read into registers and written kChunk places together.  A row
-// never moves up, so what a chunk overwrites are rows of itself and of at most
-// two chunks before it: it waits until those have been read.  CTAs take chunks
-// by a counter, in order; a chunk's reading waits for nothing, so the first
-// chunk that is not done can always go on.  Every kept row is read and written
+// The second moves rows, in place: a chunk of rows, K, V, scales and weights, is
+// read into registers and then written.  A row never moves up, so what a chunk of
+// C rows overwrites are rows of itself and of at most two chunks before it (the
+// C places hold at most C kept rows, neighbours in rank): it waits until those
+// have been read.  CTAs take chunks by a counter, in order, and a chunk's reading
+// waits for nothing but writes of chunks before it, so the first chunk that is not
+// done can always go on.  Every kept row is read and written
 // once, which is all the memory traffic there is beside the weights'.
 #include "internal.h"
 #include "rows.cuh"
@@ -34,8 +35,7 @@ using namespace rows;
 
 constexpr int kUnit = 16;          // positions of one thread at a time
 constexpr int kThreads = 512;      // of a selecting CTA
-constexpr int kChunk = 64;         // rows moved together
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256;  // that move rows, of a CTA
 constexpr int kMaxBatch = 2048;    // sequences of one launch (their prefix sums sit in shared memory)
 constexpr int kBins = 2048;        // of a digit of 11 bits
 
@@ -43,11 +43,13 @@ constexpr int kBins = 2048;        // of a digit of 11 bits
 struct Lists {
   int2* size;      // [B] (tokens before, tokens that stay); equal where nothing moves
   int* ticket;     // chunks taken
-  int* src;        // [B][H][positions] positions that stay, rising
-  int* before;     // [B][H][chunks] how many of those lie before position kChunk * c
+  int64_t* src;    // [B][H][positions] rows of the positions that stay, rising (rows: [num_pages][H][page])
+  int* before;     // [B][H][chunks] how many of those lie before position chunk * c
   int* read;       // [B][H][chunks] 1: the chunk's rows have been read
   int64_t positions, chunks;
+  int chunk;       // rows moved together: 16 KB of K and of V, at most 128
 };
+constexpr int chunk_of(int row_bytes) { return row_bytes >= 128 ? 16384 / row_bytes : 128; }
 
 // A weight as a number whose order is the weights'.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -112,12 +114,33 @@ __device__ __forceinline__ int block_scan(int x, int* sums, int& total) {
   return x + (warp > 0 ? below : 0);
 }
 
+// A barrier of the cluster's threads, or of the one CTA's.
+__device__ __forceinline__ void sync_all(int ctas) {
+  if (ctas > 1) {
+    __syncwarp();
+    tc::cluster_sync();
+  } else {
+    __syncthreads();
+  }
+}
+// An int of CTA `rank`'s shared memory, at this CTA's address of it.
+__device__ __forceinline__ int ld_rank(const int* p, int rank, int ctas) {
+  return ctas > 1 ? ld_cluster(tc::smem_u32(p), rank) : *p;
+}
+
+// Units a thread holds in registers from one digit to the next; those of longer
+// sequences are loaded again (from L2).
+constexpr int kHold = 2;
+
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a,
                                                                 const __grid_constant__ Lists l, int ctas) {
   __shared__ int hist[kBins];
+  __shared__ int part[kBins];                              // totals over the cluster, of this CTA's bins
+  __shared__ int part_sum;
   __shared__ int sums[kThreads / 32];
-  __shared__ int found[2];                                 // the digit, and how many of the chosen lie above it
+  __shared__ int found[3];                                 // the digit, the positions in the digits above it, in it
   __shared__ int mine[2];                                  // of this CTA's positions: above the threshold, at it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0, item = blockIdx.x / ctas;
   const int b = item / a.H, h = item - b * a.H;
   const int32_t* row = a.table + (int64_t)b * a.cols;
@@ -127,33 +150,42 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   int bad = 0;
   if (z.m < z.n)
     for (int c = threadIdx.x; c < (z.n + a.page - 1) / a.page; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+  if (threadIdx.x < 2) mine[threadIdx.x] = 0;
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) raise_error(kErrPages);
     z.m = z.n;
   }
   if (h == 0 && rank == 0 && threadIdx.x == 0) l.size[b] = make_int2(z.n, z.m);
   if (z.m >= z.n) return;                                  // the whole cluster
-  int* src = l.src + item * l.positions;
+  int64_t* src = l.src + item * l.positions;
   int* before = l.before + item * l.chunks;
   const int old = z.n - z.r, k = z.m - z.r;                // k of `old` positions stay
-  for (int i = rank * kThreads + threadIdx.x; i < (z.m + kChunk - 1) / kChunk; i += ctas * kThreads) l.read[item * l.chunks + i] = 0;
-  for (int i = rank * kThreads + threadIdx.x; i < z.r; i += ctas * kThreads) src[k + i] = old + i;
+  for (int i = rank * kThreads + threadIdx.x; i < (z.m + l.chunk - 1) / l.chunk; i += ctas * kThreads) l.read[item * l.chunks + i] = 0;
+  for (int i = rank * kThreads + threadIdx.x; i < z.r; i += ctas * kThreads) {
+    const int p = old + i, col = p / a.page;
+    src[k + i] = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (p - col * a.page);
+  }
   const int units = (old + kUnit - 1) / kUnit, each = (units + ctas - 1) / ctas;
   const int u0 = min(rank * each, units), u1 = min(u0 + each, units);
+  uint32_t held[kHold][kUnit];
+  if (k > 0) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int u = u0 + i * kThreads + threadIdx.x;
+      if (u < u1) load_unit(a, row, h, u, held[i]);
+    }
+  }
 
   // the threshold, digit by digit: `prefix` holds the bits found, k_left of the
   // positions that have them are to stay
   uint32_t prefix = 0;
-  int k_left = k, above = 0, at_it = 0;
+  int k_left = k;
   if (k > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
-      __syncthreads();
-      for (int u = u0 + threadIdx.x; u < u1; u += kThreads) {
-        uint32_t key[kUnit];
-        load_unit(a, row, h, u, key);
+      auto count_unit = [&](const uint32_t (&key)[kUnit], int u) {
         const int live = old - u * kUnit;
         // neighbours of one bin are counted together: tokens nobody looked at are alike
         int bin = -1, count = 0;
@@ -167,29 +199,53 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
           count = 1;
         }
         if (count) atomicAdd(hist + bin, count);
+      };
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const int u = u0 + i * kThreads + threadIdx.x;
+        if (u < u1) count_unit(held[i], u);
       }
-      __syncthreads();
-      if (ctas > 1) tc::cluster_sync();
-      // thread t has the bins kBins - 1 - 4t - i: sums from the top
-      constexpr int kOwn = kBins / kThreads;
-      int n[kOwn], sum = 0;
-      const uint32_t hist_at = tc::smem_u32(hist);
+      for (int u = u0 + kHold * kThreads + threadIdx.x; u < u1; u += kThreads) {
+        uint32_t key[kUnit];
+        load_unit(a, row, h, u, key);
+        count_unit(key, u);
+      }
+      sync_all(ctas);
+      const int share = kBins / ctas;
+      int above = 0, owner = 0, sum = 0, total;
+      if (ctas > 1) {
+        // each CTA adds up its share of the bins over the cluster ..
+        for (int i = threadIdx.x; i < share; i += kThreads) {
+          int n = 0;
+          for (int c = 0; c < ctas; ++c) n += ld_rank(hist + rank * share + i, c, ctas);
+          part[i] = n;
+          sum += n;
+        }
+        (void)block_scan(sum, sums, total);
+        if (threadIdx.x == 0) part_sum = total;
+        sync_all(ctas);
+        // .. all find the share that has the digit ..
+        for (owner = ctas - 1; owner > 0; --owner) {
+          const int n = ld_rank(&part_sum, owner, ctas);
+          if (above + n >= k_left) break;
+          above += n;
+        }
+      }
+      // .. and the digit in it, from the top
+      constexpr int kOwn = kBins / kThreads;               // bins of a thread, at most
+      int n[kOwn];
+      sum = 0;
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const int bin = kBins - 1 - ((int)threadIdx.x * kOwn + i);
-        n[i] = 0;
-        if (ctas > 1)
-          for (int c = 0; c < ctas; ++c) n[i] += ld_cluster(hist_at + bin * 4, c);
-        else
-          n[i] = hist[bin];
+        const int bin = share - 1 - ((int)threadIdx.x * kOwn + i);
+        n[i] = bin >= 0 ? (ctas > 1 ? ld_rank(part + bin, owner, ctas) : hist[bin]) : 0;
         sum += n[i];
       }
-      int total;
-      int upto = block_scan(sum, sums, total) - sum;       // positions in the bins above
+      int upto = above + block_scan(sum, sums, total) - sum;   // positions in the bins above
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         if (upto < k_left && upto + n[i] >= k_left) {      // one thread, once
-          found[0] = kBins - 1 - ((int)threadIdx.x * kOwn + i);
+          found[0] = owner * share + share - 1 - ((int)threadIdx.x * kOwn + i);
           found[1] = upto;
         }
         upto += n[i];
@@ -198,34 +254,34 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       const int digit = found[0];
       k_left -= found[1];
       prefix = prefix << bits | (uint32_t)digit;
-      int own = 0;
-      for (int i = threadIdx.x; i < kBins; i += kThreads) own += i > digit ? hist[i] : 0;
-      (void)block_scan(own, sums, total);
-      above += total;
-      at_it = hist[digit];
-      __syncthreads();
-      if (ctas > 1) tc::cluster_sync();                    // no histogram is cleared while another CTA reads it
+      if (ctas > 1) {                                      // of this CTA's: those above, at last those at it
+        int own = 0;
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+          own += i > digit ? hist[i] : 0;
+          if (i == digit && pass == 2) mine[1] = hist[i];
+        }
+        own = __reduce_add_sync(0xffffffffu, own);
+        if ((threadIdx.x & 31) == 0 && own) atomicAdd(mine, own);
+      }
+      if (pass < 2) {                                      // cleared for the next digit
+        for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+        __syncthreads();
+      }
     }
   }
   // positions that stay before this CTA's: those above the threshold and the first k_left at it
   int gt0 = 0, eq0 = 0;
   if (ctas > 1) {
-    if (threadIdx.x == 0) { mine[0] = above; mine[1] = at_it; }
     __syncthreads();
-    tc::cluster_sync();
-    const uint32_t mine_at = tc::smem_u32(mine);
+    sync_all(ctas);
     for (int c = 0; c < rank; ++c) {
-      gt0 += ld_cluster(mine_at, c);
-      eq0 += ld_cluster(mine_at + 4, c);
+      gt0 += ld_rank(mine, c, ctas);
+      eq0 += ld_rank(mine + 1, c, ctas);
     }
-    tc::cluster_sync();                                    // no CTA leaves while another reads its counts
   }
-  for (int t = u0; t < u1; t += kThreads) {
-    const int u = t + threadIdx.x;
-    uint32_t key[kUnit];
+  auto list_units = [&](const uint32_t (&key)[kUnit], int u) {
     uint32_t gt = 0, eq = 0;                               // a bit a position
     if (u < u1 && k > 0) {
-      load_unit(a, row, h, u, key);
       const int live = old - u * kUnit;
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
@@ -238,161 +294,321 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int upto = block_scan(counts, sums, total) - counts;
     int g = gt0 + (upto & 0xffff), e = eq0 + (upto >> 16);
     if (u < u1) {
-      if (u % (kChunk / kUnit) == 0) before[u / (kChunk / kUnit)] = g + min(e, k_left);
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        const bool is_gt = gt >> i & 1, is_eq = eq >> i & 1;
-        if (is_gt || (is_eq && e < k_left)) {
+      if (u * kUnit % l.chunk == 0) before[u * kUnit / l.chunk] = g + min(e, k_left);
+      const int per = a.page / kUnit, col = u / per;
+      const int64_t first = (gt | eq) == 0 ? 0 : ((int64_t)__ldg(row + col) * a.H + h) * a.page + (u - col * per) * kUnit;
+      for (uint32_t left = gt | eq; left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        const bool is_gt = gt >> i & 1;
+        if (is_gt || e < k_left) {
           const int at = g + min(e, k_left);
-          if (in_bounds(at, k)) src[at] = u * kUnit + i;
+          if (in_bounds(at, k)) src[at] = first + i;
         }
         g += is_gt;
-        e += is_eq;
+        e += !is_gt;
       }
     }
     gt0 += total & 0xffff;
     eq0 += total >> 16;
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (u0 + i * kThreads < u1) list_units(held[i], u0 + i * kThreads + threadIdx.x);
+  for (int t = u0 + kHold * kThreads; t < u1; t += kThreads) {
+    uint32_t key[kUnit];
+    const int u = t + threadIdx.x;
+    if (u < u1 && k > 0) load_unit(a, row, h, u, key);
+    list_units(key, u);
   }
+  if (ctas > 1) sync_all(ctas);                            // no CTA leaves while another reads its shared memory
 }
 
-// Moves the rows that stay.  kRowB: bytes of a row's values or codes.
+// Where a chunk's rows are and where they go; -1: a row that does not move.
+template <int kChunk>
+struct Places {
+  int64_t from[kChunk], to[kChunk];
+  int* flags;                                              // the item's; NULL: there is no chunk
+  int c, first, last;                                      // the chunk, and those that have rows in its places
+  int go;                                                  // those have been read
+};
+
+// Of a thread, in a chunk: words of K's and V's rows; weights and row scales; block scales.
+constexpr int own_words(int row_bytes) { return 2 * chunk_of(row_bytes) * (row_bytes / 16) / kMoveThreads; }
+constexpr int own_scalars(int row_bytes, bool scales) { return ((scales ? 3 : 1) * chunk_of(row_bytes) + kMoveThreads - 1) / kMoveThreads; }
+constexpr int own_blocks(int row_bytes, bool four) { return four ? 2 * chunk_of(row_bytes) / kMoveThreads : 0; }
+constexpr int stage_bytes(int row_bytes, bool four, bool scales) {
+  return (own_words(row_bytes) * 16 + own_scalars(row_bytes, scales) * 4 + own_blocks(row_bytes, four) * 8) * kMoveThreads;
+}
+// Chunks on their way through shared memory, two CTAs an SM.
+constexpr int stages_of(int row_bytes, bool four, bool scales) {
+  const int n = 102400 / stage_bytes(row_bytes, four, scales);
+  return n < 6 ? n : 6;
+}
+constexpr int kMovers = kMoveThreads + 96;
+
+// A slot of a ring and the phase of its barriers.
+struct Turn {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == n) { at = 0; phase ^= 1; }
+  }
+};
+
+// Moves the rows that stay.  Eight warps copy a chunk's rows to shared memory,
+// kStages - 1 chunks ahead, and from there to their places.  A ninth warp finds the
+// places of the chunks to come.  A tenth tells the other CTAs that a chunk's rows
+// have been read, as soon as they have arrived, and an eleventh waits for the
+// chunks whose rows lie in this one's places: each on its own, so that no chunk's
+// reading waits for another chunk.  kRowB: bytes of a row's values or codes.
 template <int kRowB, bool kFour, bool kScales>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a,
-                                                                  const __grid_constant__ Lists l) {
+__global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_constant__ EvictArgs a,
+                                                                const __grid_constant__ Lists l) {
+  constexpr int kChunk = chunk_of(kRowB);
   constexpr int kW = kRowB / 16;                           // words of a row
-  constexpr int kOwn = 2 * kChunk * kW / kMoveThreads;     // words of a thread: K's and V's of a chunk
+  constexpr int kOwn = own_words(kRowB), kScalars = own_scalars(kRowB, kScales), kBlocks = own_blocks(kRowB, kFour);
+  constexpr int kStages = stages_of(kRowB, kFour, kScales), kStageB = stage_bytes(kRowB, kFour, kScales);
+  constexpr int kRing = kStages + 2;                       // chunks whose places are known
   constexpr int D = kRowB * 2;                             // kFour
-  static_assert(kOwn >= 1, "");
-  extern __shared__ int prefix[];                          // chunks of the sequences before, of one head
-  __shared__ int64_t from[kChunk], to[kChunk];
-  __shared__ int from_slot[kChunk], to_slot[kChunk];
-  __shared__ int next_chunk, go;
+  static_assert(kOwn >= 1 && kStages >= 2, "");
+  using Place = Places<kChunk>;
+  extern __shared__ __align__(16) char stages[];           // kStages, for the rows on their way
+  int2* const size = reinterpret_cast<int2*>(stages + kStages * kStageB);   // [B], and chunks of the sequences before, of one head
+  int* const prefix = reinterpret_cast<int*>(size + a.B);
+  __shared__ Place places[kRing];
+  __shared__ __align__(8) uint64_t placed[kRing], read[kRing], free_[kRing], done[kRing];
+  __shared__ int stop;                                     // a wait gave up: all leave
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(placed + i, 1);                        // its places are known
+      tc::mbar_init(read + i, kMoveThreads);               // its rows have arrived
+      tc::mbar_init(free_ + i, 1);                         // those of others in its places too
+      tc::mbar_init(done + i, kMoveThreads / 32 + 2);      // nobody looks at its places any more
+    }
+    stop = 0;
+    tc::fence_barrier_init();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // each warp adds up a part of the sequences' chunks
-  for (int b = threadIdx.x; b < a.B; b += kMoveThreads) {
+  for (int b = threadIdx.x; b < a.B; b += kMovers) {
     const int2 z = l.size[b];
-    prefix[b + 1] = z.y < z.x ? (z.y + kChunk - 1) / kChunk : 0;
+    size[b] = z;
     if (blockIdx.x == 0) a.out[b] = z.y;
   }
-  if (threadIdx.x == 0) {
-    prefix[0] = 0;
-    next_chunk = atomicAdd(l.ticket, 1);
-  }
   __syncthreads();
-  if (threadIdx.x < 32) {
+
+  if (warp < kMoveThreads / 32) {                          // ---- the rows
+    // a thread copies its words of a chunk to places of its own in a stage, and from there; words, weights and row
+    // scales, block scales are numbered through the chunk, K's before V's
+    const auto scalar = [&](int i) { return i < kChunk ? a.w : (kScales && i < 3 * kChunk ? (i < 2 * kChunk ? a.ks : a.vs) : nullptr); };
+    const auto slot_of = [&](int64_t row) {                // of its page
+      const unsigned unit = (unsigned)(row / kUnit);
+      return (int)(unit % (unsigned)(a.page / kUnit)) * kUnit + (int)(row % kUnit);
+    };
+    const auto word_at = [&](int i, int64_t row) {
+      char* base = static_cast<char*>(i >= kChunk * kW ? a.vc : a.kc);
+      return base + (kFour ? e2m1_codes(row, slot_of(row), D) : row * kRowB) + i % kW * 16;
+    };
+    const auto block_at = [&](int i, int64_t row) {
+      return static_cast<char*>(i >= kChunk ? a.vc : a.kc) + e2m1_blocks(row, slot_of(row), a.page, D);
+    };
+    constexpr int kAtScalars = kOwn * kMoveThreads * 16, kAtBlocks = kAtScalars + kScalars * kMoveThreads * 4;
+    const auto load = [&](const Place& p, int stage, uint64_t* arrived) {
+      const uint32_t to = tc::smem_u32(stages + stage * kStageB);
+#pragma unroll
+      for (int x = 0; x < kOwn; ++x) {
+        const int i = x * kMoveThreads + threadIdx.x;
+        const int64_t from = p.from[i / kW % kChunk];
+        if (from >= 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + i * 16), "l"(word_at(i, from)) : "memory");
+      }
+#pragma unroll
+      for (int x = 0; x < kScalars; ++x) {
+        const int i = x * kMoveThreads + threadIdx.x;
+        const int64_t from = p.from[i % kChunk];
+        if (scalar(i) && from >= 0)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(to + kAtScalars + i * 4), "l"(scalar(i) + from) : "memory");
+      }
+#pragma unroll
+      for (int x = 0; x < kBlocks; ++x) {
+        const int i = x * kMoveThreads + threadIdx.x;
+        const int64_t from = p.from[i % kChunk];
+        if (from >= 0)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(to + kAtBlocks + i * 8), "l"(block_at(i, from)), "n"(D == 128 ? 8 : 4) : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(tc::smem_u32(arrived)) : "memory");
+    };
+    Turn ahead, now;
+    int to_stage = 0, stage = 0, more = 1;                 // more: of the chunk that is loaded next
+    const auto load_next = [&]() {
+      if (!more) return true;
+      if (!tc::mbar_wait(placed + ahead.at, ahead.phase, &stop)) return false;
+      more = places[ahead.at].flags != nullptr;
+      if (more) load(places[ahead.at], to_stage, read + ahead.at);
+      ahead.next(kRing);
+      to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
+      return true;
+    };
+    bool ok = true;
+    for (int i = 0; i < kStages - 1; ++i) ok = ok && load_next();
+    while (ok) {
+      const Place& p = places[now.at];
+      if (!p.flags) break;
+      ok = load_next() && tc::mbar_wait(read + now.at, now.phase, &stop) && tc::mbar_wait(free_ + now.at, now.phase, &stop);
+      if (ok && p.go) {
+        const char* from = stages + stage * kStageB;
+#pragma unroll
+        for (int x = 0; x < kOwn; ++x) {
+          const int i = x * kMoveThreads + threadIdx.x;
+          const int64_t to = p.to[i / kW % kChunk];
+          if (to >= 0) st16(word_at(i, to), *reinterpret_cast<const uint4*>(from + i * 16));
+        }
+#pragma unroll
+        for (int x = 0; x < kScalars; ++x) {
+          const int i = x * kMoveThreads + threadIdx.x;
+          const int64_t to = p.to[i % kChunk];
+          if (scalar(i) && to >= 0) scalar(i)[to] = *reinterpret_cast<const float*>(from + kAtScalars + i * 4);
+        }
+#pragma unroll
+        for (int x = 0; x < kBlocks; ++x) {
+          const int i = x * kMoveThreads + threadIdx.x;
+          const int64_t to = p.to[i % kChunk];
+          if (to >= 0) {
+            const uint32_t* b = reinterpret_cast<const uint32_t*>(from + kAtBlocks + i * 8);
+            uint32_t* q = reinterpret_cast<uint32_t*>(block_at(i, to));
+            q[0] = b[0];
+            if (D == 128) q[1] = b[1];
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(done + now.at);
+      now.next(kRing);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  if (warp == kMoveThreads / 32 + 1) {                     // ---- the tenth warp
+    if (lane != 0) return;
+    for (Turn now; tc::mbar_wait(placed + now.at, now.phase, &stop); now.next(kRing)) {
+      int* const flags = places[now.at].flags;
+      const int c = places[now.at].c;
+      if (!flags || !tc::mbar_wait(read + now.at, now.phase, &stop)) return;
+      // no fence: the copies have arrived, so no later write can reach them, and one would wait for the stores of
+      // the chunks before
+      asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" :: "l"(flags + c), "r"(1) : "memory");
+      tc::mbar_arrive(done + now.at);
+    }
+    return;
+  }
+  if (warp == kMoveThreads / 32 + 2) {                     // ---- the eleventh
+    if (lane != 0) return;
+    for (Turn now; tc::mbar_wait(placed + now.at, now.phase, &stop); now.next(kRing)) {
+      Place& p = places[now.at];
+      if (!p.flags) return;
+      // at most two, and chunks before this one: their reading waits for nothing
+      int ok = 1;
+      uint64_t begin = 0;
+      for (int x = p.first; x <= p.last && x < p.c && ok; ++x) {
+        while (true) {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(ok) : "l"(p.flags + x) : "memory");
+          if (ok) break;
+          const uint64_t t = global_timer_ns();
+          if (begin == 0) begin = t;
+          if (t - begin > kWaitLimitNs) break;
+        }
+      }
+      if (!ok) raise_error(kErrTimeout);
+      p.go = ok;
+      tc::mbar_arrive(free_ + now.at);
+      tc::mbar_arrive(done + now.at);
+    }
+    return;
+  }
+  // ---- the ninth
+  {
     int carry = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + threadIdx.x;
-      int x = b < a.B ? prefix[b + 1] : 0;
+      const int b = b0 + lane;
+      const int chunks = b < a.B && size[b].y < size[b].x ? (size[b].y + kChunk - 1) / kChunk : 0;
+      int x = chunks;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((int)threadIdx.x >= o) x += y;
+        if (lane >= o) x += y;
       }
-      if (b < a.B) prefix[b + 1] = carry + x;
+      if (b < a.B) prefix[b] = carry + x - chunks;
       carry += __shfl_sync(0xffffffffu, x, 31);
     }
+    if (lane == 0) prefix[a.B] = carry;
+    __syncwarp();
   }
-  __syncthreads();
+  constexpr int kMine = (kChunk + 31) / 32;                // rows of a lane
   const int64_t total = (int64_t)prefix[a.B] * a.H, rows = a.num_pages * a.H * a.page;
-  while (true) {
-    const int t = next_chunk;
-    __syncthreads();                                       // all have it, and the last chunk's places are done with
-    if (t >= total) return;
-    if (threadIdx.x == 0) next_chunk = atomicAdd(l.ticket, 1);
-    int lo = 0, hi = a.B - 1;                              // the last b with prefix[b] * H <= t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)prefix[mid] * a.H <= t) lo = mid; else hi = mid - 1;
-    }
-    const int b = lo, chunks = prefix[b + 1] - prefix[b], in_seq = t - prefix[b] * a.H;
-    const int h = in_seq / chunks, c = in_seq - h * chunks;
-    const int64_t item = (int64_t)b * a.H + h;
-    const int2 z = l.size[b];
-    const int r0 = c * kChunk, n = min(kChunk, z.y - r0);
-    const int* src = l.src + item * l.positions;
-    int* read = l.read + item * l.chunks;
-    if (__ldg(src + r0 + n - 1) == r0 + n - 1) {           // positions rise and none lies below its rank: none moves
-      if (threadIdx.x == 0) asm volatile("st.release.gpu.global.s32 [%0], %1;" :: "l"(read + c), "r"(1) : "memory");
-      __syncthreads();                                     // the next chunk's number is there
-      continue;
-    }
-    // threads 0-63 find where the rows are, 64-127 where they go
-    if ((int)threadIdx.x < 2 * kChunk) {
-      const int i = threadIdx.x % kChunk, side = threadIdx.x / kChunk;
-      int64_t place = -1;
-      int slot = 0;
-      if (i < n) {
-        const int s = __ldg(src + r0 + i), p = side ? r0 + i : s;
-        const int col = p / a.page;
-        slot = p - col * a.page;
-        place = ((int64_t)__ldg(a.table + (int64_t)b * a.cols + col) * a.H + h) * a.page + slot;
-        if (s == r0 + i || !in_bounds(place, rows)) place = -1;
-      }
-      (side ? to : from)[i] = place;
-      (side ? to_slot : from_slot)[i] = slot;
-    }
-    __syncthreads();
-    // K's words and then V's; word i of the chunk is word i % kW of row i / kW
-    uint4 w[kOwn];
-#pragma unroll
-    for (int x = 0; x < kOwn; ++x) {
-      const int i = x * kMoveThreads + threadIdx.x, k = i / kW % kChunk;
-      const char* base = static_cast<const char*>(i >= kChunk * kW ? a.vc : a.kc);
-      if (from[k] >= 0 && to[k] >= 0)
-        w[x] = ld16(base + (kFour ? e2m1_codes(from[k], from_slot[k], D) : from[k] * kRowB) + i % kW * 16);
-    }
-    float f[3];
-    uint32_t blocks[2];
-    const int k = threadIdx.x % kChunk, which = threadIdx.x / kChunk;   // threads 0-63 weights, 64-127 K's scales, 128-191 V's
-    const bool moves = from[k] >= 0 && to[k] >= 0;
-    float* const scalars = which == 0 ? a.w : (kScales ? (which == 1 ? a.ks : (which == 2 ? a.vs : nullptr)) : nullptr);
-    if (moves && scalars) f[0] = *reinterpret_cast<const volatile float*>(scalars + from[k]);
-    if (kFour && moves && which < 2) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const char*>(which ? a.vc : a.kc) +
-                                                            e2m1_blocks(from[k], from_slot[k], a.page, D));
-      blocks[0] = ld4(p);
-      if (D == 128) blocks[1] = ld4(p + 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      asm volatile("st.release.gpu.global.s32 [%0], %1;" :: "l"(read + c), "r"(1) : "memory");
-      // ranks of the rows that lie in the chunk's places
-      const int old = z.x - min(z.y, a.recent), k0 = z.y - min(z.y, a.recent);
-      const int* before = l.before + item * l.chunks;
-      const int first = r0 < old ? __ldg(before + c) : k0 + r0 - old;
-      const int end = min(r0 + kChunk, z.x);
-      const int last = (end < old ? __ldg(before + c + 1) : k0 + end - old) - 1;
-      int ok = 1;
-      for (int x = first / kChunk; x <= last / kChunk && x < c; ++x) {
-        int v;
-        uint64_t begin = 0;
-        while (true) {
-          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(read + x) : "memory");
-          if (v) break;
-          const uint64_t now = global_timer_ns();
-          if (begin == 0) begin = now;
-          if (now - begin > kWaitLimitNs) break;
+  int ticket = 0;                                          // lane 0's: the next chunk
+  if (lane == 0) ticket = atomicAdd(l.ticket, 1);
+  int round = 0;
+#pragma unroll 1
+  for (Turn now;; now.next(kRing), ++round) {
+    if (round >= kRing && !tc::mbar_wait_warp(done + now.at, now.phase ^ 1, &stop)) return;
+    Place& p = places[now.at];
+    while (true) {
+      const int t = __shfl_sync(0xffffffffu, ticket, 0);
+      if (t >= total) {
+        __syncwarp();
+        if (lane == 0) {
+          p.flags = nullptr;
+          tc::mbar_arrive(placed + now.at);
         }
-        ok &= v;
+        return;
       }
-      if (!ok) raise_error(kErrTimeout);
-      go = ok;
-    }
-    __syncthreads();
-    if (!go) continue;
+      if (lane == 0) ticket = atomicAdd(l.ticket, 1);
+      int lo = 0, hi = a.B - 1;                            // the last b with prefix[b] * H <= t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)prefix[mid] * a.H <= t) lo = mid; else hi = mid - 1;
+      }
+      const int b = lo, chunks = prefix[b + 1] - prefix[b], in_seq = t - prefix[b] * a.H;
+      const int h = in_seq / chunks, c = in_seq - h * chunks;
+      const int64_t item = (int64_t)b * a.H + h;
+      const int2 z = size[b];
+      const int r0 = c * kChunk, n = min(kChunk, z.y - r0);
+      const int64_t* src = l.src + item * l.positions + r0;
+      const int32_t* row = a.table + (int64_t)b * a.cols;
+      const int* before = l.before + item * l.chunks + c;
+      int64_t from[kMine], to[kMine];
 #pragma unroll
-    for (int x = 0; x < kOwn; ++x) {
-      const int i = x * kMoveThreads + threadIdx.x, k = i / kW % kChunk;
-      char* base = static_cast<char*>(i >= kChunk * kW ? a.vc : a.kc);
-      if (from[k] >= 0 && to[k] >= 0)
-        st16(base + (kFour ? e2m1_codes(to[k], to_slot[k], D) : to[k] * kRowB) + i % kW * 16, w[x]);
-    }
-    if (moves && scalars) scalars[to[k]] = f[0];
-    if (kFour && moves && which < 2) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<char*>(which ? a.vc : a.kc) + e2m1_blocks(to[k], to_slot[k], a.page, D));
-      p[0] = blocks[0];
-      if (D == 128) p[1] = blocks[1];
+      for (int x = 0; x < kMine; ++x) {
+        const int i = min(lane + 32 * x, n - 1), col = (r0 + i) / a.page;
+        from[x] = __ldg(src + i);
+        to[x] = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (r0 + i - col * a.page);
+      }
+      // ranks of the rows that lie in the chunk's places
+      const int r = min(z.y, a.recent), old = z.x - r, k0 = z.y - r, end = min(r0 + kChunk, z.x);
+      const int first = r0 < old ? __ldg(before) : k0 + r0 - old, last = (end < old ? __ldg(before + 1) : k0 + end - old) - 1;
+      // positions rise and none lies below its rank: if the last stays where it is, all do
+      if (__shfl_sync(0xffffffffu, from[kMine - 1] == to[kMine - 1], 31)) {
+        if (lane == 0) asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" :: "l"(l.read + item * l.chunks + c), "r"(1) : "memory");
+        continue;
+      }
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        const int i = lane + 32 * x;
+        const bool moves = i < n && from[x] != to[x] && in_bounds(from[x], rows) && in_bounds(to[x], rows);
+        if (i < kChunk) {
+          p.from[i] = moves ? from[x] : -1;
+          p.to[i] = moves ? to[x] : -1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+        p.flags = l.read + item * l.chunks;
+        p.c = c;
+        p.first = first / kChunk;
+        p.last = last / kChunk;
+        tc::mbar_arrive(placed + now.at);
+      }
+      break;
     }
   }
 }
@@ -404,20 +620,20 @@ WsLayout ws_layout(const EvictArgs& a) {
   WsLayout w{};
   const int64_t b = a.B < kMaxBatch ? a.B : kMaxBatch, items = b * a.H;
   w.positions = (int64_t)a.cols * a.page;
-  w.chunks = w.positions / kChunk + 2;
+  w.chunks = w.positions / 32 + 2;               // of the smallest chunk
   w.ticket = align256((size_t)b * sizeof(int2));
   w.before = w.ticket + 256;
   w.read = w.before + align256((size_t)(items * w.chunks) * 4);
   w.src = w.read + align256((size_t)(items * w.chunks) * 4);
-  w.total = w.src + align256((size_t)(items * w.positions) * 4);
+  w.total = w.src + align256((size_t)(items * w.positions) * 8);
   return w;
 }
 
-// CTAs of a cluster for each (sequence, kv head): as many as two an SM allow, and no
-// more than there are positions for.
+// CTAs of a cluster for each (sequence, kv head): a unit a thread where two CTAs an
+// SM allow it.
 int cluster_of(const EvictArgs& a) {
-  int c = 8;
-  while (c > 1 && ((int64_t)a.B * a.H * c > 152 * 2 || (int64_t)a.cols * a.page < (int64_t)c * kThreads * 4)) c /= 2;
+  int c = 1;
+  while (c < 8 && (int64_t)a.cols * a.page > (int64_t)c * kThreads * kUnit && (int64_t)a.B * a.H * c * 2 <= 152 * 2) c *= 2;
   return c;
 }
 
@@ -428,13 +644,18 @@ int launch_failed(const char* what, cudaError_t err) {
 
 template <int kRowB, bool kFour, bool kScales>
 cudaError_t move(const EvictArgs& a, const Lists& l, cudaStream_t st) {
+  constexpr int kStages = stages_of(kRowB, kFour, kScales) * stage_bytes(kRowB, kFour, kScales);
+  static PerDeviceOnce<> once;
+  if (opt_in_smem(once, (const void*)evict_move_kernel<kRowB, kFour, kScales>,
+                  kStages + kMaxBatch * (int)(sizeof(int2) + sizeof(int)) + 4, "cache_evict"))
+    return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sms * 6));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = (a.B + 1) * sizeof(int);
+  cfg.gridDim = dim3((unsigned)(sms * 2));
+  cfg.blockDim = dim3(kMovers);
+  cfg.dynamicSmemBytes = kStages + a.B * sizeof(int2) + (a.B + 1) * sizeof(int);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -461,8 +682,9 @@ size_t evict_workspace(const EvictArgs& a) { return a.B == 0 ? 0 : ws_layout(a).
 int launch_evict(const EvictArgs& a, cudaStream_t st) {
   const WsLayout w = ws_layout(a);
   char* ws = (char*)a.ws;
-  const Lists l{(int2*)(ws + w.size), (int*)(ws + w.ticket), (int*)(ws + w.src), (int*)(ws + w.before), (int*)(ws + w.read),
-                w.positions, w.chunks};
+  const int row_bytes = a.cache_dtype == ULYSSES_E2M1 ? a.D / 2 : (a.cache_dtype == ULYSSES_E4M3 ? a.D : elt_size(a.cache_dtype) * a.D);
+  const Lists l{(int2*)(ws + w.size), (int*)(ws + w.ticket), (int64_t*)(ws + w.src), (int*)(ws + w.before), (int*)(ws + w.read),
+                w.positions, w.chunks, chunk_of(row_bytes)};
   for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
     EvictArgs x = a;
     x.B = a.B - b0 < kMaxBatch ? a.B - b0 : kMaxBatch;

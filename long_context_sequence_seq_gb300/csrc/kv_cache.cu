@@ -80,27 +80,6 @@ __device__ __forceinline__ void check_cu(const CacheArgs& a) {
   }
 }
 
-// x / y to nearest, given 1 / y to nearest (a quotient's residual is exact in an
-// FMA, and one step with it rounds correctly: Markstein 1990).  Codes next to a
-// border are then those of the definition, in 64 bits too.
-__device__ __forceinline__ float divided(float x, float y, float inv_y) {
-  const float q = x * inv_y;
-  return fmaf(fmaf(-q, y, x), inv_y, q);
-}
-
-// The codes of a word of a 4-bit row, whose block scale is b (0: all of it is
-// below half of the smallest scale).  up: the inverse of the row's scale, a power
-// of two.
-template <typename T>
-__device__ __forceinline__ uint32_t to_e2m1(const Row8<T>& w, float up, float b) {
-  const float r = 1.0f / b;
-  float f[8];
-  w.get(f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = b > 0.f ? divided(f[i] * up, b, r) : 0.f;
-  return f32_to_e2m1x8(f);
-}
-
 // The rows of a CTA's tokens x heads, K's and then V's, in an order in which
 // rows that lie together in the tokens' tensor are neighbours: heads of one
 // token where those are closer, else tokens of one head.
@@ -112,15 +91,11 @@ constexpr int rows_in_work() { return kWrite ? (sizeof(T) == 2 ? 4 : 2) : (kHeld
 template <typename T, Held kHeld>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, int tb) {
   __shared__ int64_t place[kMaxTokens];
-  __shared__ int slots[kMaxTokens];
   const int64_t t0 = (int64_t)blockIdx.x * tb;
   const int tokens = (int)(a.T - t0 < tb ? a.T - t0 : tb);
   check_cu(a);
-  if ((int)threadIdx.x < tokens) {
-    int slot = 0;
-    place[threadIdx.x] = place_of(a, t0 + threadIdx.x, true, slot);
-    slots[threadIdx.x] = slot;
-  }
+  int slot;
+  if ((int)threadIdx.x < tokens) place[threadIdx.x] = place_of(a, t0 + threadIdx.x, true, slot);
   __syncthreads();
   constexpr int kRows = rows_in_work<T, kHeld, true>();
   const int lanes = a.D / 16, lane = threadIdx.x % lanes, e0 = lane * 8, e1 = (lane + lanes) * 8;
@@ -131,12 +106,10 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   for (int left = 2 * no * ni; left > 0; left -= kRows * (kThreads / lanes)) {
     Row8<T> w[kRows][2];
     int64_t row[kRows];
-    int slot[kRows];
     bool second[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       row[u] = -1;
-      slot[u] = 0;
       w[u][0].zero();
       w[u][1].zero();
       second[u] = walk.o >= no;
@@ -146,7 +119,6 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         const int64_t at = place[t];
         if (at >= 0 && in_bounds(at + (int64_t)h * a.page, a.num_pages * a.H * a.page)) {
           row[u] = at + (int64_t)h * a.page;
-          if (kHeld == kE2m1) slot[u] = slots[t];
           if (a.w && lane == 0 && !second[u]) a.w[row[u]] = 0.f;
           const int64_t off = second[u] ? (t0 + t) * a.v_s + h * a.v_h : (t0 + t) * a.k_s + h * a.k_h;
           const T* src = reinterpret_cast<const T*>(second[u] ? a.v : a.k) + off;
@@ -168,49 +140,19 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     }
     // the rows' largest magnitudes; lane u of a row's lanes keeps row u's
     float mine = 0.f;
-    float block[kRows][2];                       // 4 bits: largest magnitudes of the words' blocks
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      float a0 = w[u][0].amax(), a1 = w[u][1].amax();
-      if (kHeld == kE2m1) {                      // a block is the words of a pair of lanes
-        block[u][0] = a0 = max_nan(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-        block[u][1] = a1 = max_nan(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-      }
-      float amax = max_nan(a0, a1);
-      for (int o = lanes / 2; o > (kHeld == kE2m1 ? 1 : 0); o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float amax = max_nan(w[u][0].amax(), w[u][1].amax());
+      for (int o = lanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       mine = lane % kRows == u ? amax : mine;
     }
     // so one pair of divisions serves kRows rows
     mine = max_nan(mine, 7.888609052210118e-31f);   // 2^-100
-    float inv = 448.0f / mine, scale = mine / 448.0f;
-    if (kHeld == kE2m1) {
-      // 2688 is 1.3125 * 2^11: the exponent that takes mine to (1344, 2688]
-      const uint32_t e = (__float_as_uint(mine) + 0x57ffffu >> 23) - 11;
-      scale = __uint_as_float(e << 23);
-      inv = __uint_as_float((254 - e) << 23);
-    }
-    if (!(mine <= 3.4028234663852886e38f)) scale = __int_as_float(0x7fc00000);
+    const float inv = 448.0f / mine;
+    const float scale = mine <= 3.4028234663852886e38f ? mine / 448.0f : __int_as_float(0x7fc00000);
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const float by = __shfl_sync(0xffffffffu, inv, u, lanes);
-      if (kHeld == kE2m1) {
-        const uint16_t b2 = f32_to_e4m3x2(divided(block[u][0] * by, 6.0f, 1.0f / 6.0f), divided(block[u][1] * by, 6.0f, 1.0f / 6.0f));
-        const uint32_t bh = e4m3x2_to_f16x2(b2);
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&bh));
-        const uint32_t c0 = to_e2m1(w[u][0], by, b.x), c1 = to_e2m1(w[u][1], by, b.y);
-        if (row[u] < 0) continue;
-        uint8_t* base = reinterpret_cast<uint8_t*>(second[u] ? a.vc : a.kc);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(base + e2m1_codes(row[u], slot[u], a.D));
-        dst[lane] = c0;
-        dst[lane + lanes] = c1;
-        if ((lane & 1) == 0) {
-          uint8_t* bs = base + e2m1_blocks(row[u], slot[u], a.page, a.D) + lane / 2;
-          bs[0] = (uint8_t)b2;
-          bs[lanes / 2] = (uint8_t)(b2 >> 8);
-        }
-        if (lane == u) (second[u] ? a.vs : a.ks)[row[u]] = scale;
-        continue;
-      }
       const uint2 c0 = w[u][0].codes(by), c1 = w[u][1].codes(by);
       if (row[u] < 0) continue;
       uint8_t* dst = reinterpret_cast<uint8_t*>(second[u] ? a.vc : a.kc) + row[u] * a.D;
@@ -221,18 +163,276 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
   }
 }
 
-template <typename T, Held kHeld>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, int tb) {
-  __shared__ int64_t place[kMaxTokens];
-  __shared__ int slots[kMaxTokens];
+// ------------------------------------------------------------------ 4-bit rows
+
+// Two floats at once.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c; }"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c; }"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+// the larger magnitudes, NaN if either is (signs mean nothing)
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// A block of a row, 16 elements: a lane's part.  Loads that L1 may keep: each of a
+// lane's 16-byte words is half of what a sector has.
+//
+// A quotient next to a border between two codes has to fall on its side in 64 bits
+// too, and one on it exactly on it: ties go to the even code.
+template <typename T> struct Block;
+template <> struct Block<__nv_bfloat16> {
+  uint4 w[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    w[0] = *reinterpret_cast<const uint4*>(p);
+    w[1] = *reinterpret_cast<const uint4*>(p + 8);
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float amax() const {
+    uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0].x, w[0].y), max_abs_bf16x2(w[0].z, w[0].w));
+    m = max_abs_bf16x2(m, max_abs_bf16x2(max_abs_bf16x2(w[1].x, w[1].y), max_abs_bf16x2(w[1].z, w[1].w)));
+    return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xffff0000u)));
+  }
+  // Elements over b * the row's scale, whose inverse to nearest is r.  A border m
+  // times b has 7 bits and an element 8, so a quotient that is not m is 2^-8 of it
+  // away, 2^-10 at least; rounded to multiples of 2^-12 (what a sum with 2560 does,
+  // the product being exact in it), those on a border are back on it.
+  __device__ __forceinline__ void over(float, float r, float (&f)[16]) const {
+    const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 q = add2(fma2(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)),
+                                 make_float2(r, r), make_float2(2560.f, 2560.f)), make_float2(-2560.f, -2560.f));
+      f[2 * i] = q.x;
+      f[2 * i + 1] = q.y;
+    }
+  }
+};
+template <> struct Block<float> {
+  float4 w[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + 4 * i);
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float amax() const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max_nan(max_nan(max_nan(m, fabsf(w[i].x)), max_nan(fabsf(w[i].y), fabsf(w[i].z))), fabsf(w[i].w));
+    return m;
+  }
+  // Rounded to nearest: a quotient's residual is exact in an FMA, and one step with
+  // it rounds correctly (Markstein 1990).
+  __device__ __forceinline__ void over(float minus_b, float r, float (&f)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = w[i / 2];
+      const float2 x = i % 2 ? make_float2(v.z, v.w) : make_float2(v.x, v.y), q = mul2(x, make_float2(r, r));
+      const float2 y = fma2(fma2(q, make_float2(minus_b, minus_b), x), make_float2(r, r), q);
+      f[2 * i] = y.x;
+      f[2 * i + 1] = y.y;
+    }
+  }
+};
+// The same for one quotient, given -y and 1 / y to nearest.
+__device__ __forceinline__ float divided(float x, float minus_y, float inv_y) {
+  const float q = x * inv_y;
+  return fmaf(fmaf(q, minus_y, x), inv_y, q);
+}
+
+// Where a CTA's tokens are in a 4-bit cache, for the first head: row (-1: nothing to
+// do), and offsets of the codes and of the block scales.  Every head is
+// page * 9 D / 16 bytes, and `page` rows, further.
+struct Places4 {
+  int64_t row[kMaxTokens], codes[kMaxTokens], blocks[kMaxTokens];
+  __device__ __forceinline__ void find(const CacheArgs& a, int64_t t0, int tokens, bool write) {
+    if ((int)threadIdx.x < tokens) {
+      int slot = 0;
+      const int64_t at = place_of(a, t0 + threadIdx.x, write, slot);
+      row[threadIdx.x] = at;
+      codes[threadIdx.x] = e2m1_codes(at, slot, a.D);
+      blocks[threadIdx.x] = e2m1_blocks(at, slot, a.page, a.D);
+    }
+  }
+};
+
+// Rows to 4 bits.  A lane has a block of a row (D / 16 lanes a row), so its scale
+// is the lane's own, and the row's a 2- or 3-step shuffle away.  Instruction issue
+// is next to HBM again: quotients are formed two at a time, the inverse of a block
+// scale comes from a table of the 127 there are, the row's scale by its bits, and
+// places from offsets found once a token.  A code of magnitude 0 may have either sign.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) cache_write_4bit_kernel(const __grid_constant__ CacheArgs a, int tb) {
+  __shared__ Places4 place;
+  __shared__ float inverse[128];                           // of e4m3 values; of 0: 0
   const int64_t t0 = (int64_t)blockIdx.x * tb;
   const int tokens = (int)(a.T - t0 < tb ? a.T - t0 : tb);
   check_cu(a);
-  if ((int)threadIdx.x < tokens) {
-    int slot = 0;
-    place[threadIdx.x] = place_of(a, t0 + threadIdx.x, false, slot);
-    slots[threadIdx.x] = slot;
+  place.find(a, t0, tokens, true);
+  if (threadIdx.x < 128) {
+    const uint32_t h = e4m3x2_to_f16x2((uint16_t)threadIdx.x);
+    const float b = __half2float(__ushort_as_half((unsigned short)h));
+    inverse[threadIdx.x] = b > 0.f ? 1.0f / b : 0.f;
   }
+  __syncthreads();
+  constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+  const int lanes = a.D / 16, lane = threadIdx.x % lanes;
+  const bool heads_fast = a.k_h <= a.k_s;
+  const int ni = heads_fast ? a.H : tokens, no = heads_fast ? tokens : a.H;
+  const int head_rows = a.page, head_bytes = a.page * (a.D / 16) * 9;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {                   // K's rows, then V's
+    const int64_t step_t = side ? a.v_s : a.k_s, step_h = side ? a.v_h : a.k_h;
+    const T* const from = reinterpret_cast<const T*>(side ? a.v : a.k) + t0 * step_t + lane * 16;
+    uint8_t* const to = reinterpret_cast<uint8_t*>(side ? a.vc : a.kc);
+    float* const scales = side ? a.vs : a.ks;
+    RowWalk walk(threadIdx.x / lanes, kThreads / lanes, ni);
+    // every lane of a warp runs the same number of rounds: the row maximum is a shuffle
+    for (int left = no * ni; left > 0; left -= kRows * (kThreads / lanes)) {
+      Block<T> w[kRows];
+      int t[kRows], h[kRows];                              // t -1: no row
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        t[u] = -1;
+        h[u] = 0;
+        if (walk.o < no) {
+          h[u] = heads_fast ? walk.i : walk.o;
+          const int token = heads_fast ? walk.o : walk.i;
+          const int64_t at = place.row[token];
+          if (at >= 0 && in_bounds(at + (int64_t)h[u] * head_rows, a.num_pages * a.H * a.page)) {
+            t[u] = token;
+            w[u].load(from + token * step_t + h[u] * step_h);
+          }
+        }
+        if (t[u] < 0) w[u].zero();
+        walk.next();
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const float block = w[u].amax();
+        float amax = block;
+        for (int o = lanes / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (t[u] < 0) continue;
+        // 2688 is 1.3125 * 2^11: the exponent e that takes the maximum to (1344, 2688] times 2^e
+        amax = max_nan(amax, 7.888609052210118e-31f);      // 2^-100
+        const uint32_t e = (__float_as_uint(amax) + 0x57ffffu >> 23) - 11;
+        const float down = __uint_as_float((254 - e) << 23);
+        const uint16_t code = f32_to_e4m3x2(divided(block * down, -6.0f, 1.0f / 6.0f), 0.f);
+        const uint32_t bh = e4m3x2_to_f16x2(code);
+        // (b = 0: all of the block is below half of the smallest scale)
+        const float b = -__half2float(__ushort_as_half((unsigned short)bh)), up = __uint_as_float(e << 23);
+        float f[16];
+        w[u].over(b * up, inverse[code & 127] * down, f);
+        const int64_t head = (int64_t)h[u] * head_bytes;
+        st8(to + place.codes[t[u]] + head + lane * 8, b < 0.f ? make_uint2(f32_to_e2m1x8(f), f32_to_e2m1x8(f + 8)) : make_uint2(0, 0));
+        to[place.blocks[t[u]] + head + lane] = (uint8_t)code;
+        if (lane == 0) {
+          const int64_t row = place.row[t[u]] + (int64_t)h[u] * head_rows;
+          scales[row] = amax <= 3.4028234663852886e38f ? up : __int_as_float(0x7fc00000);
+          if (a.w && side == 0) a.w[row] = 0.f;
+        }
+      }
+    }
+  }
+}
+
+// Rows from 4 bits: code * block scale exactly in f16, and the row's in fp32.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cache_read_4bit_kernel(const __grid_constant__ CacheArgs a, int tb) {
+  __shared__ Places4 place;
+  const int64_t t0 = (int64_t)blockIdx.x * tb;
+  const int tokens = (int)(a.T - t0 < tb ? a.T - t0 : tb);
+  check_cu(a);
+  place.find(a, t0, tokens, false);
+  __syncthreads();
+  constexpr int kRows = 4;
+  const int lanes = a.D / 16, lane = threadIdx.x % lanes;  // a lane has words lane and lane + D / 16, of 8 elements
+  const bool heads_fast = a.k_h <= a.k_s;
+  const int ni = heads_fast ? a.H : tokens, no = heads_fast ? tokens : a.H;
+  const int head_rows = a.page, head_bytes = a.page * (a.D / 16) * 9;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int64_t step_t = side ? a.v_s : a.k_s, step_h = side ? a.v_h : a.k_h;
+    T* const to = reinterpret_cast<T*>(side ? a.v : a.k) + t0 * step_t + lane * 8;
+    const uint8_t* const from = reinterpret_cast<const uint8_t*>(side ? a.vc : a.kc);
+    const float* const scales = side ? a.vs : a.ks;
+    RowWalk walk(threadIdx.x / lanes, kThreads / lanes, ni);
+    while (walk.o < no) {
+      uint32_t codes[kRows][2], blocks[kRows][2];
+      float scale[kRows];
+      T* dst[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        dst[u] = nullptr;
+        if (walk.o < no) {
+          const int h = heads_fast ? walk.i : walk.o, t = heads_fast ? walk.o : walk.i;
+          const int64_t at = place.row[t], row = at + (int64_t)h * head_rows;
+          if (at >= 0 && in_bounds(row, a.num_pages * a.H * a.page)) {
+            const int64_t head = (int64_t)h * head_bytes;
+            dst[u] = to + t * step_t + h * step_h;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(from + place.codes[t] + head) + lane;
+            const uint8_t* bs = from + place.blocks[t] + head + lane / 2;
+            codes[u][0] = ld4(src);
+            codes[u][1] = ld4(src + lanes);
+            blocks[u][0] = __ldg(bs);
+            blocks[u][1] = __ldg(bs + lanes / 2);
+            scale[u] = __ldg(scales + row);
+          }
+          walk.next();
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (dst[u] == nullptr) continue;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t h[4];
+          e2m1x8_to_f16x2(codes[u][x], h);
+          const uint32_t b = e4m3x2_to_f16x2((uint16_t)(blocks[u][x] * 0x101u));
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t p = hmul2(h[i], b);             // 2 + 4 significant bits, in f16's range
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
+            f[2 * i] = v.x * scale[u];
+            f[2 * i + 1] = v.y * scale[u];
+          }
+          Row8<T> y;
+          y.set(f);
+          y.store(dst[u] + x * lanes * 8);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ reading
+
+template <typename T, Held kHeld>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, int tb) {
+  __shared__ int64_t place[kMaxTokens];
+  const int64_t t0 = (int64_t)blockIdx.x * tb;
+  const int tokens = (int)(a.T - t0 < tb ? a.T - t0 : tb);
+  check_cu(a);
+  int slot;
+  if ((int)threadIdx.x < tokens) place[threadIdx.x] = place_of(a, t0 + threadIdx.x, false, slot);
   __syncthreads();
   constexpr int kRows = rows_in_work<T, kHeld, false>();
   const int lanes = a.D / 16, lane = threadIdx.x % lanes, e0 = lane * 8, e1 = (lane + lanes) * 8;
@@ -241,7 +441,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   RowWalk walk(threadIdx.x / lanes, kThreads / lanes, ni);
   while (walk.o < 2 * no) {
     Row8<T> w[kRows][2];
-    uint2 codes[kRows][2];                       // 4 bits: a word's codes and its block's scale
+    uint2 codes[kRows][2];
     float scale[kRows];
     T* dst[kRows];
 #pragma unroll
@@ -255,14 +455,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         if (at >= 0 && in_bounds(row, a.num_pages * a.H * a.page)) {
           const int64_t off = second ? (t0 + t) * a.v_s + h * a.v_h : (t0 + t) * a.k_s + h * a.k_h;
           dst[u] = reinterpret_cast<T*>(second ? a.v : a.k) + off;
-          if (kHeld == kE2m1) {
-            const uint8_t* base = reinterpret_cast<const uint8_t*>(second ? a.vc : a.kc);
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(base + e2m1_codes(row, slots[t], a.D));
-            const uint8_t* bs = base + e2m1_blocks(row, slots[t], a.page, a.D) + lane / 2;
-            codes[u][0] = make_uint2(__ldg(src + lane), __ldg(bs));
-            codes[u][1] = make_uint2(__ldg(src + lane + lanes), __ldg(bs + lanes / 2));
-            scale[u] = __ldg((second ? a.vs : a.ks) + row);
-          } else if (kHeld == kE4m3) {
+          if (kHeld == kE4m3) {
             const uint8_t* src = reinterpret_cast<const uint8_t*>(second ? a.vc : a.kc) + row * a.D;
             codes[u][0] = ld8(src + e0);
             codes[u][1] = ld8(src + e1);
@@ -281,23 +474,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       if (dst[u] == nullptr) continue;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (kHeld != kAsIs) {
+        if (kHeld == kE4m3) {
           float f[8];
-          if (kHeld == kE2m1) {
-            uint32_t h[4];
-            e2m1x8_to_f16x2(codes[u][x].x, h);
-            const uint32_t b = e4m3x2_to_f16x2((uint16_t)(codes[u][x].y * 0x101u));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t p = hmul2(h[i], b);           // exact: 2 + 4 significant bits, in f16's range
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p));
-              f[2 * i] = v.x;
-              f[2 * i + 1] = v.y;
-            }
-          } else {
-            e4m3x4_to_f32(codes[u][x].x, f);
-            e4m3x4_to_f32(codes[u][x].y, f + 4);
-          }
+          e4m3x4_to_f32(codes[u][x].x, f);
+          e4m3x4_to_f32(codes[u][x].y, f + 4);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] *= scale[u];
           w[u][x].set(f);
@@ -312,12 +492,14 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 // resolving the places is small beside them, unless that leaves SMs idle.
 // (e4m3, 4 heads of 64: 45808 tokens 15.4 us; 16 tokens a CTA, which half fill
 // a round, 22.3.  17021 tokens 7.8 us; four CTAs an SM instead of one 10.0.)
-int tokens_per_cta(const CacheArgs& a) {
+// Rows to 4 bits: twice as many, for what a CTA sets up costs more (131072 tokens
+// of 8 heads of 128: 4BIT_A us, with 8 rows 4BIT_B).
+int tokens_per_cta(const CacheArgs& a, int rows = 8) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int tb = 1;
-  while (tb < kMaxTokens && 2 * tb * a.H * (a.D / 16) < 8 * kThreads) tb *= 2;
+  while (tb < kMaxTokens && 2 * tb * a.H * (a.D / 16) < rows * kThreads) tb *= 2;
   while (tb > 1 && (a.T + tb - 1) / tb < sms) tb /= 2;
   return tb;
 }
@@ -328,13 +510,13 @@ namespace {
 
 template <typename T>
 void write_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
-  if (a.cache_dtype == ULYSSES_E2M1) cache_write_kernel<T, kE2m1><<<grid, kThreads, 0, st>>>(a, tb);
+  if (a.cache_dtype == ULYSSES_E2M1) cache_write_4bit_kernel<T><<<grid, kThreads, 0, st>>>(a, tb);
   else if (a.cache_dtype == ULYSSES_E4M3) cache_write_kernel<T, kE4m3><<<grid, kThreads, 0, st>>>(a, tb);
   else cache_write_kernel<T, kAsIs><<<grid, kThreads, 0, st>>>(a, tb);
 }
 template <typename T>
 void read_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
-  if (a.cache_dtype == ULYSSES_E2M1) cache_read_kernel<T, kE2m1><<<grid, kThreads, 0, st>>>(a, tb);
+  if (a.cache_dtype == ULYSSES_E2M1) cache_read_4bit_kernel<T><<<grid, kThreads, 0, st>>>(a, tb);
   else if (a.cache_dtype == ULYSSES_E4M3) cache_read_kernel<T, kE4m3><<<grid, kThreads, 0, st>>>(a, tb);
   else cache_read_kernel<T, kAsIs><<<grid, kThreads, 0, st>>>(a, tb);
 }
@@ -342,7 +524,7 @@ void read_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
 }  // namespace
 
 int launch_cache_write(const CacheArgs& a, cudaStream_t st) {
-  const int tb = tokens_per_cta(a);
+  const int tb = tokens_per_cta(a, a.cache_dtype == ULYSSES_E2M1 ? 16 : 8);
   const unsigned grid = (unsigned)((a.T + tb - 1) / tb);
   if (a.dtype == ULYSSES_BF16) write_rows<__nv_bfloat16>(a, grid, tb, st);
   else write_rows<float>(a, grid, tb, st);

@@ -50,6 +50,11 @@ def pack(codes, block):
     return torch.from_numpy(np.concatenate((c, b), -1).reshape(P, H, page, 9 * D // 16))
 
 
+def same_codes(a, b):
+    """Element by element; a code of magnitude 0 may have either sign."""
+    return (a == b) | (((a | b) & 7) == 0)
+
+
 def rows_in(shape, dtype, seed, gain=1.0):
     g = torch.Generator().manual_seed(seed)
     return (torch.randn(shape, generator=g) * torch.exp(torch.randn(shape[-1:], generator=g)) * gain).to(DT[dtype])
@@ -110,7 +115,7 @@ def test_write_and_read(new, before, H, D, page, dtype, layout):
                 t = cu[b] + i
                 assert np.array_equal(got_s[pg, :, sl], sc[t]), (name, b, i)
                 assert np.array_equal(got_b[pg, :, sl], block[t]), (name, b, i)
-                ok = got_c[pg, :, sl] == codes[t]
+                ok = same_codes(got_c[pg, :, sl], codes[t])
                 if dtype == "fp32":
                     z = np.abs(rows[t] / sc[t][:, None] / np.repeat(np.where(block[t] > 0, block[t], 1), 16, -1))
                     ok |= np.min(np.abs(z[..., None] / np.array(so.E2M1_BORDERS) - 1), -1) < 2.0 ** -22
@@ -153,7 +158,8 @@ def test_rows_at_the_edges():
     c, b, s, r = one_row(z * 448.0)
     assert s == 1.0 and b[0] == 448.0 and list(b[1:]) == [0, 0, 0]
     want = [0, 2, 2, 4, 4, 6, 6]
-    assert list(c[:7]) == want and list(c[7:14]) == [8 + x for x in want] and c[15] == 7 and not c[16:].any()
+    assert list(c[:7]) == want and same_codes(c[7:14], np.array([8 + x for x in want])).all()
+    assert c[15] == 7 and not c[16:].any()
     assert r[15] == 2688.0 and r[12] == -1792.0
     # zeros; the smallest numbers; blocks far below the row's largest
     c, b, s, r = one_row(np.zeros(64))
@@ -174,7 +180,7 @@ def test_rows_at_the_edges():
         row[3] = big
         codes, block, scale = so.quantise4(np.float64(np.float32(row))[None])
         c, b, s, r = one_row(row)
-        assert np.array_equal(c, codes[0]) and np.array_equal(b, block[0]) and s == scale[0]
+        assert same_codes(c, codes[0]).all() and np.array_equal(b, block[0]) and s == scale[0]
         assert big != 2.0 ** 127 or np.isfinite(r).all()
     for bad in (math.inf, -math.inf, math.nan):
         row = np.ones(64)

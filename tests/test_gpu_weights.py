@@ -94,7 +94,7 @@ def test_weights(case, wide):
         check(o, lse, rows, dtype, cache, layout)
     # and again on top, with a workspace of the caller's
     ws = U.attn_decode_workspace(args["q"], args["k_cache"], args["page_table"], layout=layout, weights=True)
-    assert ws.numel() > 0
+    assert ws.numel() > 0 or not wide
     U.attn_decode(weights=w, workspace=ws, **args)
     U.check()
     check_weights(w, before, args, rows, times=2)
