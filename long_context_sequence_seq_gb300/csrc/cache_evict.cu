@@ -123,20 +123,23 @@ __device__ __forceinline__ void sync_all(int ctas) {
     __syncthreads();
   }
 }
-// An int of CTA `rank`'s shared memory, at this CTA's address of it.
-__device__ __forceinline__ int ld_rank(const int* p, int rank, int ctas) {
-  return ctas > 1 ? ld_cluster(tc::smem_u32(p), rank) : *p;
+// An int of every CTA's shared memory, at this CTA's address of it (0 of those there
+// are not); the loads do not wait for each other.
+constexpr int kMaxCtas = 8;
+__device__ __forceinline__ void ld_ranks(const int* p, int ctas, int (&v)[kMaxCtas]) {
+#pragma unroll
+  for (int c = 0; c < kMaxCtas; ++c) v[c] = c < ctas ? ld_cluster(tc::smem_u32(p), c) : 0;
 }
 
 // Units a thread holds in registers from one digit to the next; those of longer
 // sequences are loaded again (from L2).
 constexpr int kHold = 2;
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ EvictArgs a,
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictArgs a,
                                                                 const __grid_constant__ Lists l, int ctas) {
   __shared__ int hist[kBins];
   __shared__ int part[kBins];                              // totals over the cluster, of this CTA's bins
-  __shared__ int part_sum;
+  __shared__ int part_sum[3];                              // theirs, for each digit
   __shared__ int sums[kThreads / 32];
   __shared__ int found[3];                                 // the digit, the positions in the digits above it, in it
   __shared__ int mine[2];                                  // of this CTA's positions: above the threshold, at it
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     for (int c = threadIdx.x; c < (z.n + a.page - 1) / a.page; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
   for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
   if (threadIdx.x < 2) mine[threadIdx.x] = 0;
+  if (threadIdx.x < 3) part_sum[threadIdx.x] = 0;
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) raise_error(kErrPages);
     z.m = z.n;
@@ -187,12 +191,23 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
       auto count_unit = [&](const uint32_t (&key)[kUnit], int u) {
         const int live = old - u * kUnit;
+        if (pass > 0) {                                    // few: those with the digits found so far
+          uint32_t some = 0;
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) some |= (uint32_t)(key[i] >> (shift + bits) == prefix) << i;
+          if (live < kUnit) some &= (1u << live) - 1;
+          if (!some) return;
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i)
+            if (some >> i & 1) atomicAdd(hist + ((key[i] >> shift) & ((1 << bits) - 1)), 1);
+          return;
+        }
         // neighbours of one bin are counted together: tokens nobody looked at are alike
         int bin = -1, count = 0;
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          if (i >= live || (pass > 0 && key[i] >> (shift + bits) != prefix)) continue;
-          const int d = (int)(key[i] >> shift) & ((1 << bits) - 1);
+          if (i >= live) continue;
+          const int d = (int)(key[i] >> shift);
           if (d == bin) { ++count; continue; }
           if (count) atomicAdd(hist + bin, count);
           bin = d;
@@ -216,19 +231,27 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
       if (ctas > 1) {
         // each CTA adds up its share of the bins over the cluster ..
         for (int i = threadIdx.x; i < share; i += kThreads) {
-          int n = 0;
-          for (int c = 0; c < ctas; ++c) n += ld_rank(hist + rank * share + i, c, ctas);
+          int v[kMaxCtas], n = 0;
+          ld_ranks(hist + rank * share + i, ctas, v);
+#pragma unroll
+          for (int c = 0; c < kMaxCtas; ++c) n += v[c];
           part[i] = n;
           sum += n;
         }
-        (void)block_scan(sum, sums, total);
-        if (threadIdx.x == 0) part_sum = total;
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if ((threadIdx.x & 31) == 0 && sum) atomicAdd(part_sum + pass, sum);
         sync_all(ctas);
         // .. all find the share that has the digit ..
-        for (owner = ctas - 1; owner > 0; --owner) {
-          const int n = ld_rank(&part_sum, owner, ctas);
-          if (above + n >= k_left) break;
-          above += n;
+        int v[kMaxCtas];
+        ld_ranks(part_sum + pass, ctas, v);
+        bool passed = false;
+#pragma unroll
+        for (int c = kMaxCtas - 1; c >= 0; --c) {
+          if (!passed && (above + v[c] >= k_left || c == 0)) {
+            owner = c;
+            passed = true;
+          }
+          above += passed ? 0 : v[c];
         }
       }
       // .. and the digit in it, from the top
@@ -238,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         const int bin = share - 1 - ((int)threadIdx.x * kOwn + i);
-        n[i] = bin >= 0 ? (ctas > 1 ? ld_rank(part + bin, owner, ctas) : hist[bin]) : 0;
+        n[i] = bin >= 0 ? (ctas > 1 ? ld_cluster(tc::smem_u32(part + bin), owner) : hist[bin]) : 0;
         sum += n[i];
       }
       int upto = above + block_scan(sum, sums, total) - sum;   // positions in the bins above
@@ -274,9 +297,13 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   if (ctas > 1) {
     __syncthreads();
     sync_all(ctas);
-    for (int c = 0; c < rank; ++c) {
-      gt0 += ld_rank(mine, c, ctas);
-      eq0 += ld_rank(mine + 1, c, ctas);
+    int g[kMaxCtas], e[kMaxCtas];
+    ld_ranks(mine, ctas, g);
+    ld_ranks(mine + 1, ctas, e);
+#pragma unroll
+    for (int c = 0; c < kMaxCtas; ++c) {
+      gt0 += c < rank ? g[c] : 0;
+      eq0 += c < rank ? e[c] : 0;
     }
   }
   auto list_units = [&](const uint32_t (&key)[kUnit], int u) {
@@ -292,20 +319,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     int total;
     const int counts = __popc(gt) | __popc(eq) << 16;      // at most 8192 of each
     const int upto = block_scan(counts, sums, total) - counts;
-    int g = gt0 + (upto & 0xffff), e = eq0 + (upto >> 16);
+    const int g = gt0 + (upto & 0xffff), e = eq0 + (upto >> 16);
     if (u < u1) {
-      if (u * kUnit % l.chunk == 0) before[u * kUnit / l.chunk] = g + min(e, k_left);
-      const int per = a.page / kUnit, col = u / per;
-      const int64_t first = (gt | eq) == 0 ? 0 : ((int64_t)__ldg(row + col) * a.H + h) * a.page + (u - col * per) * kUnit;
-      for (uint32_t left = gt | eq; left; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        const bool is_gt = gt >> i & 1;
-        if (is_gt || e < k_left) {
-          const int at = g + min(e, k_left);
-          if (in_bounds(at, k)) src[at] = first + i;
-        }
-        g += is_gt;
-        e += !is_gt;
+      int at = g + min(e, k_left);
+      if ((u * kUnit & (l.chunk - 1)) == 0) before[u * kUnit / l.chunk] = at;
+      // the first of those at it, as many as are left
+      for (int over = __popc(eq) - max(k_left - e, 0); over > 0; --over) eq &= ~(0x80000000u >> __clz(eq));
+      uint32_t stay = gt | eq;
+      if (stay) {
+        const int per = a.page / kUnit, col = u / per;
+        const int64_t first = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (u - col * per) * kUnit;
+        for (; stay; stay &= stay - 1, ++at)
+          if (in_bounds(at, k)) src[at] = first + __ffs(stay) - 1;
       }
     }
     gt0 += total & 0xffff;
@@ -370,7 +395,7 @@ __global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_con
   constexpr int kStages = stages_of(kRowB, kFour, kScales), kStageB = stage_bytes(kRowB, kFour, kScales);
   constexpr int kRing = kStages + 2;                       // chunks whose places are known
   constexpr int D = kRowB * 2;                             // kFour
-  static_assert(kOwn >= 1 && kStages >= 2, "");
+  static_assert(kOwn >= 1 && kStages >= 2 && (kChunk & (kChunk - 1)) == 0 && kChunk % kUnit == 0, "");
   using Place = Places<kChunk>;
   extern __shared__ __align__(16) char stages[];           // kStages, for the rows on their way
   int2* const size = reinterpret_cast<int2*>(stages + kStages * kStageB);   // [B], and chunks of the sequences before, of one head
@@ -633,7 +658,7 @@ WsLayout ws_layout(const EvictArgs& a) {
 // SM allow it.
 int cluster_of(const EvictArgs& a) {
   int c = 1;
-  while (c < 8 && (int64_t)a.cols * a.page > (int64_t)c * kThreads * kUnit && (int64_t)a.B * a.H * c * 2 <= 152 * 2) c *= 2;
+  while (c < kMaxCtas && (int64_t)a.cols * a.page > (int64_t)c * kThreads * kUnit && (int64_t)a.B * a.H * c * 2 <= 152 * 2) c *= 2;
   return c;
 }
 
