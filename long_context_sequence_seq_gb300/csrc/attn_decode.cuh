@@ -1484,7 +1484,7 @@ __device__ __forceinline__ void add_lanes(Sum& x, int o) {   // with lane ^ o, i
 // at a time (few items, hundreds of pieces each); kRow: a CTA for the head;
 // kWarp: a warp for it (many items, of a few pieces or none).
 enum Join { kPart, kRow, kWarp };
-template <typename TQ, int D, Join kHow, int kJoin>
+template <typename TQ, int D, Join kHow, int kJoin, bool kSeen>
 __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constant__ DecodeArgs a,
                                                             const __grid_constant__ Plan p) {
   constexpr int kLanes = kHow == kPart ? 8 : D / 4;                // threads across the values, four each
@@ -1560,7 +1560,7 @@ __global__ void __launch_bounds__(kJoin) decode_join_kernel(const __grid_constan
   } else if (lane >= kLanes) {
     return;
   }
-  if (a.fin && c == 0) finish(a, b, hq, x.m, x.l);
+  if (kSeen && c == 0) finish(a, b, hq, x.m, x.l);
   if (x.l == 0.f) {   // no key that counts; a branch: selects at each quotient made 25.9 us of 24 ragged x 4096 27.0
     d[0] = d[1] = d[2] = d[3] = from_f32<TQ>(0.f);
     if (c == 0 && a.lse) a.lse[(int64_t)b * a.H_q + hq] = -INFINITY;
@@ -1717,11 +1717,12 @@ int run(const DecodeArgs& a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     using TQ = typename Engine::TQ;
-    const auto join = how == kWarp                      ? decode_join_kernel<TQ, D, kWarp, 256>
-                      : how == kPart && threads == 256 ? decode_join_kernel<TQ, D, kPart, 256>
-                      : how == kPart                   ? decode_join_kernel<TQ, D, kPart, 128>
-                      : threads == 256                 ? decode_join_kernel<TQ, D, kRow, 256>
-                                                       : decode_join_kernel<TQ, D, kRow, 128>;
+    constexpr bool kSeen = Engine::kSeen;
+    const auto join = how == kWarp                      ? decode_join_kernel<TQ, D, kWarp, 256, kSeen>
+                      : how == kPart && threads == 256 ? decode_join_kernel<TQ, D, kPart, 256, kSeen>
+                      : how == kPart                   ? decode_join_kernel<TQ, D, kPart, 128, kSeen>
+                      : threads == 256                 ? decode_join_kernel<TQ, D, kRow, 256, kSeen>
+                                                       : decode_join_kernel<TQ, D, kRow, 128, kSeen>;
     const cudaError_t err = cudaLaunchKernelEx(&cfg, join, x, p);
     if (err != cudaSuccess) return launch_failed("attn_decode join", err);
     count_launch();

@@ -88,7 +88,7 @@ __device__ __forceinline__ void check_cu(const CacheArgs& a) {
 template <typename T, Held kHeld, bool kWrite>
 constexpr int rows_in_work() { return kWrite ? (sizeof(T) == 2 ? 4 : 2) : (kHeld != kAsIs ? 4 : (sizeof(T) == 2 ? 2 : 1)); }
 
-template <typename T, Held kHeld>
+template <typename T, Held kHeld, bool kWeights>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, int tb) {
   __shared__ int64_t place[kMaxTokens];
   const int64_t t0 = (int64_t)blockIdx.x * tb;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         const int64_t at = place[t];
         if (at >= 0 && in_bounds(at + (int64_t)h * a.page, a.num_pages * a.H * a.page)) {
           row[u] = at + (int64_t)h * a.page;
-          if (a.w && lane == 0 && !second[u]) a.w[row[u]] = 0.f;
+          if (kWeights && lane == 0 && !second[u]) a.w[row[u]] = 0.f;
           const int64_t off = second[u] ? (t0 + t) * a.v_s + h * a.v_h : (t0 + t) * a.k_s + h * a.k_h;
           const T* src = reinterpret_cast<const T*>(second[u] ? a.v : a.k) + off;
           w[u][0].load(src + e0);
@@ -508,11 +508,11 @@ int tokens_per_cta(const CacheArgs& a, int rows = 8) {
 
 namespace {
 
-template <typename T>
+template <typename T, bool kWeights>
 void write_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
   if (a.cache_dtype == ULYSSES_E2M1) cache_write_4bit_kernel<T><<<grid, kThreads, 0, st>>>(a, tb);
-  else if (a.cache_dtype == ULYSSES_E4M3) cache_write_kernel<T, kE4m3><<<grid, kThreads, 0, st>>>(a, tb);
-  else cache_write_kernel<T, kAsIs><<<grid, kThreads, 0, st>>>(a, tb);
+  else if (a.cache_dtype == ULYSSES_E4M3) cache_write_kernel<T, kE4m3, kWeights><<<grid, kThreads, 0, st>>>(a, tb);
+  else cache_write_kernel<T, kAsIs, kWeights><<<grid, kThreads, 0, st>>>(a, tb);
 }
 template <typename T>
 void read_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
@@ -526,8 +526,8 @@ void read_rows(const CacheArgs& a, unsigned grid, int tb, cudaStream_t st) {
 int launch_cache_write(const CacheArgs& a, cudaStream_t st) {
   const int tb = tokens_per_cta(a, a.cache_dtype == ULYSSES_E2M1 ? 16 : 8);
   const unsigned grid = (unsigned)((a.T + tb - 1) / tb);
-  if (a.dtype == ULYSSES_BF16) write_rows<__nv_bfloat16>(a, grid, tb, st);
-  else write_rows<float>(a, grid, tb, st);
+  if (a.dtype == ULYSSES_BF16) a.w ? write_rows<__nv_bfloat16, true>(a, grid, tb, st) : write_rows<__nv_bfloat16, false>(a, grid, tb, st);
+  else a.w ? write_rows<float, true>(a, grid, tb, st) : write_rows<float, false>(a, grid, tb, st);
   count_launch();
   return check_launch("cache_write");
 }
