@@ -143,18 +143,25 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   __shared__ int sums[kThreads / 32];
   __shared__ int found[3];                                 // the digit, the positions in the digits above it, in it
   __shared__ int mine[2];                                  // of this CTA's positions: above the threshold, at it
+  __shared__ int few;                                      // positions left to choose from, when they are few: how many
+  __shared__ int few_key[32], few_at[32];                  // of this CTA's, their orders and places
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0, item = blockIdx.x / ctas;
   const int b = item / a.H, h = item - b * a.H;
   const int32_t* row = a.table + (int64_t)b * a.cols;
+  int page = (int)threadIdx.x < a.cols ? __ldg(row + threadIdx.x) : 0;   // on its way beside the lengths
   Size z = size_of(a, b);
   if (blockIdx.x == 0 && threadIdx.x == 0) *l.ticket = 0;
   // a page out of range: the sequence is left as it is, all of its heads (each looks at the whole row)
   int bad = 0;
   if (z.m < z.n)
-    for (int c = threadIdx.x; c < (z.n + a.page - 1) / a.page; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
+    for (int c = threadIdx.x, last = (z.n - 1) / a.page; c <= last; c += kThreads) {
+      bad |= (unsigned)page >= (unsigned)a.num_pages;
+      if (c + kThreads <= last) page = __ldg(row + c + kThreads);
+    }
   for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
   if (threadIdx.x < 2) mine[threadIdx.x] = 0;
+  if (threadIdx.x == 0) few = 0;
   if (threadIdx.x < 3) part_sum[threadIdx.x] = 0;
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) raise_error(kErrPages);
@@ -270,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
         if (upto < k_left && upto + n[i] >= k_left) {      // one thread, once
           found[0] = owner * share + share - 1 - ((int)threadIdx.x * kOwn + i);
           found[1] = upto;
+          found[2] = n[i];
         }
         upto += n[i];
       }
@@ -285,6 +293,75 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
         }
         own = __reduce_add_sync(0xffffffffu, own);
         if ((threadIdx.x & 31) == 0 && own) atomicAdd(mine, own);
+      }
+      if (pass < 2 && found[2] <= 32) {
+        // few have the digits so far: they are put in order one against the other
+        auto keep_few = [&](const uint32_t (&key)[kUnit], int u) {
+          const int live = old - u * kUnit;
+          uint32_t some = 0;
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) some |= (uint32_t)(i < live && key[i] >> shift == prefix) << i;
+          if (!some) return;
+          const int x = atomicAdd(&few, __popc(some));
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i)
+            if (some >> i & 1) {
+              const int at = x + __popc(some & ((1u << i) - 1));
+              few_key[at] = (int)key[i];
+              few_at[at] = u * kUnit + i;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+          const int u = u0 + i * kThreads + threadIdx.x;
+          if (u < u1) keep_few(held[i], u);
+        }
+        for (int u = u0 + kHold * kThreads + threadIdx.x; u < u1; u += kThreads) {
+          uint32_t key[kUnit];
+          load_unit(a, row, h, u, key);
+          keep_few(key, u);
+        }
+        sync_all(ctas);
+        if (threadIdx.x < 32) {
+          int v[kMaxCtas], at = threadIdx.x, owner = -1;   // lane i has the i-th of all CTAs'
+          if (ctas > 1) ld_ranks(&few, ctas, v);
+#pragma unroll
+          for (int c = 0; c < kMaxCtas; ++c) {
+            const int n = ctas > 1 ? v[c] : (c == 0 ? few : 0);
+            if (owner < 0) {
+              if (at < n) owner = c;
+              else at -= n;
+            }
+          }
+          uint32_t key = 0;
+          int place = 0, ahead = 0;
+          if (owner >= 0) {
+            key = (uint32_t)(ctas > 1 ? ld_cluster(tc::smem_u32(few_key + at), owner) : few_key[at]);
+            place = ctas > 1 ? ld_cluster(tc::smem_u32(few_at + at), owner) : few_at[at];
+          }
+          for (int i = 0; i < found[2]; ++i) {
+            const uint32_t other = __shfl_sync(0xffffffffu, key, i);
+            const int its = __shfl_sync(0xffffffffu, place, i);
+            ahead += other > key || (other == key && its < place);
+          }
+          const uint32_t last = __ballot_sync(0xffffffffu, owner >= 0 && ahead == k_left - 1);   // one lane: the last that stays
+          const uint32_t edge = __shfl_sync(0xffffffffu, key, __ffs(last) - 1);
+          const uint32_t over = __ballot_sync(0xffffffffu, owner >= 0 && key > edge);
+          const bool own = owner == rank;
+          const uint32_t own_over = __ballot_sync(0xffffffffu, own && key > edge), own_at = __ballot_sync(0xffffffffu, own && key == edge);
+          if (threadIdx.x == 0) {
+            found[0] = (int)edge;
+            found[1] = __popc(over);
+            if (ctas > 1) {
+              mine[0] += __popc(own_over);
+              mine[1] = __popc(own_at);
+            }
+          }
+        }
+        __syncthreads();
+        prefix = (uint32_t)found[0];
+        k_left -= found[1];
+        break;
       }
       if (pass < 2) {                                      // cleared for the next digit
         for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
@@ -321,16 +398,19 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
     const int upto = block_scan(counts, sums, total) - counts;
     const int g = gt0 + (upto & 0xffff), e = eq0 + (upto >> 16);
     if (u < u1) {
-      int at = g + min(e, k_left);
+      const int at = g + min(e, k_left);
       if ((u * kUnit & (l.chunk - 1)) == 0) before[u * kUnit / l.chunk] = at;
       // the first of those at it, as many as are left
       for (int over = __popc(eq) - max(k_left - e, 0); over > 0; --over) eq &= ~(0x80000000u >> __clz(eq));
-      uint32_t stay = gt | eq;
+      const uint32_t stay = gt | eq;
       if (stay) {
         const int per = a.page / kUnit, col = u / per;
         const int64_t first = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (u - col * per) * kUnit;
-        for (; stay; stay &= stay - 1, ++at)
-          if (in_bounds(at, k)) src[at] = first + __ffs(stay) - 1;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          const int to = at + __popc(stay & ((1u << i) - 1));
+          if ((stay >> i & 1) && in_bounds(to, k)) src[to] = first + i;
+        }
       }
     }
     gt0 += total & 0xffff;
@@ -415,6 +495,8 @@ __global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_con
     tc::fence_barrier_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  int ticket = 0;                                          // the ninth warp's first lane's: the next chunk
+  if (threadIdx.x == kMoveThreads) ticket = atomicAdd(l.ticket, 1);
   for (int b = threadIdx.x; b < a.B; b += kMovers) {
     const int2 z = l.size[b];
     size[b] = z;
@@ -570,8 +652,6 @@ __global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_con
   }
   constexpr int kMine = (kChunk + 31) / 32;                // rows of a lane
   const int64_t total = (int64_t)prefix[a.B] * a.H, rows = a.num_pages * a.H * a.page;
-  int ticket = 0;                                          // lane 0's: the next chunk
-  if (lane == 0) ticket = atomicAdd(l.ticket, 1);
   int round = 0;
 #pragma unroll 1
   for (Turn now;; now.next(kRing), ++round) {
