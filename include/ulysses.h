@@ -443,7 +443,8 @@ int ulysses_cache_read(const void* k_cache, const void* v_cache, const float* k_
  * the table, and a page id outside [0, num_pages), are reported by
  * ulysses_check as ULYSSES_ERR_BAD_PAGES (the keys concerned are left out).
  * Results do not depend on the order in which the GPU runs the call's blocks.
- * Row scales of an E4M3 or E2M1 cache are positive (or NaN).  An infinite element of V makes
+ * Row scales of an E4M3 or E2M1 cache are positive (or NaN), of an E2M1 cache
+ * 2^-126 or more.  An infinite element of V makes
  * its output element infinite (NaN with both signs, or where its key's weight
  * vanishes in fp32).  With FP32 queries of three heads a kv head or more (two
  * with D = 64) products are formed of two 11-bit parts of each operand: within
@@ -468,8 +469,10 @@ int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_c
  *   weights  [num_pages][H_kv][page_size] fp32, 16-byte aligned
  * A slot gets one addition a call; where sequences share a page it gets one of
  * each, in no fixed order.  Keys that the call leaves out, and heads none of whose
- * keys counts, add nothing.  The workspace holds the scores of every position of
- * the tables (4 * B * H_q * table_cols * page_size bytes, at most 2048 sequences'). */
+ * keys counts, add nothing; a head whose LSE is NaN makes its keys' weights NaN.
+ * The workspace holds the scores of every position of the tables (4 bytes each for
+ * the query heads of at most 2048 sequences, a kv head's rounded up to whole
+ * groups), unless the tables are short. */
 size_t ulysses_attn_decode_weights_workspace(int B, int H_q, int H_kv, int D, int table_cols, int page_size, int dtype,
                                              int cache_dtype);
 int ulysses_attn_decode_weights(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, const void* v_cache,

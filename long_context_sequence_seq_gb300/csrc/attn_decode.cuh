@@ -29,6 +29,12 @@
 // 344 as a call among others.)
 // Where the page table has room for a few units a warp only, a cluster of CTAs
 // takes each item and joins through distributed shared memory: one launch.
+// With weights (kSeen) the engines keep each key's scores, and once the heads'
+// maxima and sums are final a pass over the scores adds exp2(s - m) / l to the
+// keys' slots: in the cluster from shared memory (3 us more than without at 500 to
+// 4000 keys), else in a third kernel from the workspace.  Scores and not weights
+// are kept, because a weight's maximum and sum are known last; recomputing the
+// scores would read K again, 128 bytes a key in e4m3 and D = 128 against 32.
 //
 // Three engines walk a piece.
 //   Matrix engine (bf16 queries): keys are the M = 16 side of mma m16n8k16 and
@@ -1288,8 +1294,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_kernel(const __grid
 // split launch left and the heads' final maxima and sums:
 //   weights[place of key j] += sum_h exp2(s_hj - m_h) / l_h
 // the query heads h of the kv head in their order.  The units of all (sequence,
-// kv head) are dealt to the warps in equal ranges, a lane a key.  Bound by the
-// memory that the scores and the weights take, 4 G + 8 bytes a key.
+// kv head) are dealt to the warps in equal ranges, a lane a key of four pairs of
+// units at a time.  Bound by what the scores and the weights take (4 G + 8 bytes a
+// key and kv head, from L2 for the most part) and the chain of table and scores:
+// 64 ragged sequences of up to 16384 bf16 keys, 8 kv heads of 128 with 4 query
+// heads each (1.06 GB of rows): 19 us behind the split kernel's 162 and the join's
+// 7; a pair of units at a time 30.
 constexpr int kSeenThreads = 256;
 __global__ void __launch_bounds__(kSeenThreads) decode_weights_kernel(const __grid_constant__ DecodeArgs a,
                                                                       const __grid_constant__ Plan p) {

@@ -7,20 +7,31 @@
 // so position i of what is left is the i-th token that stays, and the places from
 // m on are left as they were.
 //
-// Two kernels.  The first selects: a cluster of CTAs for each (sequence, kv
-// head) finds the smallest weight that stays by its bits, three digits from the
-// top, each from a histogram over the cluster, and writes the list of the
-// positions that stay.  Weights are ordered as unsigned numbers (sign and
-// magnitude made monotone; -0 as +0, NaN above everything).
+// Two kernels.  The first selects: a cluster of CTAs for each (sequence, kv head)
+// finds the smallest weight that stays by its bits, three digits from the top, each
+// from a histogram over the cluster, and writes the list of the rows that stay.
+// Weights are ordered as unsigned numbers (sign and magnitude made monotone; -0 as
+// +0, NaN above everything).  Up to 16384 positions a CTA stay in registers from
+// digit to digit.  Bound by latencies: launch, lengths, table, weights, and about
+// 1.5 us a digit (10 us for a few positions, 25 for 131072 in 8 CTAs a head, of
+// which 2.5 would be reading them).  Where at most 32 positions are left to choose
+// from, they are put in order one against the other instead.
 //
 // The second moves rows, in place: a chunk of rows, K, V, scales and weights, is
-// read into registers and then written.  A row never moves up, so what a chunk of
-// C rows overwrites are rows of itself and of at most two chunks before it (the
-// C places hold at most C kept rows, neighbours in rank): it waits until those
-// have been read.  CTAs take chunks by a counter, in order, and a chunk's reading
-// waits for nothing but writes of chunks before it, so the first chunk that is not
-// done can always go on.  Every kept row is read and written
-// once, which is all the memory traffic there is beside the weights'.
+// read into shared memory and then written.  A row never moves up, so what a chunk
+// of C rows overwrites are rows of itself and of at most two chunks before it (the
+// C places hold at most C kept rows, neighbours in rank): it waits until those have
+// been read.  CTAs take chunks by a counter, in order.  A chunk's reading waits for
+// writes of chunks before it alone, and those for reading of chunks before them, so
+// the first chunk that is not done can always go on.  Every kept row is read and
+// written once, which is all the memory traffic there is beside the weights'.
+// Bound by HBM: 65536 rows of 8 heads of 128 in bf16 (537 MB) move in 91 us, 87% of
+// the copy rate.  Through registers, a chunk at a time, it was 128 us (a CTA's
+// loads, waits and stores one after the other); with a fence before each chunk's
+// flag, which waits for the stores before it, 139 us; one chunk ahead in shared
+// memory 118, of which 25 were waits for neighbours that read no earlier than they
+// wrote; as it is, two to five chunks ahead, the flags are there when they are
+// asked for.
 #include "internal.h"
 #include "rows.cuh"
 #include "tc_ptx.cuh"
@@ -434,7 +445,6 @@ struct Places {
   int64_t from[kChunk], to[kChunk];
   int* flags;                                              // the item's; NULL: there is no chunk
   int c, first, last;                                      // the chunk, and those that have rows in its places
-  int go;                                                  // those have been read
 };
 
 // Of a thread, in a chunk: words of K's and V's rows; weights and row scales; block scales.
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_con
       const Place& p = places[now.at];
       if (!p.flags) break;
       ok = load_next() && tc::mbar_wait(read + now.at, now.phase, &stop) && tc::mbar_wait(free_ + now.at, now.phase, &stop);
-      if (ok && p.go) {
+      if (ok) {
         const char* from = stages + stage * kStageB;
 #pragma unroll
         for (int x = 0; x < kOwn; ++x) {
@@ -625,8 +635,11 @@ __global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_con
           if (t - begin > kWaitLimitNs) break;
         }
       }
-      if (!ok) raise_error(kErrTimeout);
-      p.go = ok;
+      if (!ok) {                                           // the CTA leaves: others wait as long at most
+        raise_error(kErrTimeout);
+        *(volatile int*)&stop = 1;
+        return;
+      }
       tc::mbar_arrive(free_ + now.at);
       tc::mbar_arrive(done + now.at);
     }
