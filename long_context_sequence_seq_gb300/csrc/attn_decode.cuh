@@ -31,8 +31,8 @@
 // takes each item and joins through distributed shared memory: one launch.
 // With weights (kSeen) the engines keep each key's scores, and once the heads'
 // maxima and sums are final a pass over the scores adds exp2(s - m) / l to the
-// keys' slots: in the cluster from shared memory (3 us more than without at 500 to
-// 4000 keys), else in a third kernel from the workspace.  Scores and not weights
+// keys' slots: in the cluster from shared memory (at 500 to 8000 keys no slower than
+// without), else in a third kernel from the workspace.  Scores and not weights
 // are kept, because a weight's maximum and sum are known last; recomputing the
 // scores would read K again, 128 bytes a key in e4m3 and D = 128 against 32.
 //
@@ -102,6 +102,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;                       // of a CTA
 constexpr int kMinUnits = 2;                    // of a warp, where there are enough for all
 constexpr int kClusterUnits = 16;               // of a warp of a cluster, at most
+constexpr int kWideUnits = 64;                  // of a CTA of the wider clusters, at most
 constexpr int kMaxBatch = 2048;                 // sequences of one launch (their prefix sums sit in shared memory)
 
 // How a launch is split (host), the same for both of its kernels.
@@ -1381,12 +1382,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   const int units = (pc.len + kUnit - 1) / kUnit, warps = ctas * kWarps, w = rank * kWarps + warp;
   pc.unit0 = first_unit(w, warps, units);
   pc.units = first_unit(w + 1, warps, units) - pc.unit0;
-  extern __shared__ __align__(16) char shared[];
-  if (Engine::kSeen) {                                     // behind the rings
-    pc.heads = heads;
-    pc.scores = reinterpret_cast<float*>(shared + kWarps * ring_bytes<Engine>()) + warp * (kClusterUnits * heads * kUnit);
-  }
-  Engine e = make_engine<Engine>(lane, shared + warp * ring_bytes<Engine>());
+  Engine e = make_engine<Engine>(lane, nullptr);
   e.begin(a, pc);
   if (pc.units > 0) e.run(a, pc);
   e.partial(sml[warp], &so[warp][0][0], pc.gn);
@@ -1394,43 +1390,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
   tc::cluster_sync();
   const int total = pc.gn * D / 4, each = (total + ctas - 1) / ctas;
   const uint32_t o_at = tc::smem_u32(&so[0][0][0]), ml_at = tc::smem_u32(&sml[0][0]);
-  if (Engine::kSeen && pc.units > 0) {                     // (one group: the item has all of the kv head's query heads)
-    float mine = kNoMax, inv = 0.f;                        // of head `lane`: the maximum, and 1 / the sum
-    const int piece = min(lane, ctas * kWarps - 1);        // a lane a piece: at most 8 CTAs' four
-    for (int h = 0; h < pc.gn; ++h) {
-      float2 ml = cluster_ld2(ml_at + ((piece % kWarps) * kH + h) * 8, piece / kWarps);
-      float top = ml.x, l = lane < ctas * kWarps ? ml.y : 0.f;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      l *= exp2f(ml.x - top);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      if (lane == h) { mine = top; inv = l == 0.f ? 0.f : 1.f / l; }
-    }
-    constexpr int kPairs = 4;                              // of units, a lane a key: the warp's own scores
-    for (int u = 0; u < pc.units; u += 2 * kPairs) {
-      const int key = lane & 15;
-      int64_t row[kPairs];
-      float x[kPairs];
-      int unit[kPairs];
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        unit[i] = u + 2 * i + (lane >> 4);
-        const bool live = unit[i] < pc.units && (pc.unit0 + unit[i]) * kUnit + key < pc.len;
-        row[i] = live ? row_of_unit(a, pc.b, pc.h, pc.unit0 + unit[i]) : -1;
-        if (!live) unit[i] = 0;
-        x[i] = 0.f;
-      }
-      for (int h = 0; h < pc.gn; ++h) {
-        const float mh = __shfl_sync(0xffffffffu, mine, h), ih = __shfl_sync(0xffffffffu, inv, h);
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) x[i] += exp2f(pc.scores[(unit[i] * heads + h) * kUnit + key] - mh) * ih;
-      }
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i)
-        if (row[i] >= 0) add_weight(a, row[i] + key, x[i]);
-    }
-  }
   for (int i = rank * each + threadIdx.x; i < min(total, (rank + 1) * each); i += kWarps * 32) {
     const int hl = i / (D / 4), c = i - hl * (D / 4);
     float m = kNoMax, l = 0.f;
@@ -1448,6 +1407,140 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) decode_cluster_kernel(cons
         l += ml.y * f;
         s.x += x.x * f; s.y += x.y * f; s.z += x.z * f; s.w += x.w * f;
       }
+    }
+    using TQ = typename Engine::TQ;
+    const int hq = pc.h * a.G + pc.g0 + hl;
+    TQ* d = reinterpret_cast<TQ*>(a.o) + (int64_t)pc.b * a.o_b + (int64_t)hq * a.o_h + c * 4;
+    d[0] = from_f32<TQ>(quotient(s.x, l));
+    d[1] = from_f32<TQ>(quotient(s.y, l));
+    d[2] = from_f32<TQ>(quotient(s.z, l));
+    d[3] = from_f32<TQ>(quotient(s.w, l));
+    if (c == 0 && a.lse) a.lse[(int64_t)pc.b * a.H_q + hq] = (m + log2f(l)) * kLn2;   // l = 0: -inf
+  }
+  __syncwarp();
+  tc::cluster_sync();                                      // no CTA leaves while another reads its sums
+}
+
+// The same for the 4-bit engine, and with weights.  Pieces are joined in their CTA
+// first and then over the cluster, so a CTA may have eight warps (kW) of half as
+// many units; each warp then adds its own keys' weights to their slots, from its
+// scores in shared memory.  Bound by the chain length -> page -> K -> V -> joins:
+// 4099 bf16 keys of 8 kv heads of 128, 4 query heads each, with weights 12.9 us, 777
+// 4-bit ones without 8.0.  Joined over all warps of the cluster at once, by four
+// warps a CTA, with the heads' maxima and sums found one after the other, it was
+// 17.3 and 9.2.
+template <class Engine, int D, int kW, int kCtas>
+__global__ void __launch_bounds__(kW * 32, kCtas) decode_wide_cluster_kernel(const __grid_constant__ DecodeArgs a,
+                                                                              int groups, int heads, int ctas) {
+  constexpr int kH = Engine::kHeads, kUnits = kWideUnits / kW;
+  extern __shared__ __align__(16) char shared[];           // rings, sums, scores
+  __shared__ __align__(8) float2 sml[kW][kH], all_ml[kH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tc::cluster_ctarank(), item = blockIdx.x / ctas;
+  Piece pc;
+  const int hg = item % (a.H_kv * groups);
+  pc.b = item / (a.H_kv * groups);
+  pc.h = hg / groups;
+  pc.g0 = (hg - pc.h * groups) * heads;
+  pc.gn = min(a.G - pc.g0, heads);
+  pc.len = length_of(a, pc.b);
+  const int units = (pc.len + kUnit - 1) / kUnit, warps = ctas * kW, w = rank * kW + warp;
+  pc.unit0 = first_unit(w, warps, units);
+  pc.units = first_unit(w + 1, warps, units) - pc.unit0;
+  float* const so = reinterpret_cast<float*>(shared + kW * ring_bytes<Engine>());   // [warps][kH][D]
+  if (Engine::kSeen) {
+    pc.heads = heads;
+    pc.scores = so + kW * kH * D + warp * (kUnits * heads * kUnit);
+  }
+  Engine e = make_engine<Engine>(lane, shared + warp * ring_bytes<Engine>());
+  e.begin(a, pc);
+  if (pc.units > 0) e.run(a, pc);
+  constexpr int kPairs = kUnits / 2;                       // of units, a lane a key
+  const int key = lane & 15;
+  int64_t row[kPairs];                                     // kSeen: of the lane's keys
+  if (Engine::kSeen) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int unit = 2 * i + (lane >> 4);
+      const bool live = unit < pc.units && (pc.unit0 + unit) * kUnit + key < pc.len;
+      row[i] = live ? row_of_unit(a, pc.b, pc.h, pc.unit0 + unit) : -1;
+    }
+  }
+  e.partial(sml[warp], so + warp * kH * D, pc.gn);
+  __syncthreads();
+  const int total = pc.gn * D / 4;
+  for (int i = threadIdx.x; i < total; i += kW * 32) {
+    const int hl = i / (D / 4), c = i - hl * (D / 4);
+    float m = kNoMax, l = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kW; ++k) m = fmaxf(m, sml[k][hl].x);
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      const float2 ml = sml[k][hl];
+      const float4 x = *reinterpret_cast<const float4*>(so + (k * kH + hl) * D + c * 4);
+      const float f = exp2f(ml.x - m);
+      l += ml.y * f;
+      s.x += x.x * f; s.y += x.y * f; s.z += x.z * f; s.w += x.w * f;
+    }
+    *reinterpret_cast<float4*>(so + hl * D + c * 4) = s;   // nobody else has read or will read this place
+    if (c == 0) all_ml[hl] = make_float2(m, l);
+  }
+  __syncwarp();
+  tc::cluster_sync();
+  const uint32_t o_at = tc::smem_u32(so), ml_at = tc::smem_u32(all_ml);
+  if (Engine::kSeen) {                                     // (one group: the item has all of the kv head's query heads)
+    constexpr int kRounds = (kH + 3) / 4;                  // a lane a CTA of four heads
+    float top[kRounds], inv[kRounds], x[kPairs];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const float2 ml = cluster_ld2(ml_at + min(4 * r + (lane >> 3), pc.gn - 1) * 8, min(lane & 7, ctas - 1));
+      float t = ml.x;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      float l = (lane & 7) < ctas ? ml.y * exp2f(ml.x - t) : 0.f;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      top[r] = t;
+      inv[r] = l == 0.f ? 0.f : 1.f / l;
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) x[i] = 0.f;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      if (h >= pc.gn) break;
+      const float mh = __shfl_sync(0xffffffffu, top[h / 4], h % 4 * 8), ih = __shfl_sync(0xffffffffu, inv[h / 4], h % 4 * 8);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i)
+        if (row[i] >= 0) x[i] += exp2f(pc.scores[((2 * i + (lane >> 4)) * heads + h) * kUnit + key] - mh) * ih;
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      if (row[i] >= 0) add_weight(a, row[i] + key, x[i]);
+  }
+  const int each = (total + ctas - 1) / ctas;
+  for (int i = rank * each + threadIdx.x; i < min(total, (rank + 1) * each); i += kW * 32) {
+    const int hl = i / (D / 4), c = i - hl * (D / 4);
+    float2 ml[8];
+    float4 x[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      ml[r] = make_float2(kNoMax, 0.f);
+      x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < ctas) {
+        ml[r] = cluster_ld2(ml_at + hl * 8, r);
+        x[r] = cluster_ld4(o_at + (hl * D + c * 4) * 4, r);
+      }
+    }
+    float m = kNoMax, l = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) m = fmaxf(m, ml[r].x);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float f = exp2f(ml[r].x - m);
+      l += ml[r].y * f;
+      s.x += x[r].x * f; s.y += x[r].y * f; s.z += x[r].z * f; s.w += x[r].w * f;
     }
     using TQ = typename Engine::TQ;
     const int hq = pc.h * a.G + pc.g0 + hl;
@@ -1623,6 +1716,20 @@ inline int cluster_of(const DecodeArgs& a, int heads) {
   while (c > 1 && units <= (int64_t)(c / 2) * kWarps) c /= 2;   // no more warps than units
   return c;
 }
+// CTAs of eight warps for each item, one an SM, or 0: four warps.  Twice the warps
+// are taken where they hold the table too and four in each of eight CTAs would have
+// more than `most` units.  (8 kv heads of 4, one sequence, 8 warps and 4: with weights
+// 1000 bf16 keys 9.4 and 10.7 us, 1000 4-bit ones 9.6 and 10.7, 4 x 1500 bf16 11.4 and
+// 13.0; without, of 4-bit ones, which are walked two units a step, 777 8.6 and 8.0,
+// 1500 8.7 and 10.  Few: 100 keys 8.5 and 7.6.  Two CTAs an SM: 4 x 1500 with weights
+// 23.3 and 11.4.)
+inline int wide_cluster_of(const DecodeArgs& a, int heads, int most) {
+  const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
+  const int64_t units = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit;
+  int c = 8;
+  while (c > 1 && items * c > 152) c /= 2;
+  return items * c > 152 || units > (int64_t)c * kWideUnits || units <= 8 * kWarps * most ? 0 : c;
+}
 
 struct WsLayout { size_t prefix, ml, o, fin, scores, total; };
 inline WsLayout ws_layout(const DecodeArgs& a, int heads) {
@@ -1643,7 +1750,36 @@ inline int launch_failed(const char* what, cudaError_t err) {
   return set_error(ULYSSES_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(err));
 }
 
-template <class Engine, int D, int kCtas>
+template <class Kernel>
+int launch_cluster(Kernel kernel, int warps, int bytes, const DecodeArgs& a, const Plan& p, int c, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)c;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, a, p.groups, p.heads, c);
+  if (err != cudaSuccess) return launch_failed("attn_decode", err);
+  count_launch();
+  return ULYSSES_OK;
+}
+template <class Engine, int D, int kW, int kCtas>
+int run_cluster(const DecodeArgs& a, const Plan& p, int c, cudaStream_t st) {
+  constexpr int kSums = kW * (ring_bytes<Engine>() + Engine::kHeads * D * 4);
+  constexpr int kScores = Engine::kSeen ? kWideUnits * kUnit * 4 : 0;   // bytes of a head
+  const auto kernel = decode_wide_cluster_kernel<Engine, D, kW, kCtas>;
+  static PerDeviceOnce<> once;
+  if (const int rc = opt_in_smem(once, (const void*)kernel, kSums + kScores * Engine::kHeads, "attn_decode")) return rc;
+  return launch_cluster(kernel, kW, kSums + kScores * p.heads, a, p, c, st);
+}
+
+// kEight: clusters may have eight warps a CTA.
+template <class Engine, int D, int kCtas, bool kEight = Engine::kSeen || (ring_bytes<Engine>() > 0)>
 int run(const DecodeArgs& a, cudaStream_t st) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -1655,26 +1791,13 @@ int run(const DecodeArgs& a, cudaStream_t st) {
   p.groups = (a.G + p.heads - 1) / p.heads;
   p.warps = ctas * kWarps;
   if (const int c = cluster_of(a, p.heads)) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.B * a.H_kv * p.groups * c));
-    cfg.blockDim = dim3(kWarps * 32);
-    constexpr int kScores = Engine::kSeen ? kClusterUnits * kUnit * 4 : 0;   // bytes of a head, in a warp
-    cfg.dynamicSmemBytes = kWarps * (ring_bytes<Engine>() + kScores * p.heads);
-    cfg.stream = st;
-    if (constexpr int kMost = kWarps * (ring_bytes<Engine>() + kScores * Engine::kHeads)) {
-      static PerDeviceOnce<> once;
-      if (const int rc = opt_in_smem(once, (const void*)decode_cluster_kernel<Engine, D, kCtas>, kMost, "attn_decode")) return rc;
+    if constexpr (Engine::kSeen || ring_bytes<Engine>() > 0) {
+      if constexpr (kEight)
+        if (const int wide = wide_cluster_of(a, p.heads, Engine::kSeen ? 1 : 2)) return run_cluster<Engine, D, 8, 1>(a, p, wide, st);
+      return run_cluster<Engine, D, kWarps, kCtas < 3 ? kCtas : 2>(a, p, c, st);
+    } else {
+      return launch_cluster(decode_cluster_kernel<Engine, D, kCtas>, kWarps, 0, a, p, c, st);
     }
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)c;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, decode_cluster_kernel<Engine, D, kCtas>, a, p.groups, p.heads, c);
-    if (err != cudaSuccess) return launch_failed("attn_decode", err);
-    count_launch();
-    return ULYSSES_OK;
   }
   const WsLayout w = ws_layout(a, p.heads);
   char* ws = (char*)a.ws;
@@ -1756,9 +1879,9 @@ int run_matrix(const DecodeArgs& a, cudaStream_t st) {
 }
 template <typename TQ, typename TC, int D, bool kSeen>
 int run_simt(const DecodeArgs& a, cudaStream_t st) {
-  if (a.G == 1) return run<SimtEngine<TQ, TC, D, 1, kSeen>, D, 4>(a, st);
-  if (a.G <= 3) return run<SimtEngine<TQ, TC, D, 2, kSeen>, D, 3>(a, st);
-  return run<SimtEngine<TQ, TC, D, 4, kSeen>, D, 2>(a, st);
+  if (a.G == 1) return run<SimtEngine<TQ, TC, D, 1, kSeen>, D, 4, false>(a, st);
+  if (a.G <= 3) return run<SimtEngine<TQ, TC, D, 2, kSeen>, D, 3, false>(a, st);
+  return run<SimtEngine<TQ, TC, D, 4, kSeen>, D, 2, false>(a, st);
 }
 
 template <bool kQuant, int D, bool kSeen>

@@ -281,6 +281,9 @@ DECODES = [  # lens, Hq, H, D, page, dtype, layout
     ([1200, 64, 0, 65], 6, 2, 64, 64, "fp32", "seq"),
     ([1200, 64, 0, 65], 16, 1, 128, 256, "fp32", "seq"),
     ([2500], 8, 2, 128, 64, "bf16", "head"),
+    ([1025, 1, 0, 1040], 32, 8, 64, 16, "bf16", "seq"),           # eight warps a CTA, of four CTAs
+    ([2047, 1031], 32, 2, 128, 64, "bf16", "head"),
+    ([8100], 12, 2, 64, 16, "bf16", "seq"),
 ]
 
 

@@ -14,7 +14,7 @@ import torch
 from long_context_sequence_seq_gb300 import ulysses as U
 from oracle import serving_oracle as so
 
-from tests.test_gpu_4bit import build4
+from tests.test_gpu_4bit import build4, check4
 from tests.test_gpu_decode import build, check, f64, widen
 
 pytestmark = pytest.mark.gpu
@@ -70,6 +70,11 @@ CASES = [  # lens, Hq, H, D, page, dtype, cache, layout
     ([700, 100], 20, 1, 128, 16, "fp32", "e2m1", "seq"),         # three
     ([900, 31], 3, 1, 64, 16, "fp32", "e4m3", "seq"),
     ([900, 31], 1, 1, 128, 16, "fp32", "fp32", "seq"),
+    ([4099], 32, 8, 128, 16, "bf16", "bf16", "head"),            # eight warps a CTA: eight CTAs,
+    ([2047, 2033], 64, 4, 128, 64, "bf16", "e2m1", "seq"),       # 16 heads a kv head
+    ([1000, 0, 900, 512, 1], 24, 4, 64, 48, "bf16", "e4m3", "head"),   # four CTAs
+    ([1023, 800], 16, 2, 128, 32, "fp32", "fp32", "seq"),
+    ([500 + 13 * i for i in range(20)], 8, 8, 128, 16, "bf16", "bf16", "seq"),   # too many for eight warps: one CTA of four
 ]
 
 
@@ -85,12 +90,13 @@ def test_weights(case, wide):
     o, lse = U.attn_decode(weights=w, **args)
     U.check()
     check_weights(w, before, args, rows)
-    # the outputs beside them are the plain call's: the same kernels, unless a kv head has several groups of heads
-    # (the plain call of a narrow table then takes clusters, which add pieces up in another order)
+    # the outputs beside them: the plain call's (a narrow table's clusters add pieces up in another order)
     po, pl = U.attn_decode(**args)
-    if wide or Hq // H <= (16 if dtype == "bf16" else 8):
+    if wide:
         assert torch.equal(o, po) and torch.equal(lse, pl)
-    elif cache != "e2m1":
+    elif cache == "e2m1":
+        check4(o, lse, rows, build4(lens, Hq, H, D, page, dtype, layout, seed=case)[2], dtype, layout)
+    else:
         check(o, lse, rows, dtype, cache, layout)
     # and again on top, with a workspace of the caller's
     ws = U.attn_decode_workspace(args["q"], args["k_cache"], args["page_table"], layout=layout, weights=True)
