@@ -8,14 +8,19 @@
 // m on are left as they were.
 //
 // Two kernels.  The first selects: a cluster of CTAs for each (sequence, kv head)
-// finds the smallest weight that stays by its bits, three digits from the top, each
-// from a histogram over the cluster, and writes the list of the rows that stay.
-// Weights are ordered as unsigned numbers (sign and magnitude made monotone; -0 as
-// +0, NaN above everything).  Up to 16384 positions a CTA stay in registers from
-// digit to digit.  Bound by latencies: launch, lengths, table, weights, and about
-// 1.5 us a digit (10 us for a few positions, 25 for 131072 in 8 CTAs a head, of
-// which 2.5 would be reading them).  Where at most 32 positions are left to choose
-// from, they are put in order one against the other instead.
+// finds the smallest weight that stays by its bits, three digits from the top (10,
+// 11 and 11 bits), each from a histogram over the cluster, and writes the list of
+// the rows that stay.  Weights are ordered as unsigned numbers (sign and magnitude
+// made monotone; -0 as +0, NaN above everything).  Up to 16384 positions a CTA stay
+// in shared memory from digit to digit.  Bound by latencies: launch, lengths,
+// table, weights, and 2 us a digit, of which the largest is counting (the hardware
+// adds to one word at a time; neighbouring lanes therefore have counts of their own
+// in the first digit, where weights lie in few bins).  4160 positions of 128 heads
+// take 12 us, 131072 of 8 in 8 CTAs each 23, of which 2.5 would be reading them.
+// Loops are kept rolled and everything twice needed has one place: a launch runs
+// each instruction a few times, and fetching them is what it waited for (16 weights
+// in registers, each step written out: 16 and 25 us).  A warp writes the rows of two
+// units side by side (each lane its own unit's, 128 bytes apart: 2 us more).
 //
 // The second moves rows, in place: a chunk of rows, K, V, scales and weights, is
 // read into shared memory and then written.  A row never moves up, so what a chunk
@@ -48,7 +53,8 @@ constexpr int kUnit = 16;          // positions of one thread at a time
 constexpr int kThreads = 512;      // of a selecting CTA
 constexpr int kMoveThreads = 256;  // that move rows, of a CTA
 constexpr int kMaxBatch = 2048;    // sequences of one launch (their prefix sums sit in shared memory)
-constexpr int kBins = 2048;        // of a digit of 11 bits
+constexpr int kBins = 4096;        // counts of a digit: 1024 of 10 bits by four neighbours, 2048 of 11 by two
+constexpr int kMaxCtas = 8;        // of a cluster
 
 // What the selection leaves for the move (workspace).
 struct Lists {
@@ -82,25 +88,24 @@ __device__ __forceinline__ Size size_of(const EvictArgs& a, int b) {
   return Size{n, m, min(m, a.recent)};
 }
 
-// The orders of the 16 weights of unit `unit` of a sequence's head.
-__device__ __forceinline__ void load_unit(const EvictArgs& a, const int32_t* row, int h, int unit, uint32_t (&key)[kUnit]) {
-  const int per = a.page / kUnit, col = unit / per;
-  const int64_t at = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (unit - col * per) * kUnit;
-  const float4* p = reinterpret_cast<const float4*>(a.w + at);
-  if (!in_bounds(at, a.num_pages * a.H * a.page)) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = p[i];
-    key[4 * i] = order_of(v.x); key[4 * i + 1] = order_of(v.y); key[4 * i + 2] = order_of(v.z); key[4 * i + 3] = order_of(v.w);
-  }
-}
-
-__device__ __forceinline__ int ld_cluster(uint32_t at, int rank) {
+__device__ __forceinline__ int ld_cluster(const int* at, int rank) {   // `at` in this CTA's shared memory
   uint32_t p;
   int v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(at), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(tc::smem_u32(at)), "r"(rank));
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
   return v;
+}
+__device__ __forceinline__ int4 ld_cluster4(const int* at, int rank) {
+  uint32_t p;
+  int4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(tc::smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+
+// Of the CTA `rank`, or of the one CTA.
+__device__ __forceinline__ int4 ld4(const int* at, int rank, int ctas) {
+  return ctas > 1 ? ld_cluster4(at, rank) : *reinterpret_cast<const int4*>(at);
 }
 
 // Inclusive sums over the block's threads; `sums` holds a number for each warp.
@@ -134,70 +139,126 @@ __device__ __forceinline__ void sync_all(int ctas) {
     __syncthreads();
   }
 }
-// An int of every CTA's shared memory, at this CTA's address of it (0 of those there
-// are not); the loads do not wait for each other.
-constexpr int kMaxCtas = 8;
-__device__ __forceinline__ void ld_ranks(const int* p, int ctas, int (&v)[kMaxCtas]) {
+
+// Of 128 counts, four a lane, the one in which the k-th from the top lies (1 <= k
+// <= their sum), for all lanes: its number, how many lie above it and in it.
+struct Found { int at, above, count; };
+__device__ __forceinline__ Found find(int4 n, int k) {
+  const int lane = threadIdx.x & 31, own = n.x + n.y + n.z + n.w;
+  int upto = own;
 #pragma unroll
-  for (int c = 0; c < kMaxCtas; ++c) v[c] = c < ctas ? ld_cluster(tc::smem_u32(p), c) : 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_down_sync(0xffffffffu, upto, o);
+    if (lane + o < 32) upto += y;
+  }
+  Found f{4 * lane + 3, upto - own, n.w};
+  if (f.above + f.count < k) { --f.at; f.above += f.count; f.count = n.z; }
+  if (f.above + f.count < k) { --f.at; f.above += f.count; f.count = n.y; }
+  if (f.above + f.count < k) { --f.at; f.above += f.count; f.count = n.x; }
+  const int from = __ffs(__ballot_sync(0xffffffffu, upto >= k && upto - own < k)) - 1;
+  f.at = __shfl_sync(0xffffffffu, f.at, from);
+  f.above = __shfl_sync(0xffffffffu, f.above, from);
+  f.count = __shfl_sync(0xffffffffu, f.count, from);
+  return f;
 }
 
-// Units a thread holds in registers from one digit to the next; those of longer
-// sequences are loaded again (from L2).
-constexpr int kHold = 2;
+// Units of a thread that have a place in shared memory.  A CTA's positions stay
+// there from digit to digit where that is enough; else they come again for each
+// digit (from L2), one unit ahead.
+constexpr int kSlots = 2;
+constexpr int kSlotB = kThreads * kUnit * 4;
 
 __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ EvictArgs a,
-                                                                const __grid_constant__ Lists l, int ctas) {
-  __shared__ int hist[kBins];
-  __shared__ int part[kBins];                              // totals over the cluster, of this CTA's bins
-  __shared__ int part_sum[3];                              // theirs, for each digit
+                                                                   const __grid_constant__ Lists l, int ctas) {
+  extern __shared__ __align__(16) uint4 slots[];           // [slot][thread][4]: weights, then their orders
+  __shared__ __align__(16) int hist[kBins];
+  __shared__ __align__(16) int part[kBins / 2];            // totals over the cluster, of this CTA's bins
+  __shared__ __align__(16) int group[16];                  // and of a 16th of them each
   __shared__ int sums[kThreads / 32];
-  __shared__ int found[3];                                 // the digit, the positions in the digits above it, in it
   __shared__ int mine[2];                                  // of this CTA's positions: above the threshold, at it
-  __shared__ int few;                                      // positions left to choose from, when they are few: how many
-  __shared__ int few_key[32], few_at[32];                  // of this CTA's, their orders and places
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0, item = blockIdx.x / ctas;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0, lg = __ffs(ctas) - 1, item = blockIdx.x >> lg;
   const int b = item / a.H, h = item - b * a.H;
   const int32_t* row = a.table + (int64_t)b * a.cols;
-  int page = (int)threadIdx.x < a.cols ? __ldg(row + threadIdx.x) : 0;   // on its way beside the lengths
+  int page[4];                                             // on their way beside the lengths
+#pragma unroll
+  for (int i = 0; i < 4; ++i) page[i] = tid + i * kThreads < a.cols ? __ldg(row + tid + i * kThreads) : 0;
   Size z = size_of(a, b);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *l.ticket = 0;
+  if (blockIdx.x == 0 && tid == 0) *l.ticket = 0;
+  static_assert(kBins == 8 * kThreads, "");
+  reinterpret_cast<int4*>(hist)[2 * tid] = reinterpret_cast<int4*>(hist)[2 * tid + 1] = make_int4(0, 0, 0, 0);
+  if (tid < 2) mine[tid] = 0;
   // a page out of range: the sequence is left as it is, all of its heads (each looks at the whole row)
   int bad = 0;
-  if (z.m < z.n)
-    for (int c = threadIdx.x, last = (z.n - 1) / a.page; c <= last; c += kThreads) {
-      bad |= (unsigned)page >= (unsigned)a.num_pages;
-      if (c + kThreads <= last) page = __ldg(row + c + kThreads);
-    }
-  for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
-  if (threadIdx.x < 2) mine[threadIdx.x] = 0;
-  if (threadIdx.x == 0) few = 0;
-  if (threadIdx.x < 3) part_sum[threadIdx.x] = 0;
+  if (z.m < z.n) {
+    const int last = (z.n - 1) / a.page;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= tid + i * kThreads <= last && (unsigned)page[i] >= (unsigned)a.num_pages;
+    for (int c = tid + 4 * kThreads; c <= last; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
+  }
   if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) raise_error(kErrPages);
+    if (tid == 0) raise_error(kErrPages);
     z.m = z.n;
   }
-  if (h == 0 && rank == 0 && threadIdx.x == 0) l.size[b] = make_int2(z.n, z.m);
+  if (h == 0 && rank == 0 && tid == 0) l.size[b] = make_int2(z.n, z.m);
   if (z.m >= z.n) return;                                  // the whole cluster
+
   int64_t* src = l.src + item * l.positions;
   int* before = l.before + item * l.chunks;
   const int old = z.n - z.r, k = z.m - z.r;                // k of `old` positions stay
-  for (int i = rank * kThreads + threadIdx.x; i < (z.m + l.chunk - 1) / l.chunk; i += ctas * kThreads) l.read[item * l.chunks + i] = 0;
-  for (int i = rank * kThreads + threadIdx.x; i < z.r; i += ctas * kThreads) {
-    const int p = old + i, col = p / a.page;
-    src[k + i] = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (p - col * a.page);
-  }
-  const int units = (old + kUnit - 1) / kUnit, each = (units + ctas - 1) / ctas;
+  const int units = (old + kUnit - 1) / kUnit, each = (units + ctas - 1) >> lg;
   const int u0 = min(rank * each, units), u1 = min(u0 + each, units);
-  uint32_t held[kHold][kUnit];
+  const int rounds = (u1 - u0 + kThreads - 1) / kThreads;  // units of a thread, at most
+  const bool all = rounds <= kSlots;
+  // the thread's `r`-th unit and its place in shared memory, where nobody else looks (16-byte words change places
+  // so that no bank is met twice)
+  const auto unit_of = [&](int r) { return u0 + r * kThreads + tid; };
+  const auto row_of = [&](int p) {                         // of position p
+    const int col = p / a.page;
+    return ((int64_t)__ldg(row + col) * a.H + h) * a.page + (p - col * a.page);
+  };
+  const auto place = [&](int i) { return slots + (i * kThreads + tid) * 4; };
+  const auto fetch = [&](int r, int i) {
+    const int u = unit_of(r);
+    if (u < u1) {
+      const int64_t at = row_of(u * kUnit);
+      const uint32_t to = tc::smem_u32(place(i));
+      if (in_bounds(at, a.num_pages * a.H * a.page)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + (j ^ (tid >> 1 & 3)) * 16), "l"(a.w + at + 4 * j) : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // the r-th unit's place, when its weights are there and (round about) the next one's on their way
+  int turn = 0;
+  const auto arrived = [&](int r) {
+    if (all) return place(r);
+    fetch(r + 1 < rounds ? r + 1 : 0, (turn + 1) & 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    return place(turn++ & 1);
+  };
+  // the orders of four of the unit's weights; `raw`: they are weights yet.  Places behind the last get 0, which is no
+  // weight's order
+  const auto four = [&](const uint4* slot, int j, int u, bool raw) {
+    uint4 x = slot[j ^ (tid >> 1 & 3)];
+    if (raw) {
+      const int live = old - u * kUnit - 4 * j;
+      x.x = live > 0 ? order_of(__uint_as_float(x.x)) : 0; x.y = live > 1 ? order_of(__uint_as_float(x.y)) : 0;
+      x.z = live > 2 ? order_of(__uint_as_float(x.z)) : 0; x.w = live > 3 ? order_of(__uint_as_float(x.w)) : 0;
+    }
+    return x;
+  };
   if (k > 0) {
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int u = u0 + i * kThreads + threadIdx.x;
-      if (u < u1) load_unit(a, row, h, u, held[i]);
-    }
+    for (int r = 0; r < kSlots; ++r)
+      if (r < (all ? rounds : 1)) fetch(r, r);
   }
+  for (int i = rank * kThreads + tid; i < (z.m + l.chunk - 1) / l.chunk; i += ctas * kThreads) l.read[item * l.chunks + i] = 0;
+  for (int i = rank * kThreads + tid; i < z.r; i += ctas * kThreads) src[k + i] = row_of(old + i);
+  if (all) asm volatile("cp.async.wait_all;" ::: "memory");
 
   // the threshold, digit by digit: `prefix` holds the bits found, k_left of the
   // positions that have them are to stay
@@ -206,237 +267,148 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   if (k > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-      auto count_unit = [&](const uint32_t (&key)[kUnit], int u) {
-        const int live = old - u * kUnit;
-        if (pass > 0) {                                    // few: those with the digits found so far
-          uint32_t some = 0;
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) some |= (uint32_t)(key[i] >> (shift + bits) == prefix) << i;
-          if (live < kUnit) some &= (1u << live) - 1;
-          if (!some) return;
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i)
-            if (some >> i & 1) atomicAdd(hist + ((key[i] >> shift) & ((1 << bits) - 1)), 1);
-          return;
+      // bins lie 2^fold apart, and neighbouring lanes count in places of their own
+      const int shift = pass == 0 ? 22 : (pass == 1 ? 11 : 0), bits = pass == 0 ? 10 : 11, fold = pass == 0 ? 2 : 1;
+      int* const own = hist + (tid & ((1 << fold) - 1));
+#pragma unroll 1
+      for (int r = 0; r < rounds; ++r) {
+        uint4* const slot = arrived(r);
+        const int u = unit_of(r);
+        if (u >= u1) continue;
+#pragma unroll 2
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = four(slot, j, u, pass == 0 || !all);
+          if (pass == 0 && all) slot[j ^ (tid >> 1 & 3)] = x;
+          // those with the digits found so far; four of one bin are counted together: tokens nobody looked at are alike
+          const uint32_t top = pass == 0 ? 0 : 0xffffffffu << (shift + bits), want = pass == 0 ? 0 : prefix << (shift + bits);
+          const bool in[4] = {(x.x & top) == want, (x.y & top) == want, (x.z & top) == want, (x.w & top) == want};
+          if (!(in[0] || in[1] || in[2] || in[3])) continue;
+          const uint32_t mask = (1u << bits) - 1, d = x.x >> shift & mask;
+          if (x.x >> shift == x.y >> shift && x.x >> shift == x.z >> shift && x.x >> shift == x.w >> shift) {
+            atomicAdd(own + (d << fold), 4);
+          } else {
+            if (in[0]) atomicAdd(own + (d << fold), 1);
+            if (in[1]) atomicAdd(own + ((x.y >> shift & mask) << fold), 1);
+            if (in[2]) atomicAdd(own + ((x.z >> shift & mask) << fold), 1);
+            if (in[3]) atomicAdd(own + ((x.w >> shift & mask) << fold), 1);
+          }
         }
-        // neighbours of one bin are counted together: tokens nobody looked at are alike
-        int bin = -1, count = 0;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          if (i >= live) continue;
-          const int d = (int)(key[i] >> shift);
-          if (d == bin) { ++count; continue; }
-          if (count) atomicAdd(hist + bin, count);
-          bin = d;
-          count = 1;
-        }
-        if (count) atomicAdd(hist + bin, count);
-      };
-#pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const int u = u0 + i * kThreads + threadIdx.x;
-        if (u < u1) count_unit(held[i], u);
-      }
-      for (int u = u0 + kHold * kThreads + threadIdx.x; u < u1; u += kThreads) {
-        uint32_t key[kUnit];
-        load_unit(a, row, h, u, key);
-        count_unit(key, u);
       }
       sync_all(ctas);
-      const int share = kBins / ctas;
-      int above = 0, owner = 0, sum = 0, total;
-      if (ctas > 1) {
-        // each CTA adds up its share of the bins over the cluster ..
-        for (int i = threadIdx.x; i < share; i += kThreads) {
-          int v[kMaxCtas], n = 0;
-          ld_ranks(hist + rank * share + i, ctas, v);
+      // each CTA adds up its share of the counts over the cluster, four of them a thread (eight where it is alone) ..
+      const int share = kBins >> lg, wide = ctas == 1 ? 5 : 6 - lg;   // 2^wide threads of a 16th
+      int sum = 0;
+      const auto add = [&](int i, int4 v) {
+        const int lo = v.x + v.y, hi = v.z + v.w;
+        if (fold == 2) part[i] = lo + hi;
+        else reinterpret_cast<int2*>(part)[i] = make_int2(lo, hi);
+        sum += lo + hi;
+      };
+      if (ctas == 1) {
+        add(2 * tid, reinterpret_cast<const int4*>(hist)[2 * tid]);
+        add(2 * tid + 1, reinterpret_cast<const int4*>(hist)[2 * tid + 1]);
+      } else if (4 * tid < share) {
+        int4 v[kMaxCtas];
 #pragma unroll
-          for (int c = 0; c < kMaxCtas; ++c) n += v[c];
-          part[i] = n;
-          sum += n;
+        for (int c = 0; c < kMaxCtas; ++c) v[c] = c < ctas ? ld_cluster4(hist + rank * share + 4 * tid, c) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 1; c < kMaxCtas; ++c) {
+          v[0].x += v[c].x; v[0].y += v[c].y; v[0].z += v[c].z; v[0].w += v[c].w;
         }
-        sum = __reduce_add_sync(0xffffffffu, sum);
-        if ((threadIdx.x & 31) == 0 && sum) atomicAdd(part_sum + pass, sum);
-        sync_all(ctas);
-        // .. all find the share that has the digit ..
-        int v[kMaxCtas];
-        ld_ranks(part_sum + pass, ctas, v);
-        bool passed = false;
-#pragma unroll
-        for (int c = kMaxCtas - 1; c >= 0; --c) {
-          if (!passed && (above + v[c] >= k_left || c == 0)) {
-            owner = c;
-            passed = true;
-          }
-          above += passed ? 0 : v[c];
-        }
+        add(tid, v[0]);
       }
-      // .. and the digit in it, from the top
-      constexpr int kOwn = kBins / kThreads;               // bins of a thread, at most
-      int n[kOwn];
-      sum = 0;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const int bin = share - 1 - ((int)threadIdx.x * kOwn + i);
-        n[i] = bin >= 0 ? (ctas > 1 ? ld_cluster(tc::smem_u32(part + bin), owner) : hist[bin]) : 0;
-        sum += n[i];
-      }
-      int upto = above + block_scan(sum, sums, total) - sum;   // positions in the bins above
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        if (upto < k_left && upto + n[i] >= k_left) {      // one thread, once
-          found[0] = owner * share + share - 1 - ((int)threadIdx.x * kOwn + i);
-          found[1] = upto;
-          found[2] = n[i];
-        }
-        upto += n[i];
-      }
-      __syncthreads();
-      const int digit = found[0];
-      k_left -= found[1];
+      for (int o = 1 << wide >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if ((tid & ((1 << wide) - 1)) == 0 && tid >> wide < 16) group[tid >> wide] = sum;
+      sync_all(ctas);
+      // .. and every warp finds the 16th of a share that has the digit, and the digit in it
+      const Found g = find(lane < 4 * ctas ? ld4(group + lane % 4 * 4, lane / 4, ctas) : make_int4(0, 0, 0, 0), k_left);
+      const int bins = (share >> fold) / 16, owner = min(g.at / 16, ctas - 1), first = g.at % 16 * bins;
+      const Found f = find(4 * lane < bins ? ld4(part + first + 4 * lane, owner, ctas) : make_int4(0, 0, 0, 0), k_left - g.above);
+      const int digit = owner * (share >> fold) + first + f.at;
+      k_left -= g.above + f.above;
       prefix = prefix << bits | (uint32_t)digit;
-      if (ctas > 1) {                                      // of this CTA's: those above, at last those at it
-        int own = 0;
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
-          own += i > digit ? hist[i] : 0;
-          if (i == digit && pass == 2) mine[1] = hist[i];
+      // this CTA's above it, at last those at it, and the counts cleared for the next digit
+      int4* const n = reinterpret_cast<int4*>(hist) + 2 * tid;
+      if (ctas > 1) {
+        int over = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int lo = n[i].x + n[i].y, hi = n[i].z + n[i].w, at = (8 * tid + 4 * i) >> fold, next = at + (fold == 1);
+          over += (at > digit ? lo : 0) + (next > digit ? hi : 0);
+          if (pass == 2 && at == digit) mine[1] = lo;
+          if (pass == 2 && next == digit) mine[1] = hi;
         }
-        own = __reduce_add_sync(0xffffffffu, own);
-        if ((threadIdx.x & 31) == 0 && own) atomicAdd(mine, own);
+        over = __reduce_add_sync(0xffffffffu, over);
+        if (lane == 0 && over) atomicAdd(mine, over);
       }
-      if (pass < 2 && found[2] <= 32) {
-        // few have the digits so far: they are put in order one against the other
-        auto keep_few = [&](const uint32_t (&key)[kUnit], int u) {
-          const int live = old - u * kUnit;
-          uint32_t some = 0;
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i) some |= (uint32_t)(i < live && key[i] >> shift == prefix) << i;
-          if (!some) return;
-          const int x = atomicAdd(&few, __popc(some));
-#pragma unroll
-          for (int i = 0; i < kUnit; ++i)
-            if (some >> i & 1) {
-              const int at = x + __popc(some & ((1u << i) - 1));
-              few_key[at] = (int)key[i];
-              few_at[at] = u * kUnit + i;
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-          const int u = u0 + i * kThreads + threadIdx.x;
-          if (u < u1) keep_few(held[i], u);
-        }
-        for (int u = u0 + kHold * kThreads + threadIdx.x; u < u1; u += kThreads) {
-          uint32_t key[kUnit];
-          load_unit(a, row, h, u, key);
-          keep_few(key, u);
-        }
-        sync_all(ctas);
-        if (threadIdx.x < 32) {
-          int v[kMaxCtas], at = threadIdx.x, owner = -1;   // lane i has the i-th of all CTAs'
-          if (ctas > 1) ld_ranks(&few, ctas, v);
-#pragma unroll
-          for (int c = 0; c < kMaxCtas; ++c) {
-            const int n = ctas > 1 ? v[c] : (c == 0 ? few : 0);
-            if (owner < 0) {
-              if (at < n) owner = c;
-              else at -= n;
-            }
-          }
-          uint32_t key = 0;
-          int place = 0, ahead = 0;
-          if (owner >= 0) {
-            key = (uint32_t)(ctas > 1 ? ld_cluster(tc::smem_u32(few_key + at), owner) : few_key[at]);
-            place = ctas > 1 ? ld_cluster(tc::smem_u32(few_at + at), owner) : few_at[at];
-          }
-          for (int i = 0; i < found[2]; ++i) {
-            const uint32_t other = __shfl_sync(0xffffffffu, key, i);
-            const int its = __shfl_sync(0xffffffffu, place, i);
-            ahead += other > key || (other == key && its < place);
-          }
-          const uint32_t last = __ballot_sync(0xffffffffu, owner >= 0 && ahead == k_left - 1);   // one lane: the last that stays
-          const uint32_t edge = __shfl_sync(0xffffffffu, key, __ffs(last) - 1);
-          const uint32_t over = __ballot_sync(0xffffffffu, owner >= 0 && key > edge);
-          const bool own = owner == rank;
-          const uint32_t own_over = __ballot_sync(0xffffffffu, own && key > edge), own_at = __ballot_sync(0xffffffffu, own && key == edge);
-          if (threadIdx.x == 0) {
-            found[0] = (int)edge;
-            found[1] = __popc(over);
-            if (ctas > 1) {
-              mine[0] += __popc(own_over);
-              mine[1] = __popc(own_at);
-            }
-          }
-        }
-        __syncthreads();
-        prefix = (uint32_t)found[0];
-        k_left -= found[1];
-        break;
-      }
-      if (pass < 2) {                                      // cleared for the next digit
-        for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
-        __syncthreads();
-      }
+      n[0] = n[1] = make_int4(0, 0, 0, 0);
+      __syncthreads();
     }
   }
   // positions that stay before this CTA's: those above the threshold and the first k_left at it
   int gt0 = 0, eq0 = 0;
   if (ctas > 1) {
-    __syncthreads();
     sync_all(ctas);
-    int g[kMaxCtas], e[kMaxCtas];
-    ld_ranks(mine, ctas, g);
-    ld_ranks(mine + 1, ctas, e);
-#pragma unroll
-    for (int c = 0; c < kMaxCtas; ++c) {
-      gt0 += c < rank ? g[c] : 0;
-      eq0 += c < rank ? e[c] : 0;
+    int g = 0, e = 0;
+    if (lane < rank) {
+      g = ld_cluster(mine, lane);
+      e = ld_cluster(mine + 1, lane);
     }
+    gt0 = __reduce_add_sync(0xffffffffu, g);
+    eq0 = __reduce_add_sync(0xffffffffu, e);
+    // no CTA leaves while another reads its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
-  auto list_units = [&](const uint32_t (&key)[kUnit], int u) {
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    const int u = unit_of(r);
     uint32_t gt = 0, eq = 0;                               // a bit a position
-    if (u < u1 && k > 0) {
-      const int live = old - u * kUnit;
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        gt |= (uint32_t)(i < live && key[i] > prefix) << i;
-        eq |= (uint32_t)(i < live && key[i] == prefix) << i;
+    if (k > 0) {
+      const uint4* slot = arrived(r);
+      if (u < u1) {
+#pragma unroll 2
+        for (int j = 0; j < 4; ++j) {
+          const uint4 x = four(slot, j, u, !all);
+          gt |= ((x.x > prefix) + 2 * (x.y > prefix) + 4 * (x.z > prefix) + 8 * (x.w > prefix)) << 4 * j;
+          eq |= ((x.x == prefix) + 2 * (x.y == prefix) + 4 * (x.z == prefix) + 8 * (x.w == prefix)) << 4 * j;
+        }
       }
     }
+    const int first = gt | eq ? (int)(row_of(u * kUnit) / kUnit) : 0;   // the unit's rows (of 36 bytes or more: 31 bits)
     int total;
     const int counts = __popc(gt) | __popc(eq) << 16;      // at most 8192 of each
     const int upto = block_scan(counts, sums, total) - counts;
     const int g = gt0 + (upto & 0xffff), e = eq0 + (upto >> 16);
+    int at = 0;
+    uint32_t stay = 0;
     if (u < u1) {
-      const int at = g + min(e, k_left);
-      if ((u * kUnit & (l.chunk - 1)) == 0) before[u * kUnit / l.chunk] = at;
+      at = g + min(e, k_left);
+      if ((u * kUnit & (l.chunk - 1)) == 0) before[u * kUnit >> (__ffs(l.chunk) - 1)] = at;
       // the first of those at it, as many as are left
       for (int over = __popc(eq) - max(k_left - e, 0); over > 0; --over) eq &= ~(0x80000000u >> __clz(eq));
-      const uint32_t stay = gt | eq;
-      if (stay) {
-        const int per = a.page / kUnit, col = u / per;
-        const int64_t first = ((int64_t)__ldg(row + col) * a.H + h) * a.page + (u - col * per) * kUnit;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          const int to = at + __popc(stay & ((1u << i) - 1));
-          if ((stay >> i & 1) && in_bounds(to, k)) src[to] = first + i;
-        }
+      stay = gt | eq;
+    }
+    if (__reduce_max_sync(0xffffffffu, __popc(stay)) <= 4) {
+#pragma unroll 1
+      for (; stay && at < k; stay &= stay - 1, ++at) src[at] = (int64_t)first * kUnit + __ffs(stay) - 1;
+    } else {                                               // many: the rows of two units at a time, side by side
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 2) {
+        const int from = i + (lane >> 4), bit = lane & 15;
+        const uint32_t its = __shfl_sync(0xffffffffu, stay, from);
+        const int to = __shfl_sync(0xffffffffu, at, from) + __popc(its & ((1u << bit) - 1));
+        const int its_first = __shfl_sync(0xffffffffu, first, from);
+        if ((its >> bit & 1) && to < k) src[to] = (int64_t)its_first * kUnit + bit;
       }
     }
     gt0 += total & 0xffff;
     eq0 += total >> 16;
-  };
-#pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (u0 + i * kThreads < u1) list_units(held[i], u0 + i * kThreads + threadIdx.x);
-  for (int t = u0 + kHold * kThreads; t < u1; t += kThreads) {
-    uint32_t key[kUnit];
-    const int u = t + threadIdx.x;
-    if (u < u1 && k > 0) load_unit(a, row, h, u, key);
-    list_units(key, u);
   }
-  if (ctas > 1) sync_all(ctas);                            // no CTA leaves while another reads its shared memory
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (ctas > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 }
 
 // Where a chunk's rows are and where they go; -1: a row that does not move.
@@ -811,9 +783,14 @@ int launch_evict(const EvictArgs& a, cudaStream_t st) {
     x.keep = a.keep + b0;
     x.out = a.out + b0;
     const int c = cluster_of(x);
+    static PerDeviceOnce<> once;
+    if (const int rc = opt_in_smem(once, (const void*)evict_select_kernel, kSlots * kSlotB, "cache_evict")) return rc;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)x.B * x.H * c));
     cfg.blockDim = dim3(kThreads);
+    // places for the units of a full table, as far as there are any
+    const int64_t each = ((int64_t)x.cols * x.page / kUnit + c - 1) / c, rounds = (each + kThreads - 1) / kThreads;
+    cfg.dynamicSmemBytes = (size_t)(rounds < kSlots ? rounds : kSlots) * kSlotB;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -136,6 +136,14 @@ def test_long_sequences(n, keep, recent, H, held):
     run(make([n], H, 64, 64, held, seed=n), [n], [keep], recent)
 
 
+@pytest.mark.parametrize("kind", ["equal", "any"])
+@pytest.mark.parametrize("lens,keep,H", [([140001], 70000, 2), ([263001], 512, 1), ([20000] * 19 + [300], 1500, 8),
+                                         ([9001] * 9 + [16400], 8192, 8), ([20000, 0, 33001, 513, 4096], 2047, 8)])
+def test_selections_of_every_width(lens, keep, H, kind):
+    """CTAs that hold their weights from digit to digit and CTAs that read them again; one, two, four and eight of them."""
+    run(make(lens, H, 64, 64, "e2m1", seed=len(lens), kind=kind), lens, [keep] * len(lens), 100)
+
+
 def test_many_sequences():
     lens = [(37 * i) % 300 for i in range(400)]
     keep = [(11 * i) % 200 for i in range(400)]
