@@ -31,8 +31,8 @@
 // takes each item and joins through distributed shared memory: one launch.
 // With weights (kSeen) the engines keep each key's scores, and once the heads'
 // maxima and sums are final a pass over the scores adds exp2(s - m) / l to the
-// keys' slots: in the cluster from shared memory (at 500 to 8000 keys no slower than
-// without), else in a third kernel from the workspace.  Scores and not weights
+// keys' slots: in the cluster from shared memory (500 bf16 keys 9.5 us and 8.7 without,
+// 4099 12.9 and 13.5), else in a third kernel from the workspace.  Scores and not weights
 // are kept, because a weight's maximum and sum are known last; recomputing the
 // scores would read K again, 128 bytes a key in e4m3 and D = 128 against 32.
 //
