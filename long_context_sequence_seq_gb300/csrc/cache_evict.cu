@@ -720,7 +720,9 @@ WsLayout ws_layout(const EvictArgs& a) {
 }
 
 // CTAs of a cluster for each (sequence, kv head): a unit a thread where two CTAs an
-// SM allow it.
+// SM allow it.  (Four and eight an SM: 64 ragged sequences of up to 16384 positions,
+// 8 heads, 246 and 265 us where this takes 238, 16 of 40000 207 and 207 where it
+// takes 181; a CTA for each head: 1 x 131072 positions 126 where it takes 35.)
 int cluster_of(const EvictArgs& a) {
   int c = 1;
   while (c < kMaxCtas && (int64_t)a.cols * a.page > (int64_t)c * kThreads * kUnit && (int64_t)a.B * a.H * c * 2 <= 152 * 2) c *= 2;
