@@ -1722,11 +1722,12 @@ inline int cluster_of(const DecodeArgs& a, int heads) {
 // 1000 bf16 keys 9.4 and 10.7 us, 1000 4-bit ones 9.6 and 10.7, 4 x 1500 bf16 11.4 and
 // 13.0; without, of 4-bit ones, which are walked two units a step, 777 8.6 and 8.0,
 // 1500 8.7 and 10.  Few: 100 keys 8.5 and 7.6.  Two CTAs an SM: 4 x 1500 with weights
-// 23.3 and 11.4.)
+// 23.3 and 11.4.)  16 clusters of eight CTAs run at once, and not 19, as a GPC's SMs are
+// no multiple of eight: 3 x 1500 of 6 kv heads with weights 17.4 us, 11.6 in fours.
 inline int wide_cluster_of(const DecodeArgs& a, int heads, int most) {
   const int64_t items = (int64_t)a.B * a.H_kv * ((a.G + heads - 1) / heads);
   const int64_t units = ((int64_t)a.cols * a.page + kUnit - 1) / kUnit;
-  int c = 8;
+  int c = items > 16 ? 4 : 8;
   while (c > 1 && items * c > 152) c /= 2;
   return items * c > 152 || units > (int64_t)c * kWideUnits || units <= 8 * kWarps * most ? 0 : c;
 }
