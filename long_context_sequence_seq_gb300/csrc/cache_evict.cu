@@ -75,17 +75,18 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-struct Size { int n, m, r; };
-// Tokens, those that stay, those of them that stay for their age.  A length that
-// the table cannot hold is reported, and such a sequence is left as it is.
+struct Size { int n, m, r, pages; };
+// Tokens, those that stay, those of them that stay for their age, pages that hold
+// them.  A length that the table cannot hold is reported, and such a sequence is left
+// as it is (none of its pages is looked up).
 __device__ __forceinline__ Size size_of(const EvictArgs& a, int b) {
   const int n = __ldg(a.lens + b), keep = __ldg(a.keep + b);
   if (n < 0 || n > (int64_t)a.cols * a.page) {
     raise_error(kErrPages);
-    return Size{n, n, 0};
+    return Size{n, n, 0, 0};
   }
   const int m = keep < 0 || keep > n ? n : keep;
-  return Size{n, m, min(m, a.recent)};
+  return Size{n, m, min(m, a.recent), (n + a.page - 1) / a.page};
 }
 
 __device__ __forceinline__ int ld_cluster(const int* at, int rank) {   // `at` in this CTA's shared memory
@@ -189,14 +190,12 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   static_assert(kBins == 8 * kThreads, "");
   reinterpret_cast<int4*>(hist)[2 * tid] = reinterpret_cast<int4*>(hist)[2 * tid + 1] = make_int4(0, 0, 0, 0);
   if (tid < 2) mine[tid] = 0;
-  // a page out of range: the sequence is left as it is, all of its heads (each looks at the whole row)
+  // a page out of range: the sequence is left as it is, all of its heads (each looks at the whole row); where all
+  // tokens stay anyway it is reported all the same
   int bad = 0;
-  if (z.m < z.n) {
-    const int last = (z.n - 1) / a.page;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bad |= tid + i * kThreads <= last && (unsigned)page[i] >= (unsigned)a.num_pages;
-    for (int c = tid + 4 * kThreads; c <= last; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
-  }
+  for (int i = 0; i < 4; ++i) bad |= tid + i * kThreads < z.pages && (unsigned)page[i] >= (unsigned)a.num_pages;
+  for (int c = tid + 4 * kThreads; c < z.pages; c += kThreads) bad |= (unsigned)__ldg(row + c) >= (unsigned)a.num_pages;
   if (__syncthreads_or(bad)) {
     if (tid == 0) raise_error(kErrPages);
     z.m = z.n;
