@@ -491,9 +491,10 @@ int ulysses_attn_decode_weights(const void* q, int64_t q_b, int64_t q_h, const v
  * left as they were, and pages that hold none below m are the caller's again.
  *   weights   [num_pages][H_kv][page_size] fp32, 16-byte aligned
  *   keep      [B] int32, device;  recent >= 0
- *   new_lens  [B] int32, device, written: m (may be seq_lens)
+ *   new_lens  [B] int32, device, written: m (may be seq_lens or keep)
  *   workspace >= ulysses_cache_evict_workspace() bytes, 256-byte aligned,
  *        contents need no init; calls that share one must not overlap on the GPU
+ * new_lens and the workspace lie apart from each other and from all other buffers.
  * The sequences of a call must not share pages, and a sequence's pages must be
  * distinct.  A sequence whose length does not fit the table, or that has a page
  * id outside [0, num_pages) below its length, is left as it is (new_lens its

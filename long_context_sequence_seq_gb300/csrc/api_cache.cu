@@ -457,6 +457,21 @@ int ulysses_cache_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   const size_t need = evict_workspace(a);
   if (ws_bytes < need || !workspace) return set_error(ULYSSES_ERR_INVALID, "workspace too small: %zu < %zu", ws_bytes, need);
   if (((uintptr_t)workspace & 255u) != 0) return set_error(ULYSSES_ERR_INVALID, "workspace must be 256-byte aligned");
+  // what is written apart from all that is read: a launch takes some of the sequences, so new lengths may stand in
+  // the place of the old ones (or of the budgets) entry by entry alone
+  const char *ws = (const char*)workspace, *out = (const char*)new_lens;
+  const size_t per_seq = (size_t)B * 4;
+  const struct { const void* p; size_t n; bool in_place; } held[] = {
+      {k_cache, cb, false}, {v_cache, cb, false}, {k_scale, k_scale ? rows * 4 : 0, false},
+      {v_scale, v_scale ? rows * 4 : 0, false}, {weights, rows * 4, false}, {page_table, per_seq * table_cols, false},
+      {seq_lens, per_seq, true}, {keep, per_seq, true}};
+  if (overlap(out, per_seq, ws, need)) return set_error(ULYSSES_ERR_INVALID, "the workspace overlaps new_lens");
+  for (const auto& x : held) {
+    if (x.n && overlap((const char*)x.p, x.n, ws, need))
+      return set_error(ULYSSES_ERR_INVALID, "the workspace must not overlap the call's other buffers");
+    if (x.n && !(x.in_place && x.p == new_lens) && overlap((const char*)x.p, x.n, out, per_seq))
+      return set_error(ULYSSES_ERR_INVALID, "new_lens must lie apart from the call's other buffers, or be seq_lens or keep");
+  }
   a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale; a.w = weights;
   a.table = page_table; a.lens = seq_lens; a.keep = keep; a.out = new_lens;
   a.num_pages = num_pages; a.D = D; a.cache_dtype = cache_dtype; a.recent = recent; a.ws = workspace;

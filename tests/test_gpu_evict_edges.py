@@ -54,3 +54,16 @@ def test_a_bad_page_far_down_a_wide_table():
         assert out.tolist() == [n, 20]
         got = parts(b)
         assert all(np.array_equal(got[x], want[x]) for x in want)
+
+
+@pytest.mark.parametrize("B", [3, 2100])
+def test_new_lengths_in_the_place_of_the_budgets(B):
+    lens = [(13 * i + 30) % 50 for i in range(B)]
+    keep = [(7 * i + 5) % 40 for i in range(B)]
+    a = make(lens, 1, 64, 16, "bf16", seed=4)
+    want, new = expect(a, lens, keep, 2)
+    kp = i32(keep)
+    assert U.cache_evict(keep=kp, recent=2, out=kp, **a) is kp
+    U.check()
+    got = parts(a)
+    assert kp.tolist() == new and all(np.array_equal(got[x], want[x]) for x in want)
