@@ -466,7 +466,8 @@ int ulysses_attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_c
 /* ulysses_attn_decode, which also adds to what each cached token has gathered:
  *   weights[page][h][slot of key j] += sum over the query heads of kv head h of
  *   exp(s_j - LSE), s_j = scale * q . k_j
- *   weights  [num_pages][H_kv][page_size] fp32, 16-byte aligned
+ *   weights  [num_pages][H_kv][page_size] fp32, 16-byte aligned, apart from the
+ *            call's other buffers
  * A slot gets one addition a call; where sequences share a page it gets one of
  * each, in no fixed order.  Keys that the call leaves out, and heads none of whose
  * keys counts, add nothing; a head whose LSE is NaN makes its keys' weights NaN.

@@ -316,6 +316,13 @@ int attn_decode(const void* q, int64_t q_b, int64_t q_h, const void* k_cache, co
     return set_error(ULYSSES_ERR_INVALID, "weights must not overlap q and o");
   a.seen = weights;
   const size_t need = decode_workspace(a);
+  if (weights) {
+    const struct { const void* p; size_t n; } held[] = {{lse, (size_t)B * H_q * 4}, {workspace, need}, {seq_lens, (size_t)B * 4},
+                                                        {page_table, (size_t)B * table_cols * 4}};
+    for (const auto& x : held)
+      if (x.p && x.n && overlap((const char*)weights, wb, (const char*)x.p, x.n))
+        return set_error(ULYSSES_ERR_INVALID, "weights must not overlap the LSE, the workspace, the lengths and the table");
+  }
   if (ws_bytes < need || (need && !workspace))
     return set_error(ULYSSES_ERR_INVALID, "workspace too small: %zu < %zu", ws_bytes, need);
   if (((uintptr_t)workspace & 255u) != 0) return set_error(ULYSSES_ERR_INVALID, "workspace must be 256-byte aligned");

@@ -1,4 +1,4 @@
-"""Host-side refusals of eviction's buffers where they overlap (no GPU: every
+"""Host-side refusals of buffers that overlap, of eviction and weights (no GPU: every
 call is refused before any launch)."""
 import ctypes
 
@@ -60,3 +60,20 @@ def test_new_lengths_inside_the_workspace(L):
     need = L.ulysses_cache_evict_workspace(SEQS, H, COLS, PAGE)
     for at in (0, 4, need - 4):
         refused(L, "the workspace", out=AT["ws"] + at)
+
+
+def test_weights_over_what_a_decode_call_reads_and_writes(L):
+    """Attention that adds its weights up: they lie apart from every other buffer."""
+    B, Hq, cols = 4, 4, 1 << 16
+    q, o, lse = 20 << 36, 21 << 36, 22 << 36
+    need = L.ulysses_attn_decode_weights_workspace(B, Hq, H, D, cols, PAGE, U.BF16, U.E2M1)
+    sizes = {"lse": (lse, B * Hq * 4), "ws": (AT["ws"], need), "lens": (AT["lens"], B * 4), "table": (AT["table"], B * cols * 4),
+             "kc": (AT["kc"], BYTES["kc"]), "vs": (AT["vs"], BYTES["vs"]), "q": (q, B * Hq * D * 2), "o": (o, B * Hq * D * 2)}
+    launches = L.ulysses_launch_count()
+    for name, (at, n) in sizes.items():
+        for w in (at, (at + n - 1) // 16 * 16, at - BYTES["w"] + 16):
+            rc = L.ulysses_attn_decode_weights(P(q), Hq * D, D, P(AT["kc"]), P(AT["vc"]), P(AT["ks"]), P(AT["vs"]), P(AT["table"]),
+                                               cols, P(AT["lens"]), P(o), Hq * D, D, P(lse), P(w), B, Hq, H, D, PAGES, PAGE,
+                                               0.0, U.BF16, U.E2M1, P(AT["ws"]), need, None)
+            assert rc == U.ERR_INVALID and "weights" in L.ulysses_last_error().decode(), name
+    assert L.ulysses_launch_count() == launches
