@@ -948,7 +948,7 @@ def cache_evict(k_cache, v_cache, weights, page_table, seq_lens, keep, recent=0,
     tab, cols = _batch_table(page_table, B, "seq_lens")
     if keep.numel() != B:
         raise ValueError("keep must have B entries")
-    recent = min(recent, (1 << 31) - 1)                    # as many as there are
+    recent = max(min(recent, (1 << 31) - 1), -1)           # as many as there are; any number below 0 is refused
     if out is None:
         out = _empty(seq_lens, (B,), _I32, stream)
     elif out.numel() != B:

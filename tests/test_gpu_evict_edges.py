@@ -67,3 +67,15 @@ def test_new_lengths_in_the_place_of_the_budgets(B):
     U.check()
     got = parts(a)
     assert kp.tolist() == new and all(np.array_equal(got[x], want[x]) for x in want)
+
+
+@pytest.mark.parametrize("recent", [-1, -(1 << 31), -(1 << 32), 5 - (1 << 32), -(1 << 63), -(1 << 70)])
+def test_recent_below_zero_is_refused_whatever_its_size(recent):
+    """Python's numbers have no end: cut to 32 bits some of these would be 0 or more."""
+    a = make([100], 1, 64, 16, "bf16", seed=5)
+    before, launches = parts(a), U.launch_count()
+    with pytest.raises(U.UlyssesError, match="recent"):
+        U.cache_evict(keep=i32([30]), recent=recent, **a)
+    assert U.launch_count() == launches
+    got = parts(a)
+    assert all(np.array_equal(got[x], before[x]) for x in before)
