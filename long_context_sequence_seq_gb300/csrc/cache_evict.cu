@@ -36,7 +36,9 @@
 // flag, which waits for the stores before it, 139 us; one chunk ahead in shared
 // memory 118, of which 25 were waits for neighbours that read no earlier than they
 // wrote; as it is, two to five chunks ahead, the flags are there when they are
-// asked for.
+// asked for.  What the ring takes of shared memory, so that two CTAs fit an SM, and
+// with it the sequences of a launch, is worked out in evict_ring.h.
+#include "evict_ring.h"
 #include "internal.h"
 #include "rows.cuh"
 #include "tc_ptx.cuh"
@@ -48,11 +50,10 @@ ULYSSES_ERROR_READER(read_error_cache_evict)
 namespace {
 
 using namespace rows;
+using namespace evict;
 
 constexpr int kUnit = 16;          // positions of one thread at a time
 constexpr int kThreads = 512;      // of a selecting CTA
-constexpr int kMoveThreads = 256;  // that move rows, of a CTA
-constexpr int kMaxBatch = 2048;    // sequences of one launch (their prefix sums sit in shared memory)
 constexpr int kBins = 4096;        // counts of a digit: 1024 of 10 bits by four neighbours, 2048 of 11 by two
 constexpr int kMaxCtas = 8;        // of a cluster
 
@@ -64,9 +65,8 @@ struct Lists {
   int* before;     // [B][H][chunks] how many of those lie before position chunk * c
   int* read;       // [B][H][chunks] 1: the chunk's rows have been read
   int64_t positions, chunks;
-  int chunk;       // rows moved together: 16 KB of K and of V, at most 128
+  int chunk;       // rows moved together
 };
-constexpr int chunk_of(int row_bytes) { return row_bytes >= 128 ? 16384 / row_bytes : 128; }
 
 // A weight as a number whose order is the weights'.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -410,26 +410,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   }
 }
 
-// Where a chunk's rows are and where they go; -1: a row that does not move.
-template <int kChunk>
-struct Places {
-  int64_t from[kChunk], to[kChunk];
-  int* flags;                                              // the item's; NULL: there is no chunk
-  int c, first, last;                                      // the chunk, and those that have rows in its places
-};
-
-// Of a thread, in a chunk: words of K's and V's rows; weights and row scales; block scales.
-constexpr int own_words(int row_bytes) { return 2 * chunk_of(row_bytes) * (row_bytes / 16) / kMoveThreads; }
-constexpr int own_scalars(int row_bytes, bool scales) { return ((scales ? 3 : 1) * chunk_of(row_bytes) + kMoveThreads - 1) / kMoveThreads; }
-constexpr int own_blocks(int row_bytes, bool four) { return four ? 2 * chunk_of(row_bytes) / kMoveThreads : 0; }
-constexpr int stage_bytes(int row_bytes, bool four, bool scales) {
-  return (own_words(row_bytes) * 16 + own_scalars(row_bytes, scales) * 4 + own_blocks(row_bytes, four) * 8) * kMoveThreads;
-}
-// Chunks on their way through shared memory, two CTAs an SM.
-constexpr int stages_of(int row_bytes, bool four, bool scales) {
-  const int n = 102400 / stage_bytes(row_bytes, four, scales);
-  return n < 6 ? n : 6;
-}
 constexpr int kMovers = kMoveThreads + 96;
 
 // A slot of a ring and the phase of its barriers.
@@ -448,15 +428,17 @@ struct Turn {
 // chunks whose rows lie in this one's places: each on its own, so that no chunk's
 // reading waits for another chunk.  kRowB: bytes of a row's values or codes.
 template <int kRowB, bool kFour, bool kScales>
-__global__ void __launch_bounds__(kMovers, 2) evict_move_kernel(const __grid_constant__ EvictArgs a,
+__global__ void __launch_bounds__(kMovers, kCtasAnSm) evict_move_kernel(const __grid_constant__ EvictArgs a,
                                                                 const __grid_constant__ Lists l) {
   constexpr int kChunk = chunk_of(kRowB);
   constexpr int kW = kRowB / 16;                           // words of a row
   constexpr int kOwn = own_words(kRowB), kScalars = own_scalars(kRowB, kScales), kBlocks = own_blocks(kRowB, kFour);
   constexpr int kStages = stages_of(kRowB, kFour, kScales), kStageB = stage_bytes(kRowB, kFour, kScales);
-  constexpr int kRing = kStages + 2;                       // chunks whose places are known
+  constexpr int kRing = ring_of(kStages);                  // chunks whose places are known
   constexpr int D = kRowB * 2;                             // kFour
   static_assert(kOwn >= 1 && kStages >= 2 && (kChunk & (kChunk - 1)) == 0 && kChunk % kUnit == 0, "");
+  static_assert(cta_bytes(kRowB, kFour, kScales, kStages, batch_of(kRowB, kFour, kScales)) * kCtasAnSm <= kSmBytes,
+                "two CTAs an SM, as the launch takes for granted");
   using Place = Places<kChunk>;
   extern __shared__ __align__(16) char stages[];           // kStages, for the rows on their way
   int2* const size = reinterpret_cast<int2*>(stages + kStages * kStageB);   // [B], and chunks of the sequences before, of one head
@@ -735,18 +717,17 @@ int launch_failed(const char* what, cudaError_t err) {
 
 template <int kRowB, bool kFour, bool kScales>
 cudaError_t move(const EvictArgs& a, const Lists& l, cudaStream_t st) {
-  constexpr int kStages = stages_of(kRowB, kFour, kScales) * stage_bytes(kRowB, kFour, kScales);
+  constexpr int kStages = stages_of(kRowB, kFour, kScales) * stage_bytes(kRowB, kFour, kScales), kBatch = batch_of(kRowB, kFour, kScales);
   static PerDeviceOnce<> once;
-  if (opt_in_smem(once, (const void*)evict_move_kernel<kRowB, kFour, kScales>,
-                  kStages + kMaxBatch * (int)(sizeof(int2) + sizeof(int)) + 4, "cache_evict"))
+  if (opt_in_smem(once, (const void*)evict_move_kernel<kRowB, kFour, kScales>, kStages + batch_bytes(kBatch), "cache_evict"))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sms * 2));
+  cfg.gridDim = dim3((unsigned)(sms * kCtasAnSm));
   cfg.blockDim = dim3(kMovers);
-  cfg.dynamicSmemBytes = kStages + a.B * sizeof(int2) + (a.B + 1) * sizeof(int);
+  cfg.dynamicSmemBytes = kStages + batch_bytes(a.B);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -776,9 +757,12 @@ int launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int row_bytes = a.cache_dtype == ULYSSES_E2M1 ? a.D / 2 : (a.cache_dtype == ULYSSES_E4M3 ? a.D : elt_size(a.cache_dtype) * a.D);
   const Lists l{(int2*)(ws + w.size), (int*)(ws + w.ticket), (int64_t*)(ws + w.src), (int*)(ws + w.before), (int*)(ws + w.read),
                 w.positions, w.chunks, chunk_of(row_bytes)};
-  for (int b0 = 0; b0 < a.B; b0 += kMaxBatch) {
+  const bool four = a.cache_dtype == ULYSSES_E2M1;
+  const int most = batch_of(row_bytes, four, four || a.cache_dtype == ULYSSES_E4M3), launches = (a.B + most - 1) / most;
+  const int batch = (a.B + launches - 1) / launches;
+  for (int b0 = 0; b0 < a.B; b0 += batch) {
     EvictArgs x = a;
-    x.B = a.B - b0 < kMaxBatch ? a.B - b0 : kMaxBatch;
+    x.B = a.B - b0 < batch ? a.B - b0 : batch;
     x.table = a.table + (int64_t)b0 * a.cols;
     x.lens = a.lens + b0;
     x.keep = a.keep + b0;
