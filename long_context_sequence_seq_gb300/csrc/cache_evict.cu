@@ -38,6 +38,8 @@
 // wrote; as it is, two to five chunks ahead, the flags are there when they are
 // asked for.  What the ring takes of shared memory, so that two CTAs fit an SM, and
 // with it the sequences of a launch, is worked out in evict_ring.h.
+#include <atomic>
+
 #include "evict_ring.h"
 #include "internal.h"
 #include "rows.cuh"
@@ -700,14 +702,48 @@ WsLayout ws_layout(const EvictArgs& a) {
   return w;
 }
 
+// Clusters of 2^lg selecting CTAs that the current device holds at once (with all
+// their slots), asked for once a device.  A GPC's SMs are no multiple of a cluster's:
+// with two CTAs an SM 36 clusters of eight, where 304 CTAs would be 38.
+int clusters_at_once(int lg) {
+  static std::atomic<int> known[64][4];                    // 0: not yet asked
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((n = known[dev][lg].load(std::memory_order_relaxed)) != 0) return n;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1u << lg);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSlots * kSlotB;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1u << lg;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  if (n > 0) known[dev][lg].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // CTAs of a cluster for each (sequence, kv head): a unit a thread where two CTAs an
 // SM allow it.  (Four and eight an SM: 64 ragged sequences of up to 16384 positions,
 // 8 heads, 246 and 265 us where this takes 238, 16 of 40000 207 and 207 where it
 // takes 181; a CTA for each head: 1 x 131072 positions 126 where it takes 35.)
-int cluster_of(const EvictArgs& a) {
-  int c = 1;
-  while (c < kMaxCtas && (int64_t)a.cols * a.page > (int64_t)c * kThreads * kUnit && (int64_t)a.B * a.H * c * 2 <= 152 * 2) c *= 2;
-  return c;
+// Where the wider clusters would not all run at once, the last of them adding a
+// selection's time, the narrower are taken if their CTAs hold the positions from
+// digit to digit (38 heads of 40000 in fours 36 us, in eights 45; 76 of 20000 in
+// pairs 33, in fours 43), else the wider (38 of 131072 in eights 57, in fours 82).
+int cluster_of(const EvictArgs& a, int sms) {
+  const int64_t positions = (int64_t)a.cols * a.page, items = (int64_t)a.B * a.H;
+  int lg = 0;
+  while (lg < 3 && positions > (int64_t)kThreads * kUnit << lg &&
+         (items <= clusters_at_once(lg + 1) ||
+          (items << (lg + 1) <= 2 * sms && positions > (int64_t)kSlots * kThreads * kUnit << lg)))
+    ++lg;
+  return 1 << lg;
 }
 
 int launch_failed(const char* what, cudaError_t err) {
@@ -716,14 +752,11 @@ int launch_failed(const char* what, cudaError_t err) {
 }
 
 template <int kRowB, bool kFour, bool kScales>
-cudaError_t move(const EvictArgs& a, const Lists& l, cudaStream_t st) {
+cudaError_t move(const EvictArgs& a, const Lists& l, int sms, cudaStream_t st) {
   constexpr int kStages = stages_of(kRowB, kFour, kScales) * stage_bytes(kRowB, kFour, kScales), kBatch = batch_of(kRowB, kFour, kScales);
   static PerDeviceOnce<> once;
   if (opt_in_smem(once, (const void*)evict_move_kernel<kRowB, kFour, kScales>, kStages + batch_bytes(kBatch), "cache_evict"))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(sms * kCtasAnSm));
   cfg.blockDim = dim3(kMovers);
@@ -737,13 +770,13 @@ cudaError_t move(const EvictArgs& a, const Lists& l, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, evict_move_kernel<kRowB, kFour, kScales>, a, l);
 }
 
-cudaError_t move_rows(const EvictArgs& a, const Lists& l, cudaStream_t st) {
+cudaError_t move_rows(const EvictArgs& a, const Lists& l, int sms, cudaStream_t st) {
   const bool wide = a.D == 128;
   switch (a.cache_dtype) {
-    case ULYSSES_E2M1: return wide ? move<64, true, true>(a, l, st) : move<32, true, true>(a, l, st);
-    case ULYSSES_E4M3: return wide ? move<128, false, true>(a, l, st) : move<64, false, true>(a, l, st);
-    case ULYSSES_BF16: return wide ? move<256, false, false>(a, l, st) : move<128, false, false>(a, l, st);
-    default: return wide ? move<512, false, false>(a, l, st) : move<256, false, false>(a, l, st);
+    case ULYSSES_E2M1: return wide ? move<64, true, true>(a, l, sms, st) : move<32, true, true>(a, l, sms, st);
+    case ULYSSES_E4M3: return wide ? move<128, false, true>(a, l, sms, st) : move<64, false, true>(a, l, sms, st);
+    case ULYSSES_BF16: return wide ? move<256, false, false>(a, l, sms, st) : move<128, false, false>(a, l, sms, st);
+    default: return wide ? move<512, false, false>(a, l, sms, st) : move<256, false, false>(a, l, sms, st);
   }
 }
 
@@ -760,6 +793,9 @@ int launch_evict(const EvictArgs& a, cudaStream_t st) {
   const bool four = a.cache_dtype == ULYSSES_E2M1;
   const int most = batch_of(row_bytes, four, four || a.cache_dtype == ULYSSES_E4M3), launches = (a.B + most - 1) / most;
   const int batch = (a.B + launches - 1) / launches;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   for (int b0 = 0; b0 < a.B; b0 += batch) {
     EvictArgs x = a;
     x.B = a.B - b0 < batch ? a.B - b0 : batch;
@@ -767,9 +803,9 @@ int launch_evict(const EvictArgs& a, cudaStream_t st) {
     x.lens = a.lens + b0;
     x.keep = a.keep + b0;
     x.out = a.out + b0;
-    const int c = cluster_of(x);
     static PerDeviceOnce<> once;
     if (const int rc = opt_in_smem(once, (const void*)evict_select_kernel, kSlots * kSlotB, "cache_evict")) return rc;
+    const int c = cluster_of(x, sms);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)x.B * x.H * c));
     cfg.blockDim = dim3(kThreads);
@@ -786,7 +822,7 @@ int launch_evict(const EvictArgs& a, cudaStream_t st) {
     cudaError_t err = cudaLaunchKernelEx(&cfg, evict_select_kernel, x, l, c);
     if (err != cudaSuccess) return launch_failed("cache_evict", err);
     count_launch();
-    err = move_rows(x, l, st);
+    err = move_rows(x, l, sms, st);
     if (err != cudaSuccess) return launch_failed("cache_evict move", err);
     count_launch();
   }

@@ -1,5 +1,6 @@
 """Eviction that moves so many rows that each CTA's ring in shared memory goes
-round several times, for every kind of row.  Rows are moved, not computed, so everything is compared whole.
+round several times, for every kind of row, and selections whose clusters do not
+all run at once.  Rows are moved, not computed, so everything is compared whole.
 
 The definition is the oracle's, ordered by sorts of whole arrays (held to the
 oracle's own on small ones)."""
@@ -85,3 +86,12 @@ def test_every_ring_goes_round(held, D, kind):
         a["weights"].copy_(torch.from_numpy(w))
     moved = run(a, lens, [keep] * B, 100)
     assert moved >= 0.9 * keep * B * H or kind == "any"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,n", [(37, 1, 20000), (19, 2, 40000), (19, 2, 70000), (18, 4, 9000), (25, 3, 20000), (19, 4, 20000),
+                                   (19, 4, 34000)])
+def test_selections_that_do_not_all_run_at_once(B, H, n):
+    """As many heads as there are clusters at once, and one or two more."""
+    lens = [n - 17 * b for b in range(B)]
+    run(make(lens, H, 64, 64, "e2m1", seed=B), lens, [900 + b for b in range(B)], 64)
