@@ -1,6 +1,6 @@
 // C ABI of the rotary positions, the paged cache, eviction from it and single-token attention:
-// argument validation and dispatch (the kernels are in rope.cu, kv_cache.cu
-// and attn_decode.cu).
+// argument validation and dispatch (the kernels are in rope.cu, kv_cache.cu, cache_evict.cu
+// and attn_decode*.cu).
 #include <cmath>
 
 #include "common.cuh"

@@ -35,9 +35,15 @@
 // loads, waits and stores one after the other); with a fence before each chunk's
 // flag, which waits for the stores before it, 139 us; one chunk ahead in shared
 // memory 118, of which 25 were waits for neighbours that read no earlier than they
-// wrote; as it is, two to five chunks ahead, the flags are there when they are
-// asked for.  What the ring takes of shared memory, so that two CTAs fit an SM, and
-// with it the sequences of a launch, is worked out in evict_ring.h.
+// wrote; as it is, two chunks ahead, the flags are there when they are asked for.
+// How far ahead goes by what a kind of row takes: one chunk (e4m3 rows of 128) to
+// five (4 bits of D = 64).  48 sequences cut from 4160 to 4096 tokens of 8 heads, the
+// move alone: bf16 264 us (1.62 GB, 91% of the copy rate), 24 in fp32 of D = 64 135 (89%),
+// e4m3 148 (0.84 GB, 84%; in chunks of half the rows, four of them ahead, 30 us more), 4 bits
+// 105 (0.49 GB, 69%), e4m3 of D = 64 103 (63%) and 4 bits of it 94 (0.26 GB, 41%: as
+// many rows, scales and places to look up for a third of the bytes).
+// What the ring takes of shared memory, so that two CTAs fit an SM, and with it the
+// sequences of a launch, is worked out in evict_ring.h.
 #include <atomic>
 
 #include "evict_ring.h"

@@ -932,7 +932,7 @@ def cache_evict(k_cache, v_cache, weights, page_table, seq_lens, keep, recent=0,
     order to positions 0, 1, ..., in place, with their scales and weights; the
     places behind are left as they were, and pages that hold none of them are
     the caller's again.  The sequences of a call must not share pages.  Returns
-    the new lengths int32 [B] (out: into this tensor, which may be seq_lens).
+    the new lengths int32 [B] (out: into this tensor, which may be seq_lens or keep).
     workspace: cache_evict_workspace(), for calls that do not overlap on the
     GPU; made per call if not given.  A sequence with a bad length or page is
     left as it is, and raises in check()."""
@@ -1030,6 +1030,7 @@ def attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scale=None, v_scale
     ws, n = (None, 0) if workspace is None else (_flat(workspace, _U8, "workspace"), workspace.numel())
     args = (q.data_ptr(), qb, qh, pk, pv, pks, pvs, tab, cols, _flat(seq_lens, _I32, "seq_lens"), out.data_ptr(), ob, oh, pl)
     sizes = (B, H_q, H_kv, D, n_pages, page, scale or 0.0, dq, dc, ws, n)
+    # again, for a given stream: with what was made here since their devices were looked at
     tensors = (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, workspace, out, lse, weights)
     if weights is None:
         _launch(lib().ulysses_attn_decode, idx, stream, tensors, (*args, *sizes))
